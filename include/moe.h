@@ -325,6 +325,139 @@ moe_status_t moe_route_bwd(const moe_shape_t *shape, const void *x, const void *
                            float *dw_sg, float *dx_router, void *ws,
                            moe_stream_t stream);
 
+/* moe_route_bwd with the gradient of a loss on the logits: dl gains
+ * dlogits_add [T,E] fp32 (for instance from moe_balance_loss_bwd) before dW_r,
+ * db_r and dx_router are formed from it. Other arguments and errors as
+ * moe_route_bwd; dlogits_add must not be NULL.                               */
+moe_status_t moe_route_bwd_add(const moe_shape_t *shape, const void *x, const void *W_r,
+                               const void *w_sg, const float *logits,
+                               const int32_t *topk_idx, const float *topk_prob,
+                               const float *topk_w, const float *dw, const float *dz,
+                               const float *dlogits_add, const float *dx_in, float *dW_r,
+                               float *db_r, float *dw_sg, float *dx_router, void *ws,
+                               moe_stream_t stream);
+
+/* ---- around the layer ---------------------------------------------------
+ * What a transformer block runs next to its MoE layer; the paper's pages do
+ * not describe these. Conventions as above. rows, d: a dense [rows, d]
+ * matrix; d a multiple of 8 (MOE_BF16) or 4 (MOE_F32).                       */
+
+/* RMS norm with the residual's addition.
+ *   h = dtype(x + residual), or x when residual is NULL;
+ *   rstd = 1 / sqrt(mean_j h_j^2 + eps);  y = dtype(h rstd gamma);
+ *   q = e4m3(y / s), from y before its rounding, with one fp32 scale s per
+ *   row and group of `group` consecutive columns (the last group of a row may
+ *   be shorter): s = max|y| / 448 over the group, at least 2^-110 / 448, and 1
+ *   for a group of zeros; y stands for q * s. The layout moe_permute_e4m3 reads.
+ * x, residual [rows, d] dtype; gamma [d] dtype; eps > 0.
+ *   out: h [rows, d] dtype (NULL: not stored; the backward needs it, and
+ *   without a residual it is x); y [rows, d] dtype or NULL; q [rows, d] e4m3
+ *   bytes or NULL; q_scale [rows, ceil(d / group)] fp32 (NULL iff q is NULL);
+ *   rstd [rows] fp32 or NULL. At least one of h, y, q is set.
+ *   group: 32, 64, 128, or 0 for one scale per row.
+ * h and y may each be x or residual itself (in place); no other overlap of an
+ * output with an input or with another output. rows = 0 does nothing.
+ * Statistics are fp32: |h| above 1e18 overflows them (y = 0 in that row); a
+ * NaN or infinity in a row spoils that row only.
+ * Errors: MOE_ERR_INVALID_ARG as above; MOE_ERR_UNSUPPORTED for another group,
+ *   d above 32768 (bf16) or 16384 (fp32), or rows >= 2^31.                   */
+moe_status_t moe_rmsnorm(int32_t dtype, int64_t rows, int32_t d, const void *x,
+                         const void *residual, const void *gamma, float eps, void *h, void *y,
+                         void *q, float *q_scale, int32_t group, float *rstd,
+                         moe_stream_t stream);
+
+/* Backward of moe_rmsnorm. With xhat = h rstd and g = dy gamma:
+ *   dx = rstd (g - xhat mean_j(g_j xhat_j)) + dh  (the gradient of x and of
+ *   residual alike);  dgamma = sum over rows of dy xhat  (overwritten).
+ * The e4m3 output has no gradient of its own: what reads it passes dy on as if
+ * it had read y.
+ *   dy [rows, d] dy_dtype; h [rows, d], gamma [d] dtype; rstd [rows] as
+ *   moe_rmsnorm wrote it; dh [rows, d] dtype: the gradient that reaches h
+ *   from elsewhere (the residual stream), or NULL; dx [rows, d] dx_dtype;
+ *   dgamma [d] fp32. dtype MOE_F32 takes fp32 dy and dx only; MOE_BF16 either.
+ *   dx may be dy or dh itself when the types agree; no other overlap.
+ *   ws: moe_rmsnorm_bwd_workspace_size(rows, d) bytes, 16-byte aligned, no
+ *   contents expected (0 for an invalid size). rows = 0: dgamma = 0.
+ * Errors: as moe_rmsnorm; MOE_ERR_INVALID_ARG when ws_bytes is too small.     */
+size_t moe_rmsnorm_bwd_workspace_size(int64_t rows, int32_t d);
+moe_status_t moe_rmsnorm_bwd(int32_t dtype, int32_t dy_dtype, int32_t dx_dtype, int64_t rows,
+                             int32_t d, const void *dy, const void *h, const void *gamma,
+                             const float *rstd, const void *dh, void *dx, float *dgamma,
+                             void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Balance loss of the router and the per-expert counts it is made of. For
+ * every sub-sequence j (blocks of S = shape->subseq_len tokens, 0 = all T;
+ * whatever shape->drop says) with n_j unmasked tokens, n = sum_j n_j:
+ *   counts[j,e] = unmasked (t,k) with topk_idx = e, dropped or not;
+ *   prob_mean[j,e] = mean over the unmasked tokens of softmax(logits)[t,e];
+ *   loss = alpha sum_j (n_j / n) sum_e (E counts[j,e] / (K n_j)) prob_mean[j,e]
+ * (alpha for an even load; a sub-sequence without unmasked tokens counts
+ * nowhere, and without any the loss is 0).
+ *   logits [T,E] fp32; topk_idx [T,K] int32; mask [T] uint8, 0 = padding (its
+ *   logits and indices are not read into any result), or NULL: no padding. An
+ *   expert whose logit is -inf has p = 0, a token whose logits all are, too.
+ *   out: loss [1] fp32; counts [n_sub,E] int32; prob_mean [n_sub,E] fp32 or
+ *   NULL; coef [n_sub * E + 1] fp32: kept for the backward. n_sub = ceil(T/S).
+ *   ws: workspace of moe_workspace_size(shape) bytes. shape: T, E, K,
+ *   subseq_len are used, all fields are checked.
+ * Errors: an unmasked topk_idx outside [0, E) is not counted and records
+ *   MOE_ERR_DEVICE in the status word.                                       */
+moe_status_t moe_balance_loss(const moe_shape_t *shape, const float *logits,
+                              const int32_t *topk_idx, const uint8_t *mask, float alpha,
+                              float *loss, int32_t *counts, float *prob_mean, float *coef,
+                              void *ws, moe_stream_t stream);
+
+/* dlogits[t,e] = dloss * d loss / d logits[t,e] (the counts are constants; 0
+ * for padding), for moe_route_bwd_add. logits, mask, coef as in
+ * moe_balance_loss; dloss [1] fp32 on the device, or NULL for 1; dlogits [T,E]
+ * fp32, which may be logits itself.                                          */
+moe_status_t moe_balance_loss_bwd(const moe_shape_t *shape, const float *logits,
+                                  const uint8_t *mask, const float *coef, const float *dloss,
+                                  float *dlogits, moe_stream_t stream);
+
+/* moe_permute of rows held in e4m3 with scales, as moe_rmsnorm writes them:
+ *   Xp[row_of[t,k]] = dtype(q[t] * scale of its group), dtype = shape->dtype.
+ *   q [T,d] e4m3 bytes; q_scale [T, ceil(d / group)] fp32 (group 32, 64, 128,
+ *   or 0: one per row). Other arguments and the map as moe_permute; Xp is
+ *   required. Errors: as moe_permute; MOE_ERR_UNSUPPORTED for another group. */
+moe_status_t moe_permute_e4m3(const moe_shape_t *shape, const void *q, const float *q_scale,
+                              int32_t group, const int32_t *topk_idx, const uint8_t *keep,
+                              void *Xp, int32_t *row_of, int32_t *src_of, int32_t *counts,
+                              int32_t *offsets, void *ws, moe_stream_t stream);
+
+/* One tensor of a list: numel >= 0 contiguous elements at `data` (a device
+ * pointer, aligned to its element; NULL allowed when numel is 0).           */
+typedef struct {
+  void *data;
+  int64_t numel;
+  int32_t dtype; /* MOE_F32 or MOE_BF16, per tensor */
+} moe_tensor_t;
+
+/* Workspace bytes of moe_grad_norm (16-byte aligned, no contents expected). */
+#define MOE_GRAD_NORM_WORKSPACE_BYTES 9728u
+
+/* Global norm of n gradient tensors (n >= 0): norm[0] = sqrt(sum of all
+ * squares), fp32, right wherever that is an fp32 number (squares outside the
+ * fp32 range are added in fp64); NaN or infinity among the gradients gives a
+ * norm that is not finite; an empty list gives 0. `grads` is a HOST array and
+ * is read before the call returns. A tensor may be listed once only if it is
+ * to count once.                                                            */
+moe_status_t moe_grad_norm(int32_t n, const moe_tensor_t *grads, float *norm, void *ws,
+                           size_t ws_bytes, moe_stream_t stream);
+
+/* Clipping by a norm on the device (moe_grad_norm's, or one that a caller
+ * joined over ranks): out = grads * coef, rounded once, with coef = max_norm /
+ * norm if max_norm < norm < inf, else 1 -- a norm that is not finite leaves
+ * the gradients as they are, so that the step can be skipped by the norm.
+ *   max_norm >= 0 (finite); out: NULL for in place, or n tensors of the same
+ *   sizes and types, each of which is its gradient itself or does not overlap
+ *   any gradient; coef [1] fp32 or NULL receives coef. In place with coef = 1
+ *   nothing is read or written. Both arrays are HOST arrays.
+ *   norm and coef are not among the tensors.                                 */
+moe_status_t moe_grad_clip(int32_t n, const moe_tensor_t *grads, const moe_tensor_t *out,
+                           const float *norm, float max_norm, float *coef,
+                           moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,6 +18,7 @@ LIB_PATH = os.environ.get("MOE_LIBRARY") or os.path.join(PKG, "libmoe.so")
 
 MOE_F32, MOE_BF16 = 0, 1
 MOE_FFN_BWD_WORKSPACE_BYTES = 33280   # include/moe.h
+MOE_GRAD_NORM_WORKSPACE_BYTES = 9728
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_CUDA",
           4: "MOE_ERR_TIMEOUT", 5: "MOE_ERR_DEVICE"}
 
@@ -35,6 +36,30 @@ class MoEShape(ctypes.Structure):
                 ("subseq_len", ctypes.c_int64), ("renorm", ctypes.c_int32), ("Fs", ctypes.c_int32)]
 
 
+class MoETensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class TensorList:
+    """moe_tensor_t[] of contiguous fp32 or bf16 CUDA tensors on one device, kept alive here; build it once and
+    pass it to moe_grad_norm and moe_grad_clip in every step."""
+
+    def __init__(self, tensors):
+        import torch
+        self.tensors = list(tensors)
+        codes = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+        for i, t in enumerate(self.tensors):
+            if t.dtype not in codes:
+                raise ValueError(f"tensor {i}: {t.dtype}, not float32 or bfloat16")
+            if not t.is_contiguous():
+                raise ValueError(f"tensor {i} is not contiguous")
+            if not t.is_cuda or t.device != self.tensors[0].device:
+                raise ValueError(f"tensor {i} is on {t.device}: one CUDA device is wanted")
+        self.n = len(self.tensors)
+        self.array = (MoETensor * max(1, self.n))(
+            *[MoETensor(t.data_ptr(), t.numel(), codes[t.dtype]) for t in self.tensors])
+
+
 def shape_of(cfg) -> MoEShape:
     """moe_shape_t of a synthetic.MoEConfig-like object."""
     return MoEShape(T=cfg.T, d=cfg.d, E=cfg.E, K=cfg.K, F=cfg.F,
@@ -50,7 +75,7 @@ lib = ctypes.CDLL(LIB_PATH)
 
 _P = ctypes.c_void_p
 _S = ctypes.POINTER(MoEShape)
-_I32, _I64 = ctypes.c_int32, ctypes.c_int64
+_I32, _I64, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 _SIGS = {
     "moe_route": [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
@@ -68,6 +93,15 @@ _SIGS = {
     "moe_permute_bwd": [_S, _P, _P, _P, _P, _P],
     "moe_sum_partials": [_I32, _I32, _I64, _I32, _P, _P, _P],
     "moe_route_bwd": [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "moe_route_bwd_add": [_S, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "moe_rmsnorm": [_I32, _I64, _I32, _P, _P, _P, _F, _P, _P, _P, _P, _I32, _P, _P],
+    "moe_rmsnorm_bwd": [_I32, _I32, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P,
+                        ctypes.c_size_t, _P],
+    "moe_balance_loss": [_S, _P, _P, _P, _F, _P, _P, _P, _P, _P, _P],
+    "moe_balance_loss_bwd": [_S, _P, _P, _P, _P, _P, _P],
+    "moe_permute_e4m3": [_S, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "moe_grad_norm": [_I32, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_grad_clip": [_I32, _P, _P, _P, _F, _P, _P],
     "moe_clear_status": [_P, _P],
     "moe_get_status": [_P, _P, ctypes.POINTER(ctypes.c_uint32)],
 }
@@ -79,12 +113,14 @@ lib.moe_workspace_size.argtypes = [_S]
 lib.moe_workspace_size.restype = ctypes.c_size_t
 lib.moe_padded_capacity.argtypes = [_S]
 lib.moe_padded_capacity.restype = ctypes.c_int64
+lib.moe_rmsnorm_bwd_workspace_size.argtypes = [_I64, _I32]
+lib.moe_rmsnorm_bwd_workspace_size.restype = ctypes.c_size_t
 lib.moe_version.restype = ctypes.c_char_p
 lib.moe_status_string.argtypes = [ctypes.c_int]
 lib.moe_status_string.restype = ctypes.c_char_p
 
 EXPORTED = sorted(list(_SIGS) + ["moe_workspace_size", "moe_version", "moe_status_string",
-                                  "moe_padded_capacity"])
+                                  "moe_padded_capacity", "moe_rmsnorm_bwd_workspace_size"])
 
 
 def _ptr(t):
@@ -212,3 +248,65 @@ def moe_route_bwd(shape, x, W_r, w_sg, logits, topk_idx, topk_prob, topk_w, dw, 
     _call("moe_route_bwd", ctypes.byref(shape), _ptr(x), _ptr(W_r), _ptr(w_sg), _ptr(logits),
           _ptr(topk_idx), _ptr(topk_prob), _ptr(topk_w), _ptr(dw), _ptr(dz), _ptr(dx_in),
           _ptr(dW_r), _ptr(db_r), _ptr(dw_sg), _ptr(dx_router), _ptr(ws), _stream(stream))
+
+
+def moe_route_bwd_add(shape, x, W_r, w_sg, logits, topk_idx, topk_prob, topk_w, dw, dz, dlogits_add,
+                      dx_in, dW_r, db_r, dw_sg, dx_router, ws, stream=None):
+    _call("moe_route_bwd_add", ctypes.byref(shape), _ptr(x), _ptr(W_r), _ptr(w_sg), _ptr(logits),
+          _ptr(topk_idx), _ptr(topk_prob), _ptr(topk_w), _ptr(dw), _ptr(dz), _ptr(dlogits_add),
+          _ptr(dx_in), _ptr(dW_r), _ptr(db_r), _ptr(dw_sg), _ptr(dx_router), _ptr(ws),
+          _stream(stream))
+
+
+def moe_rmsnorm(dtype, rows, d, x, residual, gamma, eps, h, y, q, q_scale, group, rstd,
+                stream=None):
+    _call("moe_rmsnorm", dtype, rows, d, _ptr(x), _ptr(residual), _ptr(gamma), eps, _ptr(h),
+          _ptr(y), _ptr(q), _ptr(q_scale), group, _ptr(rstd), _stream(stream))
+
+
+def moe_rmsnorm_bwd_workspace_size(rows: int, d: int) -> int:
+    return int(lib.moe_rmsnorm_bwd_workspace_size(rows, d))
+
+
+def moe_rmsnorm_bwd(dtype, dy_dtype, dx_dtype, rows, d, dy, h, gamma, rstd, dh, dx, dgamma, ws,
+                    stream=None, ws_bytes=None):
+    """ws: a device tensor (its size becomes ws_bytes) or a pointer with ws_bytes."""
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size()
+    _call("moe_rmsnorm_bwd", dtype, dy_dtype, dx_dtype, rows, d, _ptr(dy), _ptr(h), _ptr(gamma),
+          _ptr(rstd), _ptr(dh), _ptr(dx), _ptr(dgamma), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def moe_balance_loss(shape, logits, topk_idx, mask, alpha, loss, counts, prob_mean, coef, ws,
+                     stream=None):
+    _call("moe_balance_loss", ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(mask), alpha,
+          _ptr(loss), _ptr(counts), _ptr(prob_mean), _ptr(coef), _ptr(ws), _stream(stream))
+
+
+def moe_balance_loss_bwd(shape, logits, mask, coef, dloss, dlogits, stream=None):
+    _call("moe_balance_loss_bwd", ctypes.byref(shape), _ptr(logits), _ptr(mask), _ptr(coef),
+          _ptr(dloss), _ptr(dlogits), _stream(stream))
+
+
+def moe_permute_e4m3(shape, q, q_scale, group, topk_idx, keep, Xp, row_of, src_of, counts, offsets,
+                     ws, stream=None):
+    _call("moe_permute_e4m3", ctypes.byref(shape), _ptr(q), _ptr(q_scale), group, _ptr(topk_idx),
+          _ptr(keep), _ptr(Xp), _ptr(row_of), _ptr(src_of), _ptr(counts), _ptr(offsets), _ptr(ws),
+          _stream(stream))
+
+
+def moe_grad_norm(grads, norm, ws, stream=None, ws_bytes=None):
+    """grads: a TensorList. ws: a device tensor (its size becomes ws_bytes) or a pointer with ws_bytes."""
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size()
+    _call("moe_grad_norm", grads.n, ctypes.addressof(grads.array), _ptr(norm), _ptr(ws), ws_bytes,
+          _stream(stream))
+
+
+def moe_grad_clip(grads, out, norm, max_norm, coef, stream=None):
+    """grads: a TensorList; out: a TensorList of the same tensors' sizes and types, or None for in place."""
+    if out is not None and out.n != grads.n:
+        raise MoEError("moe_grad_clip", 1)
+    _call("moe_grad_clip", grads.n, ctypes.addressof(grads.array),
+          None if out is None else ctypes.addressof(out.array), _ptr(norm), max_norm, _ptr(coef),
+          _stream(stream))

@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libmoe.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + INCLUDE, "-I" + CSRC]
-SOURCES = ["api.cu", "route.cu", "route_bwd.cu", "dispatch.cu", "gemm_simt.cu", "gemm_tc.cu"]
+SOURCES = ["api.cu", "route.cu", "route_bwd.cu", "dispatch.cu", "gemm_simt.cu", "gemm_tc.cu",
+           "norm.cu", "balance.cu", "grads.cu"]
 
 
 def nvcc() -> str:

@@ -3,6 +3,7 @@
 // Every call that launches work opens an NVTX range named after itself, so
 // profilers that record NVTX show where each layer step starts and ends
 // (without a profiler attached the range calls return at once).
+#include <cmath>
 #include <cstring>
 
 #include <nvtx3/nvToolsExt.h>
@@ -43,7 +44,7 @@ int64_t subseq(const moe_shape_t *s) {
 }
 
 struct Layout {
-  size_t status, map, cap, capn, rbwd, total;
+  size_t status, map, cap, capn, rbwd, bal, total;
 };
 
 // the tensor-core router's logits path (bf16, d % 64 == 0)
@@ -68,6 +69,8 @@ Layout layout(const moe_shape_t *s) {
   }
   L.rbwd = off;
   off += align256(route_bwd_workspace_bytes(s->T, s->d, s->E));
+  L.bal = off;
+  off += align256(balance_workspace_bytes(s->T, subseq(s), s->E));
   L.total = off > MOE_FFN_BWD_WORKSPACE_BYTES ? off : MOE_FFN_BWD_WORKSPACE_BYTES;
   return L;
 }
@@ -383,12 +386,12 @@ moe_status_t moe_sum_partials(int32_t dtype, int32_t n_parts, int64_t rows, int3
                                          (cudaStream_t)stream));
 }
 
-moe_status_t moe_route_bwd(const moe_shape_t *shape, const void *x, const void *W_r,
-                           const void *w_sg, const float *logits, const int32_t *topk_idx,
-                           const float *topk_prob, const float *topk_w, const float *dw,
-                           const float *dz, const float *dx_in, float *dW_r, float *db_r,
-                           float *dw_sg, float *dx_router, void *ws, moe_stream_t stream) {
-  NvtxRange trace("moe_route_bwd");
+static moe_status_t route_bwd(const moe_shape_t *shape, const void *x, const void *W_r,
+                              const void *w_sg, const float *logits, const int32_t *topk_idx,
+                              const float *topk_prob, const float *topk_w, const float *dw,
+                              const float *dz, const float *dl_add, const float *dx_in,
+                              float *dW_r, float *db_r, float *dw_sg, float *dx_router, void *ws,
+                              moe_stream_t stream) {
   if (!shape_ok(shape)) return MOE_ERR_INVALID_ARG;
   if (!x || !W_r || !logits || !topk_idx || !topk_prob || !topk_w || !dw || !dW_r || !dx_router || !ws)
     return MOE_ERR_INVALID_ARG;
@@ -403,10 +406,238 @@ moe_status_t moe_route_bwd(const moe_shape_t *shape, const void *x, const void *
   a.renorm = shape->renorm; a.x = x; a.W_r = W_r; a.w_sg = w_sg; a.logits = logits;
   a.topk_idx = topk_idx; a.topk_prob = topk_prob; a.topk_w = topk_w; a.dw = dw; a.dz = dz;
   a.dx_in = dx_in; a.dW_r = dW_r; a.db_r = db_r; a.dw_sg = dw_sg; a.dx_router = dx_router;
+  a.dl_add = dl_add;
   a.dl = reinterpret_cast<float *>(static_cast<char *>(ws) + L.rbwd);
   a.partial = a.dl + align256((size_t)shape->T * shape->E * sizeof(float)) / sizeof(float);
   a.status = status_word(ws);
   return cuda_status(launch_route_bwd(a, (cudaStream_t)stream));
+}
+
+moe_status_t moe_route_bwd(const moe_shape_t *shape, const void *x, const void *W_r,
+                           const void *w_sg, const float *logits, const int32_t *topk_idx,
+                           const float *topk_prob, const float *topk_w, const float *dw,
+                           const float *dz, const float *dx_in, float *dW_r, float *db_r,
+                           float *dw_sg, float *dx_router, void *ws, moe_stream_t stream) {
+  NvtxRange trace("moe_route_bwd");
+  return route_bwd(shape, x, W_r, w_sg, logits, topk_idx, topk_prob, topk_w, dw, dz, nullptr, dx_in,
+                   dW_r, db_r, dw_sg, dx_router, ws, stream);
+}
+
+moe_status_t moe_route_bwd_add(const moe_shape_t *shape, const void *x, const void *W_r,
+                               const void *w_sg, const float *logits, const int32_t *topk_idx,
+                               const float *topk_prob, const float *topk_w, const float *dw,
+                               const float *dz, const float *dlogits_add, const float *dx_in,
+                               float *dW_r, float *db_r, float *dw_sg, float *dx_router, void *ws,
+                               moe_stream_t stream) {
+  NvtxRange trace("moe_route_bwd_add");
+  if (!dlogits_add || !aligned4(dlogits_add)) return MOE_ERR_INVALID_ARG;
+  return route_bwd(shape, x, W_r, w_sg, logits, topk_idx, topk_prob, topk_w, dw, dz, dlogits_add,
+                   dx_in, dW_r, db_r, dw_sg, dx_router, ws, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Around the layer
+
+static bool overlap(const void *p, size_t np, const void *q, size_t nq) {
+  if (p == nullptr || q == nullptr) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + nq && b < a + np;
+}
+
+static bool dtype_ok(int32_t dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
+static size_t size_of(int32_t dtype) { return dtype == MOE_BF16 ? 2 : 4; }
+static bool group_ok(int32_t group) { return group == 0 || group == 32 || group == 64 || group == 128; }
+
+// MOE_OK for a [rows, d] matrix that the norm's kernels take
+static moe_status_t norm_check(int32_t dtype, int64_t rows, int32_t d) {
+  if (!dtype_ok(dtype) || rows < 0 || d < 1 || d % (dtype == MOE_BF16 ? 8 : 4) != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (rows >= (int64_t(1) << 31) || d > (dtype == MOE_BF16 ? 32768 : 16384)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t moe_rmsnorm(int32_t dtype, int64_t rows, int32_t d, const void *x, const void *residual,
+                         const void *gamma, float eps, void *h, void *y, void *q, float *q_scale,
+                         int32_t group, float *rstd, moe_stream_t stream) {
+  NvtxRange trace("moe_rmsnorm");
+  moe_status_t st = norm_check(dtype, rows, d);
+  if (st != MOE_OK) return st;
+  if (!(eps > 0.0f) || !std::isfinite(eps) || (q == nullptr) != (q_scale == nullptr) || group < 0)
+    return MOE_ERR_INVALID_ARG;
+  if (!group_ok(group)) return MOE_ERR_UNSUPPORTED;
+  if (!h && !y && !q) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!x || !gamma) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || (residual && !aligned16(residual)) || !aligned16(gamma) || (h && !aligned16(h)) ||
+      (y && !aligned16(y)) || (q && !aligned16(q)) || (q_scale && !aligned4(q_scale)) ||
+      (rstd && !aligned4(rstd)))
+    return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)rows * d, bytes = n * size_of(dtype);
+  const int ng = group > 0 ? (d + group - 1) / group : 1;
+  struct Range { const void *p; size_t n; };
+  const Range outs[] = {{h, bytes}, {y, bytes}, {q, n}, {q_scale, (size_t)rows * ng * 4},
+                        {rstd, (size_t)rows * 4}};
+  const Range ins[] = {{x, bytes}, {residual, bytes}, {gamma, d * size_of(dtype)}};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = i + 1; j < 5; ++j)
+      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return MOE_ERR_INVALID_ARG;
+    for (int j = 0; j < 3; ++j) {
+      const bool in_place = i < 2 && j < 2 && outs[i].p == ins[j].p;
+      if (!in_place && overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return MOE_ERR_INVALID_ARG;
+    }
+  }
+  RmsNormArgs a{};
+  a.rows = rows; a.d = d; a.dtype = dtype; a.group = group; a.eps = eps; a.x = x;
+  a.residual = residual; a.gamma = gamma; a.h = h; a.y = y; a.q = q; a.q_scale = q_scale;
+  a.rstd = rstd;
+  return cuda_status(launch_rmsnorm(a, (cudaStream_t)stream));
+}
+
+size_t moe_rmsnorm_bwd_workspace_size(int64_t rows, int32_t d) {
+  if (rows < 0 || rows >= (int64_t(1) << 31) || d < 1 || d > 32768) return 0;
+  const size_t n = (size_t)rmsnorm_bwd_max_partials(rows > 0 ? rows : 1) * d * sizeof(float);
+  return align256(n);
+}
+
+moe_status_t moe_rmsnorm_bwd(int32_t dtype, int32_t dy_dtype, int32_t dx_dtype, int64_t rows,
+                             int32_t d, const void *dy, const void *h, const void *gamma,
+                             const float *rstd, const void *dh, void *dx, float *dgamma, void *ws,
+                             size_t ws_bytes, moe_stream_t stream) {
+  NvtxRange trace("moe_rmsnorm_bwd");
+  moe_status_t st = norm_check(dtype, rows, d);
+  if (st != MOE_OK) return st;
+  if (!dtype_ok(dy_dtype) || !dtype_ok(dx_dtype) ||
+      (dtype == MOE_F32 && (dy_dtype != MOE_F32 || dx_dtype != MOE_F32)))
+    return MOE_ERR_INVALID_ARG;
+  if (!dgamma || !aligned16(dgamma)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (rows == 0) return cuda_status(cudaMemsetAsync(dgamma, 0, (size_t)d * sizeof(float), s));
+  if (!dy || !h || !gamma || !rstd || !dx || !ws) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(gamma) || !aligned4(rstd) ||
+      (dh && !aligned16(dh)) || !aligned16(dx) || !aligned16(ws))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_rmsnorm_bwd_workspace_size(rows, d)) return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)rows * d, b = size_of(dtype), bdx = n * size_of(dx_dtype);
+  const size_t bws = moe_rmsnorm_bwd_workspace_size(rows, d), bg = (size_t)d * sizeof(float);
+  const bool on_dy = dx == dy && dx_dtype == dy_dtype, on_dh = dx == dh && dx_dtype == dtype;
+  if ((!on_dy && overlap(dx, bdx, dy, n * size_of(dy_dtype))) ||
+      (!on_dh && overlap(dx, bdx, dh, n * b)) || overlap(dx, bdx, h, n * b) ||
+      overlap(dx, bdx, gamma, d * b) || overlap(dx, bdx, rstd, (size_t)rows * 4) ||
+      overlap(dx, bdx, ws, bws) || overlap(dx, bdx, dgamma, bg))
+    return MOE_ERR_INVALID_ARG;
+  const struct { const void *p; size_t n; } ins[] = {{dy, n * size_of(dy_dtype)}, {h, n * b},
+                                                     {gamma, d * b}, {rstd, (size_t)rows * 4},
+                                                     {dh, n * b}};
+  for (const auto &in : ins)
+    if (overlap(dgamma, bg, in.p, in.n) || overlap(ws, bws, in.p, in.n)) return MOE_ERR_INVALID_ARG;
+  if (overlap(dgamma, bg, ws, bws)) return MOE_ERR_INVALID_ARG;
+  RmsNormBwdArgs a{};
+  a.rows = rows; a.d = d; a.dtype = dtype; a.dy_dtype = dy_dtype; a.dx_dtype = dx_dtype; a.dy = dy;
+  a.h = h; a.gamma = gamma; a.rstd = rstd; a.dh = dh; a.dx = dx; a.dgamma = dgamma;
+  a.partial = static_cast<float *>(ws);
+  return cuda_status(launch_rmsnorm_bwd(a, s));
+}
+
+static BalanceArgs balance_args(const moe_shape_t *s) {
+  BalanceArgs a{};
+  a.T = s->T; a.S = subseq(s); a.n_sub = (a.T + a.S - 1) / a.S; a.E = s->E; a.K = s->K;
+  return a;
+}
+
+moe_status_t moe_balance_loss(const moe_shape_t *shape, const float *logits, const int32_t *topk_idx,
+                              const uint8_t *mask, float alpha, float *loss, int32_t *counts,
+                              float *prob_mean, float *coef, void *ws, moe_stream_t stream) {
+  NvtxRange trace("moe_balance_loss");
+  if (!shape_ok(shape) || !std::isfinite(alpha)) return MOE_ERR_INVALID_ARG;
+  if (!logits || !topk_idx || !loss || !counts || !coef || !ws) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned4(topk_idx) || !aligned4(loss) || !aligned4(counts) ||
+      !aligned4(prob_mean) || !aligned4(coef) || !aligned16(ws))
+    return MOE_ERR_INVALID_ARG;
+  BalanceArgs a = balance_args(shape);
+  a.logits = logits; a.topk_idx = topk_idx; a.mask = mask; a.alpha = alpha; a.loss = loss;
+  a.counts = counts; a.prob_mean = prob_mean; a.coef = coef;
+  a.partial = static_cast<char *>(ws) + layout(shape).bal;
+  a.status = status_word(ws);
+  return cuda_status(launch_balance_loss(a, (cudaStream_t)stream));
+}
+
+moe_status_t moe_balance_loss_bwd(const moe_shape_t *shape, const float *logits, const uint8_t *mask,
+                                  const float *coef, const float *dloss, float *dlogits,
+                                  moe_stream_t stream) {
+  NvtxRange trace("moe_balance_loss_bwd");
+  if (!shape_ok(shape) || !logits || !coef || !dlogits) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned4(coef) || !aligned4(dloss) || !aligned16(dlogits))
+    return MOE_ERR_INVALID_ARG;
+  BalanceArgs a = balance_args(shape);
+  const size_t n = (size_t)a.T * a.E * sizeof(float);
+  if (dlogits != logits && overlap(dlogits, n, logits, n)) return MOE_ERR_INVALID_ARG;
+  a.logits = logits; a.mask = mask; a.coef = const_cast<float *>(coef); a.dloss = dloss;
+  a.dlogits = dlogits;
+  return cuda_status(launch_balance_loss_bwd(a, (cudaStream_t)stream));
+}
+
+moe_status_t moe_permute_e4m3(const moe_shape_t *shape, const void *q, const float *q_scale,
+                              int32_t group, const int32_t *topk_idx, const uint8_t *keep, void *Xp,
+                              int32_t *row_of, int32_t *src_of, int32_t *counts, int32_t *offsets,
+                              void *ws, moe_stream_t stream) {
+  NvtxRange trace("moe_permute_e4m3");
+  if (!shape_ok(shape) || group < 0) return MOE_ERR_INVALID_ARG;
+  if (!group_ok(group)) return MOE_ERR_UNSUPPORTED;
+  if (!q || !q_scale || !topk_idx || !keep || !Xp || !row_of || !src_of || !counts || !offsets || !ws)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned4(q_scale) || !aligned16(Xp) || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  PermuteArgs a{};
+  a.T = shape->T; a.d = shape->d; a.E = shape->E; a.K = shape->K; a.dtype = shape->dtype;
+  a.topk_idx = topk_idx; a.keep = keep; a.row_of = row_of; a.src_of = src_of;
+  a.counts = counts; a.offsets = offsets;
+  a.blk_counts = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + layout(shape).map);
+  a.status = status_word(ws);
+  cudaError_t e = launch_permute(a, (cudaStream_t)stream);   // Xp NULL: the map
+  a.Xp = Xp;
+  if (e == cudaSuccess) e = launch_permute_e4m3_rows(a, q, q_scale, group, (cudaStream_t)stream);
+  return cuda_status(e);
+}
+
+// MOE_OK for a list of tensors
+static moe_status_t list_check(int32_t n, const moe_tensor_t *list) {
+  if (n < 0 || (n > 0 && !list)) return MOE_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n; ++i) {
+    const moe_tensor_t &t = list[i];
+    if (t.numel < 0 || t.numel >= (int64_t(1) << 56) || !dtype_ok(t.dtype)) return MOE_ERR_INVALID_ARG;
+    if (t.numel > 0 && (!t.data || reinterpret_cast<uintptr_t>(t.data) % size_of(t.dtype) != 0))
+      return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+moe_status_t moe_grad_norm(int32_t n, const moe_tensor_t *grads, float *norm, void *ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+  NvtxRange trace("moe_grad_norm");
+  static_assert(kMaxNormPartials * sizeof(double) <= MOE_GRAD_NORM_WORKSPACE_BYTES,
+                "partial sums exceed the documented workspace");
+  moe_status_t st = list_check(n, grads);
+  if (st != MOE_OK) return st;
+  if (!norm || !aligned4(norm) || !ws || !aligned16(ws) || ws_bytes < MOE_GRAD_NORM_WORKSPACE_BYTES)
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_grad_norm(n, grads, norm, static_cast<double *>(ws), (cudaStream_t)stream));
+}
+
+moe_status_t moe_grad_clip(int32_t n, const moe_tensor_t *grads, const moe_tensor_t *out,
+                           const float *norm, float max_norm, float *coef, moe_stream_t stream) {
+  NvtxRange trace("moe_grad_clip");
+  moe_status_t st = list_check(n, grads);
+  if (st == MOE_OK && out != nullptr) st = list_check(n, out);
+  if (st != MOE_OK) return st;
+  if (!norm || !aligned4(norm) || !aligned4(coef) || !(max_norm >= 0.0f) || !std::isfinite(max_norm))
+    return MOE_ERR_INVALID_ARG;
+  if (out != nullptr)
+    for (int32_t i = 0; i < n; ++i) {
+      if (out[i].numel != grads[i].numel || out[i].dtype != grads[i].dtype) return MOE_ERR_INVALID_ARG;
+      const size_t b = (size_t)grads[i].numel * size_of(grads[i].dtype);
+      if (out[i].data != grads[i].data && overlap(out[i].data, b, grads[i].data, b))
+        return MOE_ERR_INVALID_ARG;
+    }
+  return cuda_status(launch_grad_clip(n, grads, out, norm, max_norm, coef, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -221,6 +221,7 @@ struct RouteBwdArgs {
   const float *logits, *topk_prob, *topk_w, *dw, *dz, *dx_in;
   const int32_t *topk_idx;
   float *dW_r, *db_r, *dw_sg, *dx_router;
+  const float *dl_add;  // [T, E] added to the logits' gradient, or NULL
   float *dl;       // ws [T, E]
   float *partial;  // ws [nchunk, E+1, d]
   uint32_t *status;
@@ -248,5 +249,57 @@ struct RouterBwdTc {
   uint32_t *status;
 };
 cudaError_t launch_router_bwd_tc(const RouterBwdTc &a, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Operators around the layer (norm.cu, balance.cu, dispatch.cu, grads.cu).
+
+struct RmsNormArgs {
+  int64_t rows;
+  int d, dtype, group;
+  float eps;
+  const void *x, *residual, *gamma;
+  void *h, *y, *q;
+  float *q_scale, *rstd;
+};
+cudaError_t launch_rmsnorm(const RmsNormArgs &a, cudaStream_t s);
+
+struct RmsNormBwdArgs {
+  int64_t rows;
+  int d, dtype, dy_dtype, dx_dtype;
+  const void *dy, *h, *gamma, *dh;
+  const float *rstd;
+  void *dx;
+  float *dgamma;
+  float *partial;   // ws [rmsnorm_bwd_max_partials(rows), d]
+};
+int64_t rmsnorm_bwd_max_partials(int64_t rows);
+cudaError_t launch_rmsnorm_bwd(const RmsNormBwdArgs &a, cudaStream_t s);
+
+struct BalanceArgs {
+  int64_t T, S, n_sub;   // S: sub-sequence length, n_sub = ceil(T / S)
+  int E, K;
+  float alpha;
+  const float *logits, *dloss;
+  const int32_t *topk_idx;
+  const uint8_t *mask;
+  float *loss;
+  int32_t *counts;
+  float *prob_mean, *coef, *dlogits;
+  void *partial;   // ws, balance_workspace_bytes(T, S, E)
+  uint32_t *status;
+};
+size_t balance_workspace_bytes(int64_t T, int64_t S, int E);
+cudaError_t launch_balance_loss(const BalanceArgs &a, cudaStream_t s);
+cudaError_t launch_balance_loss_bwd(const BalanceArgs &a, cudaStream_t s);
+
+// Rows of an e4m3 matrix with scales, permuted: Xp[row_of[t,k]] = dtype(q[t] * scale[t]).
+cudaError_t launch_permute_e4m3_rows(const PermuteArgs &a, const void *q, const float *q_scale,
+                                     int group, cudaStream_t s);
+
+constexpr int kMaxNormPartials = 1216;   // doubles in the workspace of moe_grad_norm
+cudaError_t launch_grad_norm(int n, const moe_tensor_t *grads, float *norm, double *partial,
+                             cudaStream_t s);
+cudaError_t launch_grad_clip(int n, const moe_tensor_t *grads, const moe_tensor_t *out,
+                             const float *norm, float max_norm, float *coef, cudaStream_t s);
 
 }  // namespace moe

@@ -20,6 +20,7 @@
 #include <mutex>
 
 #include <cuda.h>
+#include <cuda_fp8.h>
 
 #include "common.cuh"
 
@@ -211,6 +212,45 @@ __global__ void __launch_bounds__(256) pad_fill_kernel(PermuteArgs a, int vec_pe
     for (int64_t i = lo * vec_per_row + threadIdx.x; i < hi * vec_per_row; i += blockDim.x)
       Xp[i] = make_uint4(0, 0, 0, 0);
   for (int64_t r = lo + threadIdx.x; r < hi; r += blockDim.x) a.src_of[r] = -1;
+}
+
+// Xp[row_of[t,k]] = T(q[t] * scale[t]): one CTA per token reads the token's
+// e4m3 row once and writes it to its kept slots' rows. HBM-bound: d bytes read
+// and K d sizeof(T) written per token.
+template <typename T>
+__global__ void __launch_bounds__(256) permute_e4m3_kernel(PermuteArgs a, const uint8_t *q,
+                                                           const float *q_scale, int group, int ng) {
+  constexpr int N = Vec<T>::N;
+  const int64_t t = blockIdx.x;
+  const int K = a.K;
+  pdl_wait();   // row_of comes from map_scatter
+  int32_t r[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) r[k] = k < K ? a.row_of[t * K + k] : -1;
+  T *Xp = reinterpret_cast<T *>(a.Xp);
+  for (int v = threadIdx.x * N; v < a.d; v += blockDim.x * N) {
+    const float s = q_scale[t * ng + v / group];
+    float f[N];
+    const uint8_t *src = q + t * a.d + v;
+    uint32_t raw[N / 4];
+    if constexpr (N == 8) {
+      const uint2 u = *reinterpret_cast<const uint2 *>(src);
+      raw[0] = u.x; raw[1] = u.y;
+    } else {
+      raw[0] = *reinterpret_cast<const uint32_t *>(src);
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+          (__nv_fp8x2_storage_t)(raw[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+      const float2 p = __half22float2(__half2(h));
+      f[2 * i] = p.x * s;
+      f[2 * i + 1] = p.y * s;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (r[k] >= 0) store16<T>(Xp + (int64_t)r[k] * a.d + v, f);
+  }
 }
 
 // out[t] = sum_k w[t,k] Yp[row_of[t,k]] (+ sigmoid(z_t) Ys[t]), fp32 sum in
@@ -510,6 +550,25 @@ cudaError_t launch_permute(const PermuteArgs &a, cudaStream_t s) {
   cfg.blockDim = dim3(32);
   cfg.dynamicSmemBytes = smem;
   return cudaLaunchKernelEx(&cfg, permute_bulk_kernel, a, row_bytes, tpc);
+}
+
+cudaError_t launch_permute_e4m3_rows(const PermuteArgs &a, const void *q, const float *q_scale,
+                                     int group, cudaStream_t s) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.T);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  const int g = group > 0 ? group : a.d;
+  const int ng = (a.d + g - 1) / g;
+  const uint8_t *qb = static_cast<const uint8_t *>(q);
+  return a.dtype == MOE_BF16
+             ? cudaLaunchKernelEx(&cfg, permute_e4m3_kernel<__nv_bfloat16>, a, qb, q_scale, g, ng)
+             : cudaLaunchKernelEx(&cfg, permute_e4m3_kernel<float>, a, qb, q_scale, g, ng);
 }
 
 // Slot bound KK >= K of the un-permute kernels: 1, 2, 4 or 8.

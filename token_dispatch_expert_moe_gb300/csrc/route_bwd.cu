@@ -6,7 +6,8 @@
 // combine weights w = prob / Z.
 //   1. dl_kernel (one warp per token): p = softmax(logits) (same fp32
 //      arithmetic as the forward); dp on the Top-K slots
-//      ((g - <g,w>) / Z with renorm, g without); dl = p (dp - <p,dp>).
+//      ((g - <g,w>) / Z with renorm, g without); dl = p (dp - <p,dp>)
+//      (+ dl_add, the gradient of a loss on the logits).
 //   2. dx_kernel: dx_router[t] = dx_in[t] + sum_e dl[t,e] W_r[e] + dz[t] w_sg,
 //      register-tiled (8 tokens x 4 columns per thread);
 //   3. wgrad_partial_kernel: per chunk of tokens, partial sums of dl^T x (and
@@ -51,8 +52,13 @@ __global__ void __launch_bounds__(256) dl_kernel(RouteBwdArgs a) {
   const bool v0 = lane < E, v1 = lane + 32 < E;
   float s = (v0 ? p0 * dp0 : 0.0f) + (v1 ? p1 * dp1 : 0.0f);
   s = warp_sum(s);
-  if (v0) a.dl[t * E + lane] = p0 * (dp0 - s);
-  if (v1) a.dl[t * E + lane + 32] = p1 * (dp1 - s);
+  float dl0 = p0 * (dp0 - s), dl1 = p1 * (dp1 - s);
+  if (a.dl_add != nullptr) {   // a loss on the logits
+    if (v0) dl0 += a.dl_add[t * E + lane];
+    if (v1) dl1 += a.dl_add[t * E + lane + 32];
+  }
+  if (v0) a.dl[t * E + lane] = dl0;
+  if (v1) a.dl[t * E + lane + 32] = dl1;
 }
 
 // dx_router[t, j] = dx_in[t, j] + sum_c dl[t, c] W[c, j]  (row c = E is w_sg
