@@ -1,9 +1,11 @@
 """MoELayer: the whole layer through the C ABI, buffers held in torch tensors.
 
-Forward: moe_route -> moe_permute -> moe_expert_ffn (routed experts)
+Forward: [moe_rmsnorm ->] moe_route [-> moe_balance_loss] -> moe_permute or
+moe_permute_e4m3 -> moe_expert_ffn (routed experts)
 [-> moe_expert_ffn (shared expert: one group, offsets {0, T})] -> moe_unpermute.
-Backward: moe_unpermute_bwd -> moe_expert_ffn_bwd (routed [, shared]) ->
-moe_route_bwd -> moe_permute_bwd.
+Backward: moe_unpermute_bwd -> moe_expert_ffn_bwd (routed [, shared])
+[-> moe_balance_loss_bwd] -> moe_route_bwd -> moe_permute_bwd
+[-> moe_rmsnorm_bwd]; clip_grads: moe_grad_norm -> moe_grad_clip.
 torch only allocates device memory and supplies the stream; every step runs
 in libmoe.so.
 """
@@ -13,6 +15,8 @@ import numpy as np
 import torch
 
 from . import _lib as L
+
+E4M3_GROUP = 128   # columns per scale of the 8-bit rows
 
 
 def to_device(a: np.ndarray, device="cuda") -> torch.Tensor:
@@ -41,10 +45,30 @@ class MoELayer:
     gather=True (bf16, forward only, etp = 1) fuses the permutation into the
     routed experts' gate/up GEMM: moe_permute builds the map alone (Xp NULL)
     and moe_expert_ffn_gather reads each permuted row from x through src_of,
-    so the permuted copy of the tokens is never written."""
+    so the permuted copy of the tokens is never written.
+
+    With a weight "gamma" [d] (in the layer's dtype) the layer is pre-normed:
+    forward(x, residual) first forms h = x + residual (kept in self.h, the
+    residual stream that goes on beside the output) and runs the MoE layer on
+    its RMS norm; backward(dout, dh=...) takes the gradient that reaches h from
+    elsewhere and gives "dx", the gradient of h (so of x and residual alike),
+    and "dgamma". dx_dtype="act" gives dx in the layer's dtype instead of
+    fp32, which is what the layer below takes as its dout and dh.
+
+    dispatch="e4m3" (with gamma; compact layout, no gather) moves the routed
+    experts' rows in 8 bits with one scale per 128 columns: the norm writes
+    them and moe_permute_e4m3 reads them. Router and shared expert still read
+    the norm's output; the gradient passes the rounding as if it were not there.
+
+    balance > 0 adds the router's balance loss with that factor: forward leaves
+    it in self.loss ([1], on the device) and the pre-drop counts per
+    sub-sequence and expert in self.load; forward's mask ([T] uint8, 0 =
+    padding) takes tokens out of it; backward adds its gradient, times dloss
+    ([1] on the device) if given, to the router's."""
 
     def __init__(self, cfg, weights: dict, device="cuda", backward=None, etp: int = 1,
-                 layout: str = "compact", gather: bool = False):
+                 layout: str = "compact", gather: bool = False, norm_eps: float = 1e-6,
+                 dispatch: str = "act", balance: float = 0.0, dx_dtype: str = "f32"):
         self.cfg = cfg
         self.etp = etp
         self.layout = layout
@@ -69,8 +93,31 @@ class MoELayer:
         else:
             raise ValueError(f"unknown layout {layout!r}")
         self.rows = N   # rows of the permuted buffers
+        self.norm, self.norm_eps, self.balance = "gamma" in weights, norm_eps, balance
+        if dispatch not in ("act", "e4m3") or dx_dtype not in ("f32", "act"):
+            raise ValueError(f"unknown dispatch {dispatch!r} or dx_dtype {dx_dtype!r}")
+        if dispatch == "e4m3" and (not self.norm or layout != "compact" or gather):
+            raise ValueError('dispatch="e4m3" needs gamma, the compact layout and gather=False')
+        if dx_dtype == "act" and not self.norm:
+            raise ValueError('dx_dtype="act" needs gamma')
+        self.e4m3 = dispatch == "e4m3"
         z = lambda *s, dtype=dt: torch.empty(*s, dtype=dtype, device=device)  # noqa: E731
         self.ws = torch.zeros(L.moe_workspace_size(self.shape), dtype=torch.uint8, device=device)
+        if self.norm:
+            self.h_own = z(T, d)   # x + residual; without a residual h is x
+            self.y = z(T, d)
+            self.rstd = z(T, dtype=torch.float32)
+            self.q = self.q_scale = None
+            if self.e4m3:
+                self.q = z(T, d, dtype=torch.float8_e4m3fn)
+                self.q_scale = z(T, -(-d // E4M3_GROUP), dtype=torch.float32)
+        if balance:
+            n_sub = -(-T // cfg.subseq)
+            self.loss = z(1, dtype=torch.float32)
+            self.load = z(n_sub, E, dtype=torch.int32)
+            self.prob_mean = z(n_sub, E, dtype=torch.float32)
+            self.balance_coef = z(n_sub * E + 1, dtype=torch.float32)
+            self.dlogits = z(T, E, dtype=torch.float32)
         self.logits = z(T, E, dtype=torch.float32)
         self.topk_idx = z(T, K, dtype=torch.int32)
         self.topk_prob = z(T, K, dtype=torch.float32)
@@ -127,6 +174,12 @@ class MoELayer:
             self.db_r = z(E, dtype=torch.float32)
             self.dx_router = z(T, d, dtype=torch.float32)
             self.dx = z(T, d, dtype=torch.float32)
+            if self.norm:
+                self.dgamma = z(d, dtype=torch.float32)
+                self.dx_h = z(T, d) if dx_dtype == "act" and dt != torch.float32 else self.dx
+                self.norm_ws = z(L.moe_rmsnorm_bwd_workspace_size(T, d), dtype=torch.uint8)
+            self.grad_ws = z(L.MOE_GRAD_NORM_WORKSPACE_BYTES, dtype=torch.uint8)
+            self.grad_norm = z(1, dtype=torch.float32)
             if self.shared:
                 Fs = cfg.Fs
                 self.dYs = z(T, d)
@@ -137,14 +190,34 @@ class MoELayer:
                 self.dWs_down = z(d, Fs, dtype=torch.float32)
                 self.dw_sg = z(d, dtype=torch.float32)
 
-    def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:
+        self.grads = None   # the weight gradients' list, made by the first clip_grads
+
+    def forward(self, x: torch.Tensor, stream=None, residual=None, mask=None) -> torch.Tensor:
         c, s, w = self.cfg, self.shape, self.w
-        self.x = x
+        if residual is not None and not self.norm:
+            raise ValueError("a residual needs the norm (weight gamma)")
+        if mask is not None and not self.balance:
+            raise ValueError("a mask needs the balance loss")
+        if self.norm:
+            self.h = x if residual is None else self.h_own
+            L.moe_rmsnorm(self.dtype_code, c.T, c.d, x, residual, w["gamma"], self.norm_eps,
+                          None if residual is None else self.h, self.y, self.q, self.q_scale,
+                          E4M3_GROUP if self.e4m3 else 0, self.rstd, stream)
+            x = self.y
+        self.x, self.mask = x, mask
         L.moe_route(s, x, w["W_r"], w.get("b_r"), w.get("w_sg"), self.logits, self.gate_logit,
                     self.topk_idx, self.topk_prob, self.topk_w, self.keep, self.ws, stream)
-        permute = L.moe_permute_padded if self.layout == "padded" else L.moe_permute
-        permute(s, x, self.topk_idx, self.keep, self.Xp, self.row_of, self.src_of,
-                self.counts, self.offsets, self.ws, stream)
+        if self.balance:
+            L.moe_balance_loss(s, self.logits, self.topk_idx, mask, self.balance, self.loss,
+                               self.load, self.prob_mean, self.balance_coef, self.ws, stream)
+        if self.e4m3:
+            L.moe_permute_e4m3(s, self.q, self.q_scale, E4M3_GROUP, self.topk_idx, self.keep,
+                               self.Xp, self.row_of, self.src_of, self.counts, self.offsets,
+                               self.ws, stream)
+        else:
+            permute = L.moe_permute_padded if self.layout == "padded" else L.moe_permute
+            permute(s, x, self.topk_idx, self.keep, self.Xp, self.row_of, self.src_of,
+                    self.counts, self.offsets, self.ws, stream)
         self.routed_ffn(stream)
         if self.shared:
             L.moe_expert_ffn(self.dtype_code, c.T, c.d, c.Fs, 1, self.off1, x, w["Ws_gu"],
@@ -184,13 +257,18 @@ class MoELayer:
                                  self.dW_down[s], self.ws, stream)
         L.moe_sum_partials(L.MOE_F32, self.etp, self.rows, c.d, self.dX_parts, self.dXp, stream)
 
-    def backward(self, dout: torch.Tensor, stream=None, marks=None) -> dict:
+    def backward(self, dout: torch.Tensor, stream=None, marks=None, dh=None, dloss=None) -> dict:
         """marks: optional dict of (start, end) CUDA event pairs, keyed by
         "unpermute_bwd", "ffn_bwd" (routed experts), "shared_ffn_bwd",
-        "route_bwd" and "permute_bwd"; each present pair is recorded on the
-        current stream around that call."""
+        "route_bwd" (the balance loss's gradient included), "permute_bwd" and
+        "norm_bwd"; each present pair is recorded on the current stream around
+        that call."""
         c, s, w = self.cfg, self.shape, self.w
         marks = marks or {}
+        if dh is not None and not self.norm:
+            raise ValueError("dh needs the norm (weight gamma)")
+        if dloss is not None and not self.balance:
+            raise ValueError("dloss needs the balance loss")
 
         def mark(name, i):
             if name in marks:
@@ -213,17 +291,57 @@ class MoELayer:
             mark("shared_ffn_bwd", 1)
             dx_in = self.dXs
         mark("route_bwd", 0)
-        L.moe_route_bwd(s, self.x, w["W_r"], w.get("w_sg"), self.logits, self.topk_idx,
-                        self.topk_prob, self.topk_w, self.dw, self.dz if self.shared else None,
-                        dx_in, self.dW_r, self.db_r if "b_r" in w else None,
-                        self.dw_sg if self.shared else None, self.dx_router, self.ws, stream)
+        args = [s, self.x, w["W_r"], w.get("w_sg"), self.logits, self.topk_idx, self.topk_prob,
+                self.topk_w, self.dw, self.dz if self.shared else None]
+        outs = [dx_in, self.dW_r, self.db_r if "b_r" in w else None,
+                self.dw_sg if self.shared else None, self.dx_router, self.ws, stream]
+        if self.balance:
+            L.moe_balance_loss_bwd(s, self.logits, self.mask, self.balance_coef, dloss,
+                                   self.dlogits, stream)
+            L.moe_route_bwd_add(*args, self.dlogits, *outs)
+        else:
+            L.moe_route_bwd(*args, *outs)
         mark("route_bwd", 1)
         mark("permute_bwd", 0)
         L.moe_permute_bwd(s, self.dXp, self.row_of, self.dx_router, self.dx, stream)
         mark("permute_bwd", 1)
-        g = {"dx": self.dx, "dW_r": self.dW_r, "dW_gu": self.dW_gu, "dW_down": self.dW_down}
+        dx = self.dx
+        if self.norm:
+            mark("norm_bwd", 0)
+            dx = self.dx_h   # self.dx itself, in place, unless dx leaves in the layer's dtype
+            L.moe_rmsnorm_bwd(self.dtype_code, L.MOE_F32, self.dtype_code if dx is not self.dx else L.MOE_F32,
+                              c.T, c.d, self.dx, self.h, w["gamma"], self.rstd, dh, dx, self.dgamma,
+                              self.norm_ws, stream)
+            mark("norm_bwd", 1)
+        g = {"dx": dx, "dW_r": self.dW_r, "dW_gu": self.dW_gu, "dW_down": self.dW_down}
+        if self.norm:
+            g["dgamma"] = self.dgamma
         if "b_r" in w:
             g["db_r"] = self.db_r
         if self.shared:
             g.update(dWs_gu=self.dWs_gu, dWs_down=self.dWs_down, dw_sg=self.dw_sg)
         return g
+
+    def weight_grads(self) -> list:
+        """The weight gradients that backward writes, as one flat list (for a
+        TensorList over several layers)."""
+        g = [self.dW_r]
+        for t in (self.dW_gu, self.dW_down):
+            g += t if isinstance(t, list) else [t]
+        if "b_r" in self.w:
+            g.append(self.db_r)
+        if self.shared:
+            g += [self.dWs_gu, self.dWs_down, self.dw_sg]
+        if self.norm:
+            g.append(self.dgamma)
+        return g
+
+    def clip_grads(self, max_norm: float, stream=None) -> torch.Tensor:
+        """Clips the weight gradients in place to a global norm of max_norm and
+        returns their norm before it, [1] on the device; a norm that is not
+        finite leaves them as they are."""
+        if self.grads is None:
+            self.grads = L.TensorList(self.weight_grads())
+        L.moe_grad_norm(self.grads, self.grad_norm, self.grad_ws, stream)
+        L.moe_grad_clip(self.grads, None, self.grad_norm, max_norm, None, stream)
+        return self.grad_norm
