@@ -58,6 +58,7 @@ class TensorList:
         self.n = len(self.tensors)
         self.array = (MoETensor * max(1, self.n))(
             *[MoETensor(t.data_ptr(), t.numel(), codes[t.dtype]) for t in self.tensors])
+        self.address = ctypes.addressof(self.array)
 
 
 def shape_of(cfg) -> MoEShape:
@@ -131,10 +132,28 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """The handle of torch's current stream. torch.cuda.current_stream() builds a
+    Stream object (3 us on the GB300's Grace CPU, as much as the rest of a call);
+    the raw handle, where torch gives it, takes 0.1 us."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None or not hasattr(torch._C, "_cuda_getDevice"):
+        return lambda: torch.cuda.current_stream().cuda_stream
+    torch.cuda.init()
+    device = torch._C._cuda_getDevice
+    return lambda: raw(device())
+
+
 def _stream(stream):
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -299,7 +318,7 @@ def moe_grad_norm(grads, norm, ws, stream=None, ws_bytes=None):
     """grads: a TensorList. ws: a device tensor (its size becomes ws_bytes) or a pointer with ws_bytes."""
     if ws_bytes is None:
         ws_bytes = ws.numel() * ws.element_size()
-    _call("moe_grad_norm", grads.n, ctypes.addressof(grads.array), _ptr(norm), _ptr(ws), ws_bytes,
+    _call("moe_grad_norm", grads.n, grads.address, _ptr(norm), _ptr(ws), ws_bytes,
           _stream(stream))
 
 
@@ -307,6 +326,6 @@ def moe_grad_clip(grads, out, norm, max_norm, coef, stream=None):
     """grads: a TensorList; out: a TensorList of the same tensors' sizes and types, or None for in place."""
     if out is not None and out.n != grads.n:
         raise MoEError("moe_grad_clip", 1)
-    _call("moe_grad_clip", grads.n, ctypes.addressof(grads.array),
-          None if out is None else ctypes.addressof(out.array), _ptr(norm), max_norm, _ptr(coef),
+    _call("moe_grad_clip", grads.n, grads.address,
+          None if out is None else out.address, _ptr(norm), max_norm, _ptr(coef),
           _stream(stream))

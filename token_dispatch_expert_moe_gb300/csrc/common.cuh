@@ -257,6 +257,8 @@ struct RmsNormArgs {
   int64_t rows;
   int d, dtype, group;
   float eps;
+  float inv_d;           // these three: set by launch_rmsnorm
+  int ng, group_shift;   // groups per row, log2(vectors per group)
   const void *x, *residual, *gamma;
   void *h, *y, *q;
   float *q_scale, *rstd;
@@ -266,6 +268,7 @@ cudaError_t launch_rmsnorm(const RmsNormArgs &a, cudaStream_t s);
 struct RmsNormBwdArgs {
   int64_t rows;
   int d, dtype, dy_dtype, dx_dtype;
+  float inv_d;           // set by launch_rmsnorm_bwd
   const void *dy, *h, *gamma, *dh;
   const float *rstd;
   void *dx;

@@ -9,6 +9,8 @@
 // y is rounded once, and q is taken from the unrounded y.
 // Backward, with xhat = h rstd and g = dy gamma:
 //   dx = rstd (g - xhat mean_j(g_j xhat_j)) + dh,  dgamma = sum_rows dy xhat.
+#include <atomic>
+
 #include <cuda_fp8.h>
 
 #include "launch.cuh"
@@ -20,25 +22,56 @@ constexpr float kE4m3Max = 448.0f;
 // Smallest amax a scale is made of: 448 / amax stays finite.
 constexpr float kAmaxFloor = 7.70372e-34f;   // 2^-110
 
-__device__ __forceinline__ float block_max(float v, float *smem32) {
+// Sum or maximum over the CTA with one barrier: every warp writes its value
+// and reads them all. `red` alternates between two rows from call to call, so
+// that a warp ahead by one call overwrites nothing that is still read.
+template <bool MAX> __device__ __forceinline__ float reduce_op(float a, float b) {
+  return MAX ? fmaxf(a, b) : a + b;
+}
+template <bool MAX>
+__device__ __forceinline__ float warp_reduce(float v) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = 16; o >= 1; o >>= 1) v = reduce_op<MAX>(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <bool MAX>
+__device__ __forceinline__ float cta_reduce(float v, float (&red)[2][32], int &turn) {
+  v = warp_reduce<MAX>(v);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) red[turn][warp] = v;
   __syncthreads();
-  if (lane == 0) smem32[warp] = v;
-  __syncthreads();
-  const int nw = blockDim.x >> 5;
-  float r = lane < nw ? smem32[lane] : 0.0f;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+  v = lane < (int)(blockDim.x >> 5) ? red[turn][lane] : 0.0f;
+  turn ^= 1;
+  return warp_reduce<MAX>(v);
+}
+
+// Copies of 16 or 8 bytes to shared memory that complete in the background;
+// a thread copies only what it reads itself, so waiting for its own groups is
+// all the synchronisation that they need.
+template <int BYTES> __device__ __forceinline__ void copy_async(void *smem, const void *gmem) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(gmem) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float reciprocal(float v) {   // within 1 ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
-// Scale of a group and the factor y is multiplied with.
+// Scale of a group and the factor that y is multiplied with, its reciprocal.
+// The largest |y| may come out a few ulp above 448: the conversion saturates.
 __device__ __forceinline__ float2 scale_of(float amax) {
   if (amax == 0.0f) return make_float2(1.0f, 0.0f);
-  const float a = fmaxf(amax, kAmaxFloor);
-  return make_float2(__fdiv_rn(a, kE4m3Max), __fdiv_rn(kE4m3Max, a));
+  const float s = fmaxf(amax, kAmaxFloor) * (1.0f / kE4m3Max);
+  return make_float2(s, reciprocal(s));
 }
 
 template <int N> struct Bytes;
@@ -57,19 +90,97 @@ __device__ __forceinline__ typename Bytes<N>::type to_e4m3(const float (&v)[N], 
   return out;
 }
 
-// One row per warp (WARP) or per CTA, held in registers as packed vectors:
-// x and the residual are read once, and a thread writes only columns that it
-// has read, so h and y may replace x or the residual in place.
+// h = dtype(x + residual) of one vector
+template <typename T> __device__ __forceinline__ uint4 add_residual(uint4 x, uint4 r) {
+  constexpr int N = Vec<T>::N;
+  float xv[N], rv[N];
+  unpack16<T>(x, xv);
+  unpack16<T>(r, rv);
+#pragma unroll
+  for (int k = 0; k < N; ++k) xv[k] = __fadd_rn(xv[k], rv[k]);
+  uint4 h;
+  store16<T>(reinterpret_cast<T *>(&h), xv);
+  return h;
+}
+
+// The row's outputs from its h and gamma (in registers, W threads, vector
+// id + i W in thread id): y, and q with its scales.
+template <typename T, int NV, bool WARP>
+__device__ __forceinline__ void write_row(const RmsNormArgs &a, int64_t row, int id, int W,
+                                          const uint4 (&h)[NV], const uint4 (&g)[NV], float rstd,
+                                          float (&red)[2][32], int &turn) {
+  constexpr int N = Vec<T>::N;
+  using Q = typename Bytes<N>::type;
+  const int nvec = a.d / N;
+  T *y = reinterpret_cast<T *>(a.y) + row * a.d;
+  Q *q = reinterpret_cast<Q *>(a.q) + row * nvec;
+  float2 sc = make_float2(0.0f, 0.0f);
+  if (a.q != nullptr && a.group == 0) {   // one scale for the row
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float f[N], gv[N];
+      unpack16<T>(h[i], f);
+      unpack16<T>(g[i], gv);
+#pragma unroll
+      for (int k = 0; k < N; ++k) m = fmaxf(m, fabsf(f[k] * rstd * gv[k]));
+    }
+    m = WARP ? warp_reduce<true>(m) : cta_reduce<true>(m, red, turn);
+    sc = scale_of(m);
+    if (id == 0) a.q_scale[row] = sc.x;
+  }
+  // a group is 2^group_shift consecutive vectors, so consecutive lanes of a
+  // warp: 4 to 32 of them
+  const int last = (1 << a.group_shift) - 1;
+  float *scales = a.q_scale + row * a.ng;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = id + i * W;
+    const bool in = v < nvec;
+    float f[N], gv[N];
+    unpack16<T>(h[i], f);
+    unpack16<T>(g[i], gv);
+#pragma unroll
+    for (int k = 0; k < N; ++k) f[k] = f[k] * rstd * gv[k];
+    if (a.y != nullptr && in) store16<T>(y + v * N, f);
+    if (a.q != nullptr) {
+      if (a.group > 0) {
+        float m = 0.0f;
+#pragma unroll
+        for (int k = 0; k < N; ++k) m = fmaxf(m, fabsf(f[k]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+#pragma unroll
+        for (int o = 4; o <= 16; o *= 2)
+          if (o <= last) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        sc = scale_of(m);
+        if (in && (v & last) == 0) scales[v >> a.group_shift] = sc.x;
+      }
+      if (in) q[v] = to_e4m3<N>(f, sc.y);
+    }
+  }
+}
+
+__device__ __forceinline__ float rstd_of(float ss, const RmsNormArgs &a) {
+  return rsqrtf(fmaf(ss, a.inv_d, a.eps));   // within 2 ulp
+}
+
+// One row per warp (WARP: rows of up to 4 vectors a lane) or per CTA (rows
+// too wide for the ring below), held in registers as packed vectors: x and
+// the residual are read once, and a thread writes only columns that it has
+// read, so h and y may replace x or the residual in place.
 template <typename T, int NV, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(RmsNormArgs a) {
   constexpr int N = Vec<T>::N;
-  __shared__ float red[32];
+  __shared__ float red[2][32];
+  int turn = 0;
   const int W = WARP ? 32 : blockDim.x;
   const int id = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int64_t row = WARP ? ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5))
                            : (int64_t)blockIdx.x;
   if (WARP && row >= a.rows) return;   // a whole warp
   const int nvec = a.d / N;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
   const uint4 *x = reinterpret_cast<const uint4 *>(a.x) + row * nvec;
   const uint4 *res = reinterpret_cast<const uint4 *>(a.residual) + row * nvec;
   const uint4 *gam = reinterpret_cast<const uint4 *>(a.gamma);
@@ -77,29 +188,15 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(RmsNormArgs 
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = id + i * W;
-    h[i] = v < nvec ? x[v] : make_uint4(0, 0, 0, 0);
+    h[i] = v < nvec ? x[v] : zero;
+    g[i] = v < nvec ? gam[v] : zero;
   }
   if (a.residual != nullptr) {
-    uint4 r[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = id + i * W;
-      r[i] = v < nvec ? res[v] : make_uint4(0, 0, 0, 0);
+      h[i] = add_residual<T>(h[i], v < nvec ? res[v] : zero);
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float xv[N], rv[N];
-      unpack16<T>(h[i], xv);
-      unpack16<T>(r[i], rv);
-#pragma unroll
-      for (int k = 0; k < N; ++k) xv[k] = __fadd_rn(xv[k], rv[k]);
-      store16<T>(reinterpret_cast<T *>(&h[i]), xv);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = id + i * W;
-    g[i] = v < nvec ? gam[v] : make_uint4(0, 0, 0, 0);
   }
   float ss = 0.0f;
 #pragma unroll
@@ -111,168 +208,241 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(RmsNormArgs 
 #pragma unroll
     for (int k = 0; k < N; ++k) ss = fmaf(f[k], f[k], ss);
   }
-  ss = WARP ? warp_sum(ss) : block_sum(ss, red);
-  const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.d), a.eps));
+  ss = WARP ? warp_reduce<false>(ss) : cta_reduce<false>(ss, red, turn);
+  const float rstd = rstd_of(ss, a);
   if (a.rstd != nullptr && id == 0) a.rstd[row] = rstd;
-  if (a.y != nullptr) {
+  write_row<T, NV, WARP>(a, row, id, W, h, g, rstd, red, turn);
+}
+
+// Rows of several hundred columns and more: a persistent grid, a CTA per row
+// at a time, the next kStages - 1 rows of x and residual on their way to
+// shared memory while one row is reduced and written. gamma stays in
+// registers. HBM-bound: the ring keeps the loads in flight across the
+// reduction's barrier.
+constexpr int kStages = 3;
+
+template <typename T, int NV, bool RES>
+__global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) rmsnorm_ring_kernel(RmsNormArgs a) {
+  constexpr int N = Vec<T>::N;
+  constexpr int R = RES ? 2 : 1;
+  extern __shared__ uint4 ring[];   // [kStages][R][NV][W]
+  __shared__ float red[2][32];
+  int turn = 0;
+  const int W = blockDim.x, id = threadIdx.x;
+  const int nvec = a.d / N;
+  const uint4 *x = reinterpret_cast<const uint4 *>(a.x);
+  const uint4 *res = reinterpret_cast<const uint4 *>(a.residual);
+  const int64_t step = gridDim.x;
+  auto fetch = [&](int64_t row, int stage) {
+    uint4 *slot = ring + (size_t)stage * R * NV * W + id;
+    if (row < a.rows) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = id + i * W;
-      float f[N], gv[N];
-      unpack16<T>(h[i], f);
-      unpack16<T>(g[i], gv);
-#pragma unroll
-      for (int k = 0; k < N; ++k) f[k] = f[k] * rstd * gv[k];
-      if (v < nvec) store16<T>(reinterpret_cast<T *>(a.y) + row * a.d + (int64_t)v * N, f);
+      for (int i = 0; i < NV; ++i) {
+        const int v = id + i * W;
+        if (v < nvec) {
+          copy_async<16>(slot + i * W, x + row * nvec + v);
+          if (RES) copy_async<16>(slot + (NV + i) * W, res + row * nvec + v);
+        }
+      }
     }
-  }
-  if (a.q == nullptr) return;
-  using Q = typename Bytes<N>::type;
-  Q *q = reinterpret_cast<Q *>(a.q) + row * nvec;
-  if (a.group == 0) {   // one scale for the row
-    float m = 0.0f;
+    copy_commit();   // an empty group past the end keeps the count
+  };
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float f[N], gv[N];
-      unpack16<T>(h[i], f);
-      unpack16<T>(g[i], gv);
-#pragma unroll
-      for (int k = 0; k < N; ++k) m = fmaxf(m, fabsf(f[k] * rstd * gv[k]));
-    }
-    if (WARP) {
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    } else {
-      m = block_max(m, red);
-    }
-    const float2 sc = scale_of(m);
-    if (id == 0) a.q_scale[row] = sc.x;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = id + i * W;
-      float f[N], gv[N];
-      unpack16<T>(h[i], f);
-      unpack16<T>(g[i], gv);
-#pragma unroll
-      for (int k = 0; k < N; ++k) f[k] = f[k] * rstd * gv[k];
-      if (v < nvec) q[v] = to_e4m3<N>(f, sc.y);
-    }
-    return;
-  }
-  // a group is group / N consecutive vectors, so consecutive lanes of a warp
-  const int lanes = a.group / N;
-  const int ng = (a.d + a.group - 1) / a.group;
+  for (int s = 0; s < kStages - 1; ++s) fetch(blockIdx.x + s * step, s);
+  uint4 g[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = id + i * W;
-    float f[N], gv[N], m = 0.0f;
-    unpack16<T>(h[i], f);
-    unpack16<T>(g[i], gv);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      f[k] = f[k] * rstd * gv[k];
-      m = fmaxf(m, fabsf(f[k]));
-    }
-    for (int o = lanes >> 1; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float2 sc = scale_of(m);
-    if (v < nvec) {
-      if ((v & (lanes - 1)) == 0) a.q_scale[row * ng + v / lanes] = sc.x;
-      q[v] = to_e4m3<N>(f, sc.y);
-    }
+    g[i] = v < nvec ? reinterpret_cast<const uint4 *>(a.gamma)[v] : make_uint4(0, 0, 0, 0);
   }
+  int stage = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += step) {
+    // the stage read one row ago is free: its values have been used
+    fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+    copy_wait<kStages - 1>();   // this row's group
+    const uint4 *slot = ring + (size_t)stage * R * NV * W + id;
+    uint4 h[NV];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = id + i * W;
+      h[i] = make_uint4(0, 0, 0, 0);
+      if (v < nvec) {
+        h[i] = slot[i * W];
+        if (RES) h[i] = add_residual<T>(h[i], slot[(NV + i) * W]);
+        if (a.h != nullptr) reinterpret_cast<uint4 *>(a.h)[row * nvec + v] = h[i];
+      }
+      float f[N];
+      unpack16<T>(h[i], f);
+#pragma unroll
+      for (int k = 0; k < N; ++k) ss = fmaf(f[k], f[k], ss);
+    }
+    ss = cta_reduce<false>(ss, red, turn);
+    const float rstd = rstd_of(ss, a);
+    if (a.rstd != nullptr && id == 0) a.rstd[row] = rstd;
+    write_row<T, NV, false>(a, row, id, W, h, g, rstd, red, turn);
+    stage = stage == kStages - 1 ? 0 : stage + 1;
+  }
+  copy_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
 // Backward. A persistent grid: a CTA takes rows blockIdx.x, + gridDim.x, ...;
 // a thread keeps the same columns for every row, so its share of dgamma stays
-// in registers and leaves once, as a row of `partial`.
+// in registers and leaves once, as a row of `partial`. A thread's unit is 4
+// columns, 16 bytes of fp32 or 8 of bf16, so that every access of a warp is
+// contiguous whatever mixture of types the call has.
 
-template <typename T> __device__ __forceinline__ void load_n(const T *p, float (&v)[8]) {
-  if constexpr (Vec<T>::N == 8) {
-    load16<T>(p, v);
-  } else {
-    const float4 a = *reinterpret_cast<const float4 *>(p);
-    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
+template <typename T> struct Unit;
+template <> struct Unit<float> { using type = float4; };
+template <> struct Unit<__nv_bfloat16> { using type = uint2; };
+
+__device__ __forceinline__ void unpack4(const float4 &u, float (&v)[4]) {
+  v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
 }
-template <typename T> __device__ __forceinline__ void load_n(const T *p, float (&v)[4]) {
-  load16<T>(p, v);
+__device__ __forceinline__ void unpack4(const uint2 &u, float (&v)[4]) {
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
-template <typename T> __device__ __forceinline__ void store_n(T *p, const float (&v)[8]) {
-  if constexpr (Vec<T>::N == 8) {
-    store16<T>(p, v);
-  } else {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  }
+__device__ __forceinline__ void pack4(const float (&v)[4], float4 *out) {
+  *out = make_float4(v[0], v[1], v[2], v[3]);
 }
-template <typename T> __device__ __forceinline__ void store_n(T *p, const float (&v)[4]) {
-  store16<T>(p, v);
+__device__ __forceinline__ void pack4(const float (&v)[4], uint2 *out) {
+  uint2 u;
+  *reinterpret_cast<__nv_bfloat162 *>(&u.x) = __floats2bfloat162_rn(v[0], v[1]);
+  *reinterpret_cast<__nv_bfloat162 *>(&u.y) = __floats2bfloat162_rn(v[2], v[3]);
+  *out = u;
 }
 
-template <typename T, typename TY, typename TX, int NV>
-__global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) rmsnorm_bwd_kernel(RmsNormBwdArgs a) {
-  constexpr int N = Vec<T>::N;   // columns per thread and step
-  __shared__ float red[32];
-  const int nvec = a.d / N, W = blockDim.x;
-  const T *h = reinterpret_cast<const T *>(a.h);
-  const T *dh = reinterpret_cast<const T *>(a.dh);
-  const T *gamma = reinterpret_cast<const T *>(a.gamma);
-  const TY *dy = reinterpret_cast<const TY *>(a.dy);
-  TX *dx = reinterpret_cast<TX *>(a.dx);
-  float acc[NV][N];
+template <typename T, typename TY> constexpr int bwd_unit_bytes(bool dh) {
+  return 4 * (int)(sizeof(TY) + sizeof(T) * (dh ? 2 : 1));
+}
+
+// RING: the next kStages - 1 rows of dy, h and dh are copied to shared memory
+// in the background (rows of up to 16384 columns); otherwise they are read
+// from global memory twice, before and after the row's sum, the second time
+// from the caches.
+template <typename T, typename TY, typename TX, int NU, bool DH, bool RING>
+__global__ void __launch_bounds__(RING ? 512 : 1024) rmsnorm_bwd_kernel(RmsNormBwdArgs a) {
+  using UT = typename Unit<T>::type;
+  using UY = typename Unit<TY>::type;
+  using UX = typename Unit<TX>::type;
+  extern __shared__ uint4 ring[];   // per stage: dy [NU][W], h [NU][W], dh [NU][W]
+  __shared__ float red[2][32];
+  int turn = 0;
+  const int W = blockDim.x, id = threadIdx.x, nu = a.d / 4;
+  const UY *dy = reinterpret_cast<const UY *>(a.dy);
+  const UT *h = reinterpret_cast<const UT *>(a.h);
+  const UT *dh = reinterpret_cast<const UT *>(a.dh);
+  UX *dx = reinterpret_cast<UX *>(a.dx);
+  const int64_t step = gridDim.x;
+  const size_t stage_bytes = (size_t)NU * W * bwd_unit_bytes<T, TY>(DH);
+  auto dy_at = [&](int stage) {
+    return reinterpret_cast<UY *>(reinterpret_cast<char *>(ring) + stage * stage_bytes) + id;
+  };
+  auto h_at = [&](int stage) {
+    return reinterpret_cast<UT *>(reinterpret_cast<char *>(ring) + stage * stage_bytes +
+                                  (size_t)NU * W * sizeof(UY)) + id;
+  };
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < a.rows) {
+      UY *sy = dy_at(stage);
+      UT *sh = h_at(stage);
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NU; ++i) {
+        const int u = id + i * W;
+        if (u < nu) {
+          copy_async<sizeof(UY)>(sy + i * W, dy + row * nu + u);
+          copy_async<sizeof(UT)>(sh + i * W, h + row * nu + u);
+          if (DH) copy_async<sizeof(UT)>(sh + (NU + i) * W, dh + row * nu + u);
+        }
+      }
+    }
+    copy_commit();
+  };
+  if (RING) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) acc[i][k] = 0.0f;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    for (int s = 0; s < kStages - 1; ++s) fetch(blockIdx.x + s * step, s);
+  }
+  UT g[NU];
+  float acc[NU][4];
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int u = id + i * W;
+    g[i] = u < nu ? reinterpret_cast<const UT *>(a.gamma)[u] : UT{};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
+  }
+  int stage = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += step) {
     const float rstd = a.rstd[row];
-    float xh[NV][N], gy[NV][N];
+    float xh[NU][4], gy[NU][4];   // xhat and dy gamma
+    auto read = [&](int i, int u, float (&y4)[4]) {
+      unpack4(RING ? dy_at(stage)[i * W] : dy[row * nu + u], y4);
+      unpack4(RING ? h_at(stage)[i * W] : h[row * nu + u], xh[i]);
+      float gv[4];
+      unpack4(g[i], gv);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        xh[i][k] *= rstd;
+        gy[i][k] = y4[k] * gv[k];
+      }
+    };
+    if (RING) {
+      // the stage read one row ago is free: its values have gone into that row's dx
+      fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+      copy_wait<kStages - 1>();   // this row's group
+    }
     float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * W;
-      if (v < nvec) {
-        const int64_t at = row * a.d + (int64_t)v * N;
-        float gv[N];
-        load_n<T>(h + at, xh[i]);
-        load_n<TY>(dy + at, gy[i]);
-        load_n<T>(gamma + v * N, gv);
+    for (int i = 0; i < NU; ++i) {
+      const int u = id + i * W;
+      if (u < nu) {
+        float y4[4];
+        read(i, u, y4);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          xh[i][k] *= rstd;
-          acc[i][k] = fmaf(gy[i][k], xh[i][k], acc[i][k]);
-          gy[i][k] *= gv[k];
+        for (int k = 0; k < 4; ++k) {
+          acc[i][k] = fmaf(y4[k], xh[i][k], acc[i][k]);
           dot = fmaf(gy[i][k], xh[i][k], dot);
         }
       }
     }
-    const float m = __fdiv_rn(block_sum(dot, red), (float)a.d);
+    const float m = cta_reduce<false>(dot, red, turn) * a.inv_d;
+    UT dv[NU];
+    if (RING && DH) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * W;
-      if (v < nvec) {
-        const int64_t at = row * a.d + (int64_t)v * N;
-        float o[N];
+      for (int i = 0; i < NU; ++i) dv[i] = h_at(stage)[(NU + i) * W];
+    }
 #pragma unroll
-        for (int k = 0; k < N; ++k) o[k] = rstd * fmaf(-xh[i][k], m, gy[i][k]);
-        if (a.dh != nullptr) {
-          float dv[N];
-          load_n<T>(dh + at, dv);
-#pragma unroll
-          for (int k = 0; k < N; ++k) o[k] += dv[k];
+    for (int i = 0; i < NU; ++i) {
+      const int u = id + i * W;
+      if (u < nu) {
+        if (!RING) {
+          float y4[4];
+          read(i, u, y4);
+          if (DH) dv[i] = dh[row * nu + u];
         }
-        store_n<TX>(dx + at, o);
+        float o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = rstd * fmaf(-xh[i][k], m, gy[i][k]);
+        if (DH) {
+          float d4[4];
+          unpack4(dv[i], d4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[k] += d4[k];
+        }
+        pack4(o, dx + row * nu + u);
       }
     }
+    stage = stage == kStages - 1 ? 0 : stage + 1;
   }
+  if (RING) copy_wait<0>();
   float *part = a.partial + (int64_t)blockIdx.x * a.d;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = threadIdx.x + i * W;
-    if (v < nvec) store_n<float>(part + v * N, acc[i]);
+  for (int i = 0; i < NU; ++i) {
+    const int u = id + i * W;
+    if (u < nu) pack4(acc[i], reinterpret_cast<float4 *>(part) + u);
   }
 }
 
@@ -304,34 +474,93 @@ cudaError_t fwd(const RmsNormArgs &a, int threads, cudaStream_t s) {
 }
 
 constexpr int round32(int v) { return (v + 31) & ~31; }
+constexpr size_t kSmem = 227 * 1024;   // per CTA; the SM holds 228 KB, 1 KB of it per CTA reserved
+
+// CTAs of a persistent grid: those that fit the device at once, at most
+// `most`. The answer for the last device and size that a kernel was asked for
+// is kept (one word, so that threads may race for it): the two calls behind it
+// cost the host 1 us, half of what the launch does.
+template <typename K>
+cudaError_t resident(K k, std::atomic<uint64_t> &kept, int threads, size_t smem, int64_t most,
+                     int64_t *grid) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  // device (12 bits, + 1 so that no key is zero), threads (11), bytes (20), CTAs (21)
+  const uint64_t key = (uint64_t)(dev + 1) << 52 | (uint64_t)threads << 41 | (uint64_t)smem << 21;
+  uint64_t word = kept.load(std::memory_order_relaxed);
+  if ((word >> 21) != (key >> 21)) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem);
+    if (e != cudaSuccess) return e;
+    word = key | (uint64_t)(sm_count() * (per_sm > 0 ? per_sm : 1));
+    kept.store(word, std::memory_order_relaxed);
+  }
+  const int64_t fit = (int64_t)(word & ((1u << 21) - 1));
+  *grid = most < fit ? most : fit;
+  return cudaSuccess;
+}
+
+template <typename T, int NV, bool RES>
+cudaError_t fwd_ring(const RmsNormArgs &a, int threads, cudaStream_t s) {
+  auto k = rmsnorm_ring_kernel<T, NV, RES>;
+  const size_t smem = (size_t)kStages * (RES ? 2 : 1) * NV * threads * 16;
+  static std::atomic<uint64_t> kept{0};
+  int64_t grid = 0;
+  cudaError_t e = resident(k, kept, threads, smem, a.rows, &grid);
+  if (e != cudaSuccess) return e;
+  k<<<(unsigned)grid, threads, smem, s>>>(a);
+  return cudaGetLastError();
+}
 
 template <typename T> cudaError_t fwd_t(const RmsNormArgs &a, cudaStream_t s) {
   const int nvec = a.d / Vec<T>::N;
   if (nvec <= 32) return fwd<T, 1, true>(a, 128, s);
   if (nvec <= 64) return fwd<T, 2, true>(a, 128, s);
   if (nvec <= 128) return fwd<T, 4, true>(a, 128, s);
-  if (nvec <= 512) return fwd<T, 2, false>(a, round32((nvec + 1) / 2), s);
-  return fwd<T, 4, false>(a, round32((nvec + 3) / 4), s);
+  // a row for each SM at most: nothing to fetch ahead, and the most threads a row
+  if (nvec <= 1024 && a.rows <= sm_count()) return fwd<T, 1, false>(a, round32(nvec), s);
+  const bool res = a.residual != nullptr;
+  if (nvec <= 1024) {
+    const int threads = round32((nvec + 1) / 2);
+    return res ? fwd_ring<T, 2, true>(a, threads, s) : fwd_ring<T, 2, false>(a, threads, s);
+  }
+  const int threads = round32((nvec + 3) / 4);
+  if (threads <= 512 && (size_t)kStages * (res ? 2 : 1) * 4 * threads * 16 <= kSmem)
+    return res ? fwd_ring<T, 4, true>(a, threads, s) : fwd_ring<T, 4, false>(a, threads, s);
+  return fwd<T, 4, false>(a, threads, s);
 }
 
-template <typename T, typename TY, typename TX, int NV>
+template <typename T, typename TY, typename TX, int NU, bool DH, bool RING>
 cudaError_t bwd(const RmsNormBwdArgs &a, int threads, cudaStream_t s) {
-  int64_t grid = rmsnorm_bwd_max_partials(a.rows);
-  const int64_t want = (int64_t)sm_count() * 2;
-  if (grid > want) grid = want;
-  rmsnorm_bwd_kernel<T, TY, TX, NV><<<(unsigned)grid, threads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  auto k = rmsnorm_bwd_kernel<T, TY, TX, NU, DH, RING>;
+  const size_t smem = RING ? (size_t)kStages * NU * threads * bwd_unit_bytes<T, TY>(DH) : 0;
+  static std::atomic<uint64_t> kept{0};
+  int64_t grid = 0;
+  cudaError_t e = resident(k, kept, threads, smem, rmsnorm_bwd_max_partials(a.rows), &grid);
+  if (e != cudaSuccess) return e;
+  k<<<(unsigned)grid, threads, smem, s>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_pdl(dgamma_kernel, dim3((a.d + 31) / 32), dim3(1024), 0, s, a.partial, (int)grid, a.d,
                     a.dgamma);
 }
 
-template <typename T, typename TY, typename TX>
+template <typename T, typename TY, typename TX, bool DH>
 cudaError_t bwd_t(const RmsNormBwdArgs &a, cudaStream_t s) {
-  const int nvec = a.d / Vec<T>::N;
-  if (nvec <= 256) return bwd<T, TY, TX, 1>(a, round32(nvec), s);
-  if (nvec <= 1024) return bwd<T, TY, TX, 2>(a, round32((nvec + 1) / 2), s);
-  return bwd<T, TY, TX, 4>(a, round32((nvec + 3) / 4), s);
+  const int nu = a.d / 4;
+  if (nu <= 32) return bwd<T, TY, TX, 1, DH, true>(a, 32, s);
+  const int threads = round32((nu + 3) / 4);
+  if (threads <= 512 && (size_t)kStages * 4 * threads * bwd_unit_bytes<T, TY>(DH) <= kSmem)
+    return bwd<T, TY, TX, 4, DH, true>(a, threads, s);
+  return bwd<T, TY, TX, 8, DH, false>(a, round32((nu + 7) / 8), s);
+}
+
+template <typename T, typename TY, typename TX>
+cudaError_t bwd_dh(const RmsNormBwdArgs &a, cudaStream_t s) {
+  return a.dh != nullptr ? bwd_t<T, TY, TX, true>(a, s) : bwd_t<T, TY, TX, false>(a, s);
 }
 
 }  // namespace
@@ -339,16 +568,23 @@ cudaError_t bwd_t(const RmsNormBwdArgs &a, cudaStream_t s) {
 // Rows of `partial` that the workspace holds, whatever the device's SM count.
 int64_t rmsnorm_bwd_max_partials(int64_t rows) { return rows < 1024 ? rows : 1024; }
 
-cudaError_t launch_rmsnorm(const RmsNormArgs &a, cudaStream_t s) {
+cudaError_t launch_rmsnorm(const RmsNormArgs &args, cudaStream_t s) {
+  RmsNormArgs a = args;
+  a.inv_d = 1.0f / (float)a.d;
+  a.ng = a.group > 0 ? (a.d + a.group - 1) / a.group : 1;
+  a.group_shift = 0;
+  while ((a.dtype == MOE_BF16 ? 8 : 4) << a.group_shift < a.group) ++a.group_shift;
   return a.dtype == MOE_BF16 ? fwd_t<__nv_bfloat16>(a, s) : fwd_t<float>(a, s);
 }
 
-cudaError_t launch_rmsnorm_bwd(const RmsNormBwdArgs &a, cudaStream_t s) {
+cudaError_t launch_rmsnorm_bwd(const RmsNormBwdArgs &args, cudaStream_t s) {
   using B = __nv_bfloat16;
-  if (a.dtype == MOE_F32) return bwd_t<float, float, float>(a, s);
+  RmsNormBwdArgs a = args;
+  a.inv_d = 1.0f / (float)a.d;
+  if (a.dtype == MOE_F32) return bwd_dh<float, float, float>(a, s);
   if (a.dy_dtype == MOE_F32)
-    return a.dx_dtype == MOE_F32 ? bwd_t<B, float, float>(a, s) : bwd_t<B, float, B>(a, s);
-  return a.dx_dtype == MOE_F32 ? bwd_t<B, B, float>(a, s) : bwd_t<B, B, B>(a, s);
+    return a.dx_dtype == MOE_F32 ? bwd_dh<B, float, float>(a, s) : bwd_dh<B, float, B>(a, s);
+  return a.dx_dtype == MOE_F32 ? bwd_dh<B, B, float>(a, s) : bwd_dh<B, B, B>(a, s);
 }
 
 }  // namespace moe
