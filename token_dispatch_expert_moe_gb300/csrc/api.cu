@@ -603,7 +603,7 @@ static moe_status_t list_check(int32_t n, const moe_tensor_t *list) {
   if (n < 0 || (n > 0 && !list)) return MOE_ERR_INVALID_ARG;
   for (int32_t i = 0; i < n; ++i) {
     const moe_tensor_t &t = list[i];
-    if (t.numel < 0 || t.numel >= (int64_t(1) << 56) || !dtype_ok(t.dtype)) return MOE_ERR_INVALID_ARG;
+    if (t.numel < 0 || t.numel >= (int64_t(1) << 42) || !dtype_ok(t.dtype)) return MOE_ERR_INVALID_ARG;
     if (t.numel > 0 && (!t.data || reinterpret_cast<uintptr_t>(t.data) % size_of(t.dtype) != 0))
       return MOE_ERR_INVALID_ARG;
   }

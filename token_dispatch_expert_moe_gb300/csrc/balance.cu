@@ -13,65 +13,92 @@
 //   dl_te = (dloss / n) p_te (a_je - sum_i p_ti a_ji):
 // nothing cancels when the load is nearly even. Sums are fp32, counts are
 // integers, every order is fixed.
+#include <cooperative_groups.h>
+
 #include "launch.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;      // counting pass
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512, kJoinCtas = 8;   // one cluster
 constexpr int kBwdThreads = 256;
-// CTAs of the counting pass when sub-sequences are cut into chunks.
+
+// How the counting pass cuts the tokens. A sub-sequence that one CTA gets
+// through in a few tokens a thread stays whole and needs no joining (a join
+// adds 3 to 4 us); others are cut into chunks, two CTAs for each of 152 SMs
+// in all.
+constexpr int kMaxThreads = 512;
+constexpr int kFewTokens = 8;            // a thread, of a whole sub-sequence
+constexpr int kChunkThreads = 256;
 constexpr int64_t kTargetCtas = 304;
 
 struct Split {
   int64_t chunks, len;   // chunks per sub-sequence and tokens per chunk
+  int threads;
 };
 Split split_of(int64_t T, int64_t S, int lanes) {
   const int64_t n_sub = (T + S - 1) / S;
-  const int64_t step = kThreads / lanes;   // tokens a CTA takes at once
+  Split r;
+  if (S * lanes <= kMaxThreads * kFewTokens || n_sub >= kTargetCtas) {
+    r.chunks = 1;
+    r.len = S;
+    // few CTAs: as many threads as have a token; many: fewer, longer ones
+    const int64_t want = n_sub <= 152 ? S * lanes : (S * lanes + kFewTokens - 1) / kFewTokens;
+    r.threads = want <= 128 ? 128 : want <= 256 ? 256 : kMaxThreads;
+    return r;
+  }
+  const int64_t step = kChunkThreads / lanes;   // tokens a CTA takes at once
   int64_t chunks = kTargetCtas / n_sub;
   const int64_t most = (S + step - 1) / step;
   if (chunks > most) chunks = most;
   if (chunks < 1) chunks = 1;
-  Split r;
   r.len = (S + chunks - 1) / chunks;
   r.chunks = (S + r.len - 1) / r.len;
+  r.threads = kChunkThreads;
   return r;
 }
 
 // A token's experts lie over L lanes, V quads (4 consecutive experts) a lane:
 // quad v of lane `sub` starts at expert 4 (sub + v L), so that the lanes read
 // consecutive 16 bytes. At most 4 lanes: the row's maximum and sum take two
-// shuffles each, and a lane's 16 exponentials overlap. (16 lanes with one quad
-// each, four shuffles: 55.7 us for 262144 x 64 against the figure below.)
-// The softmax of a token's logits: p[4 v + i] of expert 4 (sub + v L) + i,
-// zero past E, for a token that is not live, and where all logits are -inf.
+// shuffles each, and a lane's 16 exponentials overlap (262144 x 64, counting
+// pass: LANES4 us; 16 lanes of one quad, four shuffles, 50 us).
+// A token's logits, l[4 v + i] of expert 4 (sub + v L) + i: -inf past E, and
+// throughout where `in` is false (nothing is read then).
 template <int L, int V>
-__device__ __forceinline__ void softmax_quads(const float *l, int sub, int E, bool live,
-                                              float (&p)[4 * V]) {
+__device__ __forceinline__ void load_quads(const float *row, int sub, int E, bool in, float (&l)[4 * V]) {
 #pragma unroll
-  for (int i = 0; i < 4 * V; ++i) p[i] = -INFINITY;
-  if (live) {
-    if ((E & 3) == 0) {
+  for (int i = 0; i < 4 * V; ++i) l[i] = -INFINITY;
+  if (!in) return;
+  if ((E & 3) == 0) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = 4 * (sub + v * L);
-        if (e < E) {
-          const float4 q = *reinterpret_cast<const float4 *>(l + e);
-          p[4 * v] = q.x; p[4 * v + 1] = q.y; p[4 * v + 2] = q.z; p[4 * v + 3] = q.w;
-        }
+    for (int v = 0; v < V; ++v) {
+      const int e = 4 * (sub + v * L);
+      if (e < E) {
+        const float4 q = *reinterpret_cast<const float4 *>(row + e);
+        l[4 * v] = q.x; l[4 * v + 1] = q.y; l[4 * v + 2] = q.z; l[4 * v + 3] = q.w;
       }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = 4 * (sub + v * L) + i;
-          if (e < E) p[4 * v + i] = l[e];
-        }
     }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = 4 * (sub + v * L) + i;
+        if (e < E) l[4 * v + i] = row[e];
+      }
   }
+}
+
+__device__ __forceinline__ float exp2_of(float v) {   // within 2 ulp; below 2^-126: 0
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// The softmax numerators in place of the token's logits; returns the factor
+// that makes them probabilities. All zero where every logit is -inf.
+template <int L, int V> __device__ __forceinline__ float softmax_quads(float (&p)[4 * V]) {
   float m = p[0];
 #pragma unroll
   for (int i = 1; i < 4 * V; ++i) m = fmaxf(m, p[i]);
@@ -81,22 +108,21 @@ __device__ __forceinline__ void softmax_quads(const float *l, int sub, int E, bo
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4 * V; ++i) {
-    p[i] = expf(p[i] - m);
+    // the distance first: lowest values and far logits neither overflow nor
+    // cancel; two more roundings of it put |l - m| 2^-23 on p
+    p[i] = exp2_of((p[i] - m) * 1.4426950408889634f);
     s += p[i];
   }
 #pragma unroll
   for (int o = L >> 1; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const float r = s == 0.0f ? 0.0f : __frcp_rn(s);
-#pragma unroll
-  for (int i = 0; i < 4 * V; ++i) p[i] *= r;
+  return s == 0.0f ? 0.0f : __frcp_rn(s);
 }
 
-// The workspace: partial sums per chunk of tokens, the loss's terms, and the
-// number of join CTAs that are done.
+// The workspace: partial sums per chunk of tokens, and the loss's term of each
+// sub-sequence that is not cut.
 struct Partials {
-  uint32_t *done;
   int32_t *tokens;   // [chunks in all]: unmasked tokens
-  float *term;       // [terms]
+  float *term;       // [n_sub]
   float *prob;       // [chunks in all, E]: sums of p
   int32_t *count;    // [chunks in all, E]
 };
@@ -114,13 +140,19 @@ __device__ __forceinline__ float finish(const BalanceArgs &a, int64_t j, int e, 
   return (float)c * mean;
 }
 
+__device__ __forceinline__ void finish_loss(const BalanceArgs &a, float terms, uint32_t n) {
+  const float inv = n > 0 ? __frcp_rn((float)n) : 0.0f;
+  a.loss[0] = a.alpha * ((float)a.E / (float)a.K) * terms * inv;
+  a.coef[a.n_sub * a.E] = inv;
+}
+
 template <int L, int V>
-__global__ void __launch_bounds__(kThreads) balance_count_kernel(BalanceArgs a, Partials w,
+__global__ void __launch_bounds__(kMaxThreads) balance_count_kernel(BalanceArgs a, Partials w,
                                                                  int64_t chunks, int64_t len) {
   __shared__ int32_t cnt[64];
   __shared__ int32_t tok;
-  __shared__ float red[kThreads / 32][64];
-  constexpr int kPer = kThreads / L;
+  __shared__ float red[kMaxThreads / 32][64];
+  const int kPer = blockDim.x / L;
   const int64_t j = blockIdx.x / chunks, c = blockIdx.x - j * chunks;
   const int64_t lo = j * a.S + c * len;
   const int64_t hi = min(min(a.T, (j + 1) * a.S), lo + len);
@@ -128,30 +160,47 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(BalanceArgs a, 
   const int E = a.E, K = a.K;
   if (threadIdx.x < 64) cnt[threadIdx.x] = 0;
   if (threadIdx.x == 0) tok = 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *w.done = 0;
+  pdl_trigger();   // the join may take its place: it waits for this grid's end
   __syncthreads();
-  float acc[4 * V];
+  float acc[4 * V], next[4 * V];
 #pragma unroll
   for (int i = 0; i < 4 * V; ++i) acc[i] = 0.0f;
   int mine = 0;
-  for (int64_t t0 = lo; t0 < hi; t0 += kPer) {   // the same trips for every thread
-    const int64_t t = t0 + slot;
-    const bool live = t < hi && (a.mask == nullptr || a.mask[t] != 0);
-    int e[8 / L];
+  // The next token's logits, indices and mask are on their way while one is
+  // worked on. A masked token's logits are read and thrown away.
+  constexpr int kSlots = 8 / L;   // the lanes share out the token's K slots
+  int idx[kSlots], keep = 0;
+  auto fetch = [&](int64_t t) {
+    const bool in = t < hi;
+    load_quads<L, V>(a.logits + t * E, sub, E, in, next);
+    keep = in && (a.mask == nullptr || a.mask[t] != 0);
 #pragma unroll
-    for (int i = 0; i < 8 / L; ++i) {   // the lanes share out the token's K slots
+    for (int i = 0; i < kSlots; ++i) {
       const int k = sub + i * L;
-      e[i] = live && k < K ? a.topk_idx[t * K + k] : -2;
+      idx[i] = in && k < K ? a.topk_idx[t * K + k] : 0;
     }
+  };
+  fetch(lo + slot);
+  for (int64_t t0 = lo; t0 < hi; t0 += kPer) {   // the same trips for every thread
     float p[4 * V];
-    softmax_quads<L, V>(a.logits + t * E, sub, E, live, p);
+    int e[kSlots];
+    const bool live = keep != 0;
 #pragma unroll
-    for (int i = 0; i < 4 * V; ++i) acc[i] += p[i];
-    if (live && sub == 0) ++mine;
+    for (int i = 0; i < 4 * V; ++i) p[i] = next[i];
 #pragma unroll
-    for (int i = 0; i < 8 / L; ++i) {
-      if (e[i] >= 0 && e[i] < E) atomicAdd(&cnt[e[i]], 1);
-      else if (live && sub + i * L < K) report(a.status, MOE_ERR_DEVICE, kInfoExpertRange);
+    for (int i = 0; i < kSlots; ++i) e[i] = idx[i];
+    fetch(t0 + kPer + slot);
+    const float r = softmax_quads<L, V>(p);
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 4 * V; ++i) acc[i] = fmaf(p[i], r, acc[i]);
+      if (sub == 0) ++mine;
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        if (sub + i * L >= K) continue;
+        if (e[i] >= 0 && e[i] < E) atomicAdd(&cnt[e[i]], 1);
+        else report(a.status, MOE_ERR_DEVICE, kInfoExpertRange);
+      }
     }
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
@@ -165,10 +214,9 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(BalanceArgs a, 
 #pragma unroll
     for (int i = 0; i < 4 * V; ++i) red[warp][4 * (lane + (i / 4) * L) + i % 4] = acc[i];
   __syncthreads();
-  pdl_trigger();
   float s = 0.0f;
   if (threadIdx.x < E)
-    for (int q = 0; q < kThreads / 32; ++q) s += red[q][threadIdx.x];
+    for (int q = 0; q < (int)(blockDim.x >> 5); ++q) s += red[q][threadIdx.x];
   if (threadIdx.x == 0) w.tokens[blockIdx.x] = tok;
   if (chunks > 1) {
     if (threadIdx.x < E) {
@@ -180,75 +228,89 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(BalanceArgs a, 
   float term = 0.0f;
   if (threadIdx.x < E) term = finish(a, j, threadIdx.x, s, cnt[threadIdx.x], tok);
   term = block_sum(term, &red[0][0]);
-  if (threadIdx.x == 0) w.term[j] = term;
+  if (threadIdx.x != 0) return;
+  if (a.n_sub == 1) finish_loss(a, term, (uint32_t)tok);   // this CTA saw every token
+  else w.term[j] = term;
 }
 
-// Joins the chunks of the sub-sequences (chunks > 1): a CTA takes 16 experts
-// of one sub-sequence, 16 threads an expert, and adds their chunks in a fixed
-// order. The CTA that finishes last (one CTA alone, when there is nothing to
-// join) adds the terms and the token counts, in order again.
-constexpr int kJoinExperts = 16, kJoinSlices = kJoinThreads / kJoinExperts;
-
-__global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs a, Partials w,
-                                                                    int64_t chunks, int64_t terms) {
-  __shared__ float probs[kJoinSlices][kJoinExperts];
-  __shared__ int32_t counts[kJoinSlices][kJoinExperts], tok[kJoinSlices][kJoinExperts];
+// Joins the chunks of the sub-sequences (chunks > 1), then the sub-sequences'
+// terms and token counts. One cluster of CTAs, so that the last step is an
+// exchange of shared memory and not another trip through global memory: every
+// such trip is 0.8 us, and this kernel is nothing else. The (sub-sequence,
+// expert) pairs lie over the cluster; `slices` threads share out the chunks of
+// a pair. Everything is added in a fixed order.
+__global__ void __cluster_dims__(kJoinCtas, 1, 1) __launch_bounds__(kJoinThreads)
+balance_join_kernel(BalanceArgs a, Partials w, int64_t chunks, int slices) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ float probs[kJoinThreads];
+  __shared__ int32_t counts[kJoinThreads], toks[kJoinThreads];
   __shared__ float red[32];
-  __shared__ uint32_t total, before;
-  pdl_wait();
-  const int E = a.E;
-  const int64_t groups = (E + kJoinExperts - 1) / kJoinExperts;
-  if (chunks > 1) {
-    const int64_t j = blockIdx.x / groups;
-    const int x = threadIdx.x % kJoinExperts, slice = threadIdx.x / kJoinExperts;
-    const int e = (int)(blockIdx.x - j * groups) * kJoinExperts + x;
-    float prob = 0.0f;
-    int c = 0, n_j = 0;
-    if (e < E) {
-#pragma unroll 8
-      for (int64_t q = j * chunks + slice; q < (j + 1) * chunks; q += kJoinSlices) {
-        prob += w.prob[q * E + e];
-        c += w.count[q * E + e];
-        n_j += w.tokens[q];
-      }
-    }
-    probs[slice][x] = prob;
-    counts[slice][x] = c;
-    tok[slice][x] = n_j;
-    __syncthreads();
-    float term = 0.0f;
-    if (slice == 0) {
-      for (int q = 1; q < kJoinSlices; ++q) {
-        prob += probs[q][x];
-        c += counts[q][x];
-        n_j += tok[q][x];
-      }
-      if (e < E) term = finish(a, j, e, prob, c, n_j);
-    }
-    term = block_sum(term, red);
-    if (threadIdx.x == 0) {
-      w.term[blockIdx.x] = term;
-      __threadfence();
-      before = atomicAdd(w.done, 1u);
-    }
-    __syncthreads();
-    if (before != gridDim.x - 1) return;   // the same in every thread
-    __threadfence();
-  }
+  __shared__ uint32_t total;
+  __shared__ float all_terms[kJoinCtas];
+  __shared__ uint32_t all_tokens[kJoinCtas];
   if (threadIdx.x == 0) total = 0;
+  const int rank = (int)cluster.block_rank();
+  const int E = a.E;
+  pdl_wait();
   __syncthreads();
-  float term = 0.0f;
   uint32_t n = 0;   // at most T < 2^31
-  const int64_t all = chunks * a.n_sub;
-  for (int64_t i = threadIdx.x; i < terms; i += kJoinThreads) term += __ldcg(w.term + i);
-  for (int64_t i = threadIdx.x; i < all; i += kJoinThreads) n += w.tokens[i];
+  for (int64_t i = rank * kJoinThreads + threadIdx.x; i < chunks * a.n_sub; i += kJoinCtas * kJoinThreads)
+    n += w.tokens[i];
+  float term = 0.0f;
+  if (chunks > 1) {
+    const int per = kJoinThreads / slices;   // pairs of a CTA at once
+    const int x = threadIdx.x % per, slice = threadIdx.x / per;
+    const int64_t pairs = a.n_sub * E;
+    for (int64_t p0 = (int64_t)rank * per; p0 < pairs; p0 += kJoinCtas * per) {   // the same in every thread
+      const int64_t pair = p0 + x;
+      const int64_t j = pair / E;
+      const int e = (int)(pair - j * E);
+      float prob = 0.0f;
+      int c = 0, n_j = 0;
+      if (pair < pairs) {
+#pragma unroll 8
+        for (int q = slice; q < (int)chunks; q += slices) {
+          const int64_t row = j * chunks + q;
+          prob += w.prob[row * E + e];
+          c += w.count[row * E + e];
+          n_j += w.tokens[row];
+        }
+      }
+      probs[threadIdx.x] = prob;
+      counts[threadIdx.x] = c;
+      toks[threadIdx.x] = n_j;
+      __syncthreads();
+      if (slice == 0 && pair < pairs) {
+        for (int q = 1; q < slices; ++q) {
+          prob += probs[q * per + x];
+          c += counts[q * per + x];
+          n_j += toks[q * per + x];
+        }
+        term += finish(a, j, e, prob, c, n_j);
+      }
+      __syncthreads();
+    }
+  } else {
+    for (int64_t i = rank * kJoinThreads + threadIdx.x; i < a.n_sub; i += kJoinCtas * kJoinThreads)
+      term += w.term[i];
+  }
   n = __reduce_add_sync(0xffffffffu, n);
-  if ((threadIdx.x & 31) == 0) atomicAdd(&total, n);   // whole numbers: the order does not matter
+  if ((threadIdx.x & 31) == 0 && n > 0) atomicAdd(&total, n);   // whole numbers: the order does not matter
   term = block_sum(term, red);
   if (threadIdx.x == 0) {
-    const float inv = total > 0 ? (float)(1.0 / (double)total) : 0.0f;
-    a.loss[0] = a.alpha * ((float)E / (float)a.K) * term * inv;
-    a.coef[a.n_sub * E] = inv;
+    *cluster.map_shared_rank(&all_terms[rank], 0) = term;
+    *cluster.map_shared_rank(&all_tokens[rank], 0) = total;
+  }
+  cluster.sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    term = 0.0f;
+    n = 0;
+    for (int r = 0; r < kJoinCtas; ++r) {
+      term += all_terms[r];
+      n += all_tokens[r];
+    }
+    finish_loss(a, term, n);
   }
 }
 
@@ -267,9 +329,13 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(BalanceArgs a)
     const int e = 4 * (sub + (i / 4) * L) + i % 4;
     w[i] = e < E ? coef[e] : 0.0f;
   }
-  softmax_quads<L, V>(a.logits + t * E, sub, E, live, p);
+  load_quads<L, V>(a.logits + t * E, sub, E, live, p);
+  const float r = softmax_quads<L, V>(p);
 #pragma unroll
-  for (int i = 0; i < 4 * V; ++i) dot = fmaf(p[i], w[i], dot);
+  for (int i = 0; i < 4 * V; ++i) {
+    p[i] *= r;
+    dot = fmaf(p[i], w[i], dot);
+  }
 #pragma unroll
   for (int o = L >> 1; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
   if (!in) return;
@@ -297,17 +363,15 @@ constexpr size_t align256_(size_t v) { return (v + 255) & ~size_t(255); }
 int lanes_of(int E) { return E <= 4 ? 1 : E <= 8 ? 2 : 4; }
 
 struct Regions {
-  size_t tokens, term, prob, count, total;
+  size_t term, prob, count, total;   // tokens come first
 };
 Regions regions_of(int64_t T, int64_t S, int E) {
   const Split sp = split_of(T, S, lanes_of(E));
   const int64_t n_sub = (T + S - 1) / S, all = sp.chunks * n_sub;
-  const int64_t terms = sp.chunks > 1 ? n_sub * ((E + kJoinExperts - 1) / kJoinExperts) : n_sub;
   const size_t rows = sp.chunks > 1 ? align256_((size_t)all * E * 4) : 0;
   Regions r{};
-  r.tokens = 256;
-  r.term = r.tokens + align256_((size_t)all * 4);
-  r.prob = r.term + align256_((size_t)terms * 4);
+  r.term = align256_((size_t)all * 4);
+  r.prob = r.term + align256_((size_t)n_sub * 4);
   r.count = r.prob + rows;
   r.total = r.count + rows;
   return r;
@@ -318,18 +382,18 @@ template <int L, int V> cudaError_t fwd(const BalanceArgs &a, cudaStream_t s) {
   const Regions r = regions_of(a.T, a.S, a.E);
   char *p = static_cast<char *>(a.partial);
   Partials w{};
-  w.done = reinterpret_cast<uint32_t *>(p);
-  w.tokens = reinterpret_cast<int32_t *>(p + r.tokens);
+  w.tokens = reinterpret_cast<int32_t *>(p);
   w.term = reinterpret_cast<float *>(p + r.term);
   w.prob = reinterpret_cast<float *>(p + r.prob);
   w.count = reinterpret_cast<int32_t *>(p + r.count);
-  balance_count_kernel<L, V><<<(unsigned)(sp.chunks * a.n_sub), kThreads, 0, s>>>(a, w, sp.chunks, sp.len);
+  balance_count_kernel<L, V><<<(unsigned)(sp.chunks * a.n_sub), sp.threads, 0, s>>>(a, w, sp.chunks, sp.len);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int64_t joins = sp.chunks > 1 ? a.n_sub * ((a.E + kJoinExperts - 1) / kJoinExperts) : 1;
-  const int64_t terms = sp.chunks > 1 ? joins : a.n_sub;
-  return launch_pdl(balance_join_kernel, dim3((unsigned)joins), dim3(kJoinThreads), 0, s, a, w,
-                    sp.chunks, terms);
+  if (e != cudaSuccess || sp.chunks * a.n_sub == 1) return e;
+  // threads a pair: as many as fill the cluster, no more than chunks
+  int slices = 1;
+  while (2 * slices * a.n_sub * a.E <= kJoinCtas * kJoinThreads && 2 * slices <= sp.chunks && slices < 32)
+    slices *= 2;
+  return launch_pdl(balance_join_kernel, dim3(kJoinCtas), dim3(kJoinThreads), 0, s, a, w, sp.chunks, slices);
 }
 
 template <int L, int V> cudaError_t bwd(const BalanceArgs &a, cudaStream_t s) {

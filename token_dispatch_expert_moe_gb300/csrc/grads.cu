@@ -3,8 +3,8 @@
 //   norm = sqrt(sum over tensors and elements of g^2)
 //   coef = max_norm / norm if max_norm < norm < inf, else 1;  out = g coef
 //
-// Tensors are cut into chunks of kChunkBytes; a persistent grid takes chunk
-// after chunk, so a few huge tensors and many tiny ones load it alike. The
+// Tensors are cut into chunks of 32 KB (norm) or 16 KB (clipping), so a few
+// huge tensors and many tiny ones load the grid alike. The
 // squares of a thread's share of a chunk are added in fp32 and carried on in
 // fp64; where that fp32 sum leaves the safe range (gradients above 1e18 or all
 // below 1e-15) the share is summed again in fp64, so the norm is right
@@ -15,8 +15,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 8;                               // 16-byte vectors per thread and chunk
-constexpr int64_t kChunkVecs = kThreads * kUnroll;       // 32 KB
+constexpr int kNormUnroll = 8;   // 16-byte vectors per thread and chunk: chunks of 32 KB
+constexpr int kClipUnroll = 4;   // 16 KB
 constexpr int kBatch = 96;                               // tensors per launch
 
 // Tensors of one launch, passed by value: nothing of the caller's host arrays
@@ -25,9 +25,10 @@ struct Batch {
   const void *in[kBatch];
   void *out[kBatch];
   int64_t numel[kBatch];
-  int64_t first_chunk[kBatch + 1];
+  int first_chunk[kBatch + 1];
   uint8_t bf16[kBatch];
   int n;
+  bool in_place;   // out == in for all of them
 };
 
 // A tensor's 16-byte vectors: those that its bytes touch, the first and the
@@ -38,8 +39,9 @@ __host__ __device__ inline int64_t vectors_of(const void *p, int64_t numel, int 
   return (head + numel * size + 15) / 16;
 }
 
-__device__ __forceinline__ int tensor_of(const Batch &b, int64_t chunk) {
-  int lo = 0, hi = b.n - 1;   // the last tensor whose first chunk is <= chunk
+// The last tensor whose first chunk is not after `chunk`.
+__device__ __forceinline__ int tensor_of(const Batch &b, int chunk) {
+  int lo = 0, hi = b.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (b.first_chunk[mid] <= chunk) lo = mid;
@@ -66,6 +68,7 @@ __device__ __forceinline__ uint4 load_vec(const T *p, int64_t numel, int64_t v) 
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const T *p, int64_t numel, int64_t v0) {
   constexpr int N = Vec<T>::N;
+  constexpr int kUnroll = kNormUnroll;
   const int64_t nvec = vectors_of(p, numel, sizeof(T));
   uint4 u[kUnroll];
 #pragma unroll
@@ -117,9 +120,10 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
   pdl_trigger();
   double s = 0.0;
   const int64_t chunks = b.first_chunk[b.n];
+  int i = tensor_of(b, blockIdx.x);
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = tensor_of(b, c);
-    const int64_t v0 = (c - b.first_chunk[i]) * kChunkVecs;
+    while (b.first_chunk[i + 1] <= c) ++i;
+    const int64_t v0 = (c - b.first_chunk[i]) * (kThreads * kNormUnroll);
     s += b.bf16[i] ? chunk_squares(static_cast<const __nv_bfloat16 *>(b.in[i]), b.numel[i], v0)
                    : chunk_squares(static_cast<const float *>(b.in[i]), b.numel[i], v0);
   }
@@ -145,6 +149,7 @@ template <typename T>
 __device__ __forceinline__ void scale_chunk(const T *in, T *out, int64_t numel, int64_t v0,
                                             float coef) {
   constexpr int N = Vec<T>::N;
+  constexpr int kUnroll = kClipUnroll;
   const int64_t head = (int64_t)((reinterpret_cast<uintptr_t>(in) & 15u) / sizeof(T));
   const int64_t nvec = vectors_of(in, numel, sizeof(T));
   // both sides at the same place within their 16 bytes: whole vectors move
@@ -176,17 +181,18 @@ __device__ __forceinline__ void scale_chunk(const T *in, T *out, int64_t numel, 
 
 __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Batch b,
                                                         const float *norm, float max_norm,
-                                                        float *coef_out) {
+                                                        float *coef_out, int per) {
   pdl_wait();
   pdl_trigger();
   const float coef = coef_of(norm[0], max_norm);
   if (coef_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) coef_out[0] = coef;
-  const int64_t chunks = b.first_chunk[b.n];
-  // last chunk first: the norm's pass has left the tail in L2
-  for (int64_t c = chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
-    const int i = tensor_of(b, c);
-    const int64_t v0 = (c - b.first_chunk[i]) * kChunkVecs;
-    if (coef == 1.0f && b.in[i] == b.out[i]) continue;
+  if (coef == 1.0f && b.in_place) return;
+  // last chunks first: the norm's pass has left the tail in L2
+  const int hi = b.first_chunk[b.n] - 1 - (int)blockIdx.x * per;
+  int i = tensor_of(b, hi);
+  for (int c = hi; c >= 0 && c > hi - per; --c) {
+    while (b.first_chunk[i] > c) --i;
+    const int64_t v0 = (int64_t)(c - b.first_chunk[i]) * (kThreads * kClipUnroll);
     if (b.bf16[i])
       scale_chunk(static_cast<const __nv_bfloat16 *>(b.in[i]), static_cast<__nv_bfloat16 *>(b.out[i]),
                   b.numel[i], v0, coef);
@@ -196,43 +202,47 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
   }
 }
 
-// Tensors [at, ...) of the list as a batch; returns the first that is left.
-int fill(Batch &b, int at, int n, const moe_tensor_t *in, const moe_tensor_t *out) {
+// Tensors [at, ...) of the list as a batch; returns the first that is left. A
+// batch ends before its chunks pass 2^30 (16 TB), so that 32 bits count them;
+// list_check has seen to it that one tensor alone does not.
+int fill(Batch &b, int at, int n, const moe_tensor_t *in, const moe_tensor_t *out, int chunk_vecs) {
   b.n = 0;
+  b.in_place = true;
   int64_t chunks = 0;
   for (; at < n && b.n < kBatch; ++at) {
     if (in[at].numel == 0) continue;
+    const bool bf16 = in[at].dtype == MOE_BF16;
+    const int64_t nvec = vectors_of(in[at].data, in[at].numel, bf16 ? 2 : 4);
+    const int64_t more = (nvec + chunk_vecs - 1) / chunk_vecs;
+    if (b.n > 0 && chunks + more > (int64_t(1) << 30)) break;
     const int i = b.n++;
     b.in[i] = in[at].data;
     b.out[i] = out != nullptr ? out[at].data : in[at].data;
+    if (b.out[i] != b.in[i]) b.in_place = false;
     b.numel[i] = in[at].numel;
-    b.bf16[i] = in[at].dtype == MOE_BF16;
-    b.first_chunk[i] = chunks;
-    const int64_t nvec = vectors_of(b.in[i], b.numel[i], b.bf16[i] ? 2 : 4);
-    chunks += (nvec + kChunkVecs - 1) / kChunkVecs;
+    b.bf16[i] = bf16;
+    b.first_chunk[i] = (int)chunks;
+    chunks += more;
   }
-  b.first_chunk[b.n] = chunks;
+  b.first_chunk[b.n] = (int)chunks;
   return at;
-}
-
-int grid_of(const Batch &b, int ctas) {
-  const int64_t chunks = b.first_chunk[b.n];
-  return (int)(chunks < ctas ? (chunks > 0 ? chunks : 1) : ctas);
 }
 
 }  // namespace
 
 cudaError_t launch_grad_norm(int n, const moe_tensor_t *grads, float *norm, double *partial,
                              cudaStream_t s) {
-  int ctas = sm_count() * 8;
+  // a persistent grid of what the registers let an SM hold (7.5 GB: 1015 us,
+  // 7.41 TB/s; 4 CTAs an SM, so a second wave, 1240 us)
+  int ctas = sm_count() * 3;
   if (ctas > kMaxNormPartials) ctas = kMaxNormPartials;
   int grid = 0;   // CTAs of every batch, so partials that hold a sum
   Batch b;
   for (int at = 0; at < n;) {
-    at = fill(b, at, n, grads, nullptr);
+    at = fill(b, at, n, grads, nullptr, kThreads * kNormUnroll);
     if (b.n == 0) break;
     const bool first = grid == 0;
-    if (first) grid = at < n ? ctas : grid_of(b, ctas);
+    if (first) grid = at == n && b.first_chunk[b.n] < ctas ? b.first_chunk[b.n] : ctas;
     cudaError_t e = launch_pdl(squares_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, b,
                                partial, first ? 0 : 1);   // later batches add theirs
     if (e != cudaSuccess) return e;
@@ -242,15 +252,22 @@ cudaError_t launch_grad_norm(int n, const moe_tensor_t *grads, float *norm, doub
 
 cudaError_t launch_grad_clip(int n, const moe_tensor_t *grads, const moe_tensor_t *out,
                              const float *norm, float max_norm, float *coef, cudaStream_t s) {
-  const int ctas = sm_count() * 8;
   Batch b;
   int at = 0;
   bool first = true;
   do {
-    at = fill(b, at, n, grads, out);
+    at = fill(b, at, n, grads, out, kThreads * kClipUnroll);
     if (b.n == 0 && !first) break;
-    cudaError_t e = launch_pdl(clip_kernel, dim3((unsigned)grid_of(b, ctas)), dim3(kThreads), 0, s, b,
-                               norm, max_norm, first ? coef : (float *)nullptr);
+    // A CTA per chunk, like the norm's rows: DRAM rewards a narrow window (7.5
+    // GB: 2100 us, 7.16 TB/s; a persistent grid 2200 us). In place the call
+    // often has nothing to do, and then costs the launch of its CTAs (7.5 GB:
+    // 465 us with a chunk each, 118 us with four, which clip in 2138 us): four
+    // chunks a CTA once they outnumber the CTAs that the SMs hold.
+    const int chunks = b.first_chunk[b.n];
+    const int per = b.in_place && chunks > sm_count() * 8 ? 4 : 1;
+    const int ctas = (chunks + per - 1) / per;
+    cudaError_t e = launch_pdl(clip_kernel, dim3((unsigned)(ctas > 0 ? ctas : 1)), dim3(kThreads), 0, s,
+                               b, norm, max_norm, first ? coef : (float *)nullptr, per);
     if (e != cudaSuccess) return e;
     first = false;
   } while (at < n);

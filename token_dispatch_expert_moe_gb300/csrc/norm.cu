@@ -165,10 +165,14 @@ __device__ __forceinline__ float rstd_of(float ss, const RmsNormArgs &a) {
   return rsqrtf(fmaf(ss, a.inv_d, a.eps));   // within 2 ulp
 }
 
-// One row per warp (WARP: rows of up to 4 vectors a lane) or per CTA (rows
-// too wide for the ring below), held in registers as packed vectors: x and
-// the residual are read once, and a thread writes only columns that it has
-// read, so h and y may replace x or the residual in place.
+// One row per warp (WARP) or per CTA, held in registers as packed vectors: x
+// and the residual are read once, and a thread writes only columns that it has
+// read, so h and y may replace x or the residual in place. HBM-bound. The
+// grid is one CTA per row, not a persistent one: CTAs that start in order walk
+// the matrices in a narrow window, which DRAM rewards (32768 x 8192 bf16 with
+// residual and 8-bit rows: 359 us, 6.72 TB/s; persistent CTAs with the next
+// rows fetched ahead through shared memory, in 2 to 4 stages: 404 to 414 us).
+// Two vectors a thread: one takes 366 us, four 408 us.
 template <typename T, int NV, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(RmsNormArgs a) {
   constexpr int N = Vec<T>::N;
@@ -214,78 +218,6 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(RmsNormArgs 
   write_row<T, NV, WARP>(a, row, id, W, h, g, rstd, red, turn);
 }
 
-// Rows of several hundred columns and more: a persistent grid, a CTA per row
-// at a time, the next kStages - 1 rows of x and residual on their way to
-// shared memory while one row is reduced and written. gamma stays in
-// registers. HBM-bound: the ring keeps the loads in flight across the
-// reduction's barrier.
-constexpr int kStages = 3;
-
-template <typename T, int NV, bool RES>
-__global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) rmsnorm_ring_kernel(RmsNormArgs a) {
-  constexpr int N = Vec<T>::N;
-  constexpr int R = RES ? 2 : 1;
-  extern __shared__ uint4 ring[];   // [kStages][R][NV][W]
-  __shared__ float red[2][32];
-  int turn = 0;
-  const int W = blockDim.x, id = threadIdx.x;
-  const int nvec = a.d / N;
-  const uint4 *x = reinterpret_cast<const uint4 *>(a.x);
-  const uint4 *res = reinterpret_cast<const uint4 *>(a.residual);
-  const int64_t step = gridDim.x;
-  auto fetch = [&](int64_t row, int stage) {
-    uint4 *slot = ring + (size_t)stage * R * NV * W + id;
-    if (row < a.rows) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = id + i * W;
-        if (v < nvec) {
-          copy_async<16>(slot + i * W, x + row * nvec + v);
-          if (RES) copy_async<16>(slot + (NV + i) * W, res + row * nvec + v);
-        }
-      }
-    }
-    copy_commit();   // an empty group past the end keeps the count
-  };
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) fetch(blockIdx.x + s * step, s);
-  uint4 g[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = id + i * W;
-    g[i] = v < nvec ? reinterpret_cast<const uint4 *>(a.gamma)[v] : make_uint4(0, 0, 0, 0);
-  }
-  int stage = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += step) {
-    // the stage read one row ago is free: its values have been used
-    fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
-    copy_wait<kStages - 1>();   // this row's group
-    const uint4 *slot = ring + (size_t)stage * R * NV * W + id;
-    uint4 h[NV];
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = id + i * W;
-      h[i] = make_uint4(0, 0, 0, 0);
-      if (v < nvec) {
-        h[i] = slot[i * W];
-        if (RES) h[i] = add_residual<T>(h[i], slot[(NV + i) * W]);
-        if (a.h != nullptr) reinterpret_cast<uint4 *>(a.h)[row * nvec + v] = h[i];
-      }
-      float f[N];
-      unpack16<T>(h[i], f);
-#pragma unroll
-      for (int k = 0; k < N; ++k) ss = fmaf(f[k], f[k], ss);
-    }
-    ss = cta_reduce<false>(ss, red, turn);
-    const float rstd = rstd_of(ss, a);
-    if (a.rstd != nullptr && id == 0) a.rstd[row] = rstd;
-    write_row<T, NV, false>(a, row, id, W, h, g, rstd, red, turn);
-    stage = stage == kStages - 1 ? 0 : stage + 1;
-  }
-  copy_wait<0>();
-}
-
 // ---------------------------------------------------------------------------
 // Backward. A persistent grid: a CTA takes rows blockIdx.x, + gridDim.x, ...;
 // a thread keeps the same columns for every row, so its share of dgamma stays
@@ -314,6 +246,8 @@ __device__ __forceinline__ void pack4(const float (&v)[4], uint2 *out) {
   *reinterpret_cast<__nv_bfloat162 *>(&u.y) = __floats2bfloat162_rn(v[2], v[3]);
   *out = u;
 }
+
+constexpr int kStages = 3;   // rows of the ring
 
 template <typename T, typename TY> constexpr int bwd_unit_bytes(bool dh) {
   return 4 * (int)(sizeof(TY) + sizeof(T) * (dh ? 2 : 1));
@@ -503,34 +437,17 @@ cudaError_t resident(K k, std::atomic<uint64_t> &kept, int threads, size_t smem,
   return cudaSuccess;
 }
 
-template <typename T, int NV, bool RES>
-cudaError_t fwd_ring(const RmsNormArgs &a, int threads, cudaStream_t s) {
-  auto k = rmsnorm_ring_kernel<T, NV, RES>;
-  const size_t smem = (size_t)kStages * (RES ? 2 : 1) * NV * threads * 16;
-  static std::atomic<uint64_t> kept{0};
-  int64_t grid = 0;
-  cudaError_t e = resident(k, kept, threads, smem, a.rows, &grid);
-  if (e != cudaSuccess) return e;
-  k<<<(unsigned)grid, threads, smem, s>>>(a);
-  return cudaGetLastError();
-}
-
 template <typename T> cudaError_t fwd_t(const RmsNormArgs &a, cudaStream_t s) {
   const int nvec = a.d / Vec<T>::N;
   if (nvec <= 32) return fwd<T, 1, true>(a, 128, s);
   if (nvec <= 64) return fwd<T, 2, true>(a, 128, s);
   if (nvec <= 128) return fwd<T, 4, true>(a, 128, s);
-  // a row for each SM at most: nothing to fetch ahead, and the most threads a row
-  if (nvec <= 1024 && a.rows <= sm_count()) return fwd<T, 1, false>(a, round32(nvec), s);
-  const bool res = a.residual != nullptr;
-  if (nvec <= 1024) {
-    const int threads = round32((nvec + 1) / 2);
-    return res ? fwd_ring<T, 2, true>(a, threads, s) : fwd_ring<T, 2, false>(a, threads, s);
+  if (nvec <= 2048) {
+    // a row for each SM at most: the most threads a row
+    if (nvec <= 1024 && a.rows <= sm_count()) return fwd<T, 1, false>(a, round32(nvec), s);
+    return fwd<T, 2, false>(a, round32((nvec + 1) / 2), s);
   }
-  const int threads = round32((nvec + 3) / 4);
-  if (threads <= 512 && (size_t)kStages * (res ? 2 : 1) * 4 * threads * 16 <= kSmem)
-    return res ? fwd_ring<T, 4, true>(a, threads, s) : fwd_ring<T, 4, false>(a, threads, s);
-  return fwd<T, 4, false>(a, threads, s);
+  return fwd<T, 4, false>(a, round32((nvec + 3) / 4), s);
 }
 
 template <typename T, typename TY, typename TX, int NU, bool DH, bool RING>
