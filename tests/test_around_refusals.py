@@ -1,5 +1,6 @@
 """Arguments that the operators around the layer refuse, before anything is
 launched: no GPU is needed."""
+import ctypes
 import os
 
 import pytest
@@ -103,6 +104,8 @@ def test_permute_e4m3(L):
         call(1, **kw)
     call(2, group=16)
     call(2, group=96)
+    call(2, shape=_shape(L, d=102408))
+    call(2, shape=_shape(L, d=51204, dtype=0))
 
 
 def test_grads(L):
@@ -110,6 +113,8 @@ def test_grads(L):
         def __init__(self, *t):
             self.n = len(t)
             self.array = (L.MoETensor * max(1, len(t)))(*[L.MoETensor(*x) for x in t])
+            self.address = ctypes.addressof(self.array)
+            self.device = None
 
     nb = L.MOE_GRAD_NORM_WORKSPACE_BYTES
     ok = List((A[0], 100, 0), (A[1], 100, 1), (None, 0, 0))
@@ -141,6 +146,25 @@ def test_tensor_list(L):
         with pytest.raises(ValueError):
             L.TensorList([bad])
     assert L.TensorList([]).n == 0
+
+
+@pytest.mark.gpu
+def test_tensors_that_the_binding_refuses(L):
+    """Strided or host tensors, and lists whose tensors share memory: nothing
+    is launched."""
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    x = torch.zeros(8, 64, device="cuda", dtype=torch.bfloat16)
+    g, y = x[0].clone(), torch.empty_like(x)
+    for bad in (x.t(), x[:, ::2], x.cpu()):
+        with pytest.raises(ValueError):
+            L.moe_rmsnorm(1, 8, 64, bad, None, g, 1e-5, None, y, None, None, 0, None)
+    flat = torch.zeros(100, device="cuda")
+    for shared in ([flat, flat], [flat[:60], flat[59:]], [flat[50:], flat]):
+        with pytest.raises(ValueError):
+            L.TensorList(shared)
+    assert L.TensorList([flat[:60], flat[60:], flat[:0]]).n == 3
 
 
 def test_constants_match_header(L):

@@ -31,7 +31,7 @@ def _outputs(T, d, E, K, dt):
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("T,d,E,K,group,kept", [
     (1, 8, 1, 1, 0, 1.0), (1, 1024, 64, 8, 128, 1.0), (3, 72, 5, 2, 32, 0.5), (257, 1000, 60, 6, 64, 0.9),
-    (777, 2056, 8, 3, 128, 0.7), (513, 3584, 64, 8, 0, 1.0), (300, 136, 8, 2, 64, 0.0), (1030, 6144, 16, 5, 128, 0.95)])
+    (777, 2056, 8, 3, 128, 0.7), (513, 3584, 64, 8, 0, 1.0), (300, 136, 8, 2, 64, 0.0), (5, 51200, 4, 2, 128, 1.0), (1030, 6144, 16, 5, 128, 0.95)])
 def test_matches_permute_of_the_values(T, d, E, K, group, kept, dt):
     L = lib()
     if dt == torch.float32 and d in (72, 1000, 136):

@@ -55,10 +55,17 @@ class TensorList:
                 raise ValueError(f"tensor {i} is not contiguous")
             if not t.is_cuda or t.device != self.tensors[0].device:
                 raise ValueError(f"tensor {i} is on {t.device}: one CUDA device is wanted")
+        # gradients that share memory would be counted, and in place scaled, twice
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i)
+                       for i, t in enumerate(self.tensors) if t.numel())
+        for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError(f"tensors {i} and {j} overlap")
         self.n = len(self.tensors)
         self.array = (MoETensor * max(1, self.n))(
             *[MoETensor(t.data_ptr(), t.numel(), codes[t.dtype]) for t in self.tensors])
         self.address = ctypes.addressof(self.array)
+        self.device = self.tensors[0].get_device() if self.tensors else None
 
 
 def shape_of(cfg) -> MoEShape:
@@ -132,31 +139,57 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_current_stream = None
+_current = None   # (stream handle, device index) getters, found on first use
 
 
-def _find_current_stream():
-    """The handle of torch's current stream. torch.cuda.current_stream() builds a
-    Stream object (3 us on the GB300's Grace CPU, as much as the rest of a call);
-    the raw handle, where torch gives it, takes 0.1 us."""
+def _find_current():
+    """Getters of torch's current stream handle and device. torch.cuda.
+    current_stream() builds a Stream object (3 us on the GB300's Grace CPU, as
+    much as the rest of a call); the raw getters, where torch has them, take
+    0.1 us."""
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None or not hasattr(torch._C, "_cuda_getDevice"):
-        return lambda: torch.cuda.current_stream().cuda_stream
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return (lambda: torch.cuda.current_stream().cuda_stream), torch.cuda.current_device
     torch.cuda.init()
-    device = torch._C._cuda_getDevice
-    return lambda: raw(device())
+    return (lambda: raw(device())), device
+
+
+def _current_device():
+    global _current
+    if _current is None:
+        _current = _find_current()
+    return _current[1]()
 
 
 def _stream(stream):
-    global _current_stream
+    global _current
     if stream is None:
-        if _current_stream is None:
-            _current_stream = _find_current_stream()
-        return _current_stream()
+        if _current is None:
+            _current = _find_current()
+        return _current[0]()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _dense(t):
+    """_ptr of a tensor that has to be contiguous: the operators around the layer
+    know no strides."""
+    if t is None or t.__class__ is int:
+        return t
+    if not t.is_contiguous():
+        raise ValueError(f"a tensor of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
+    return t.data_ptr()
+
+
+def _here(t):
+    """_dense of a call's first tensor, which says where its tensors lie: it has to
+    be the current device, whose stream the call takes."""
+    if t is not None and t.__class__ is not int and t.get_device() != _current_device():
+        raise ValueError(f"a tensor on {t.device}: the current CUDA device is wanted")
+    return _dense(t)
 
 
 def _call(name, *args):
@@ -271,16 +304,16 @@ def moe_route_bwd(shape, x, W_r, w_sg, logits, topk_idx, topk_prob, topk_w, dw, 
 
 def moe_route_bwd_add(shape, x, W_r, w_sg, logits, topk_idx, topk_prob, topk_w, dw, dz, dlogits_add,
                       dx_in, dW_r, db_r, dw_sg, dx_router, ws, stream=None):
-    _call("moe_route_bwd_add", ctypes.byref(shape), _ptr(x), _ptr(W_r), _ptr(w_sg), _ptr(logits),
-          _ptr(topk_idx), _ptr(topk_prob), _ptr(topk_w), _ptr(dw), _ptr(dz), _ptr(dlogits_add),
-          _ptr(dx_in), _ptr(dW_r), _ptr(db_r), _ptr(dw_sg), _ptr(dx_router), _ptr(ws),
-          _stream(stream))
+    _call("moe_route_bwd_add", ctypes.byref(shape), _here(x), _dense(W_r), _dense(w_sg),
+          _dense(logits), _dense(topk_idx), _dense(topk_prob), _dense(topk_w), _dense(dw), _dense(dz),
+          _dense(dlogits_add), _dense(dx_in), _dense(dW_r), _dense(db_r), _dense(dw_sg),
+          _dense(dx_router), _dense(ws), _stream(stream))
 
 
 def moe_rmsnorm(dtype, rows, d, x, residual, gamma, eps, h, y, q, q_scale, group, rstd,
                 stream=None):
-    _call("moe_rmsnorm", dtype, rows, d, _ptr(x), _ptr(residual), _ptr(gamma), eps, _ptr(h),
-          _ptr(y), _ptr(q), _ptr(q_scale), group, _ptr(rstd), _stream(stream))
+    _call("moe_rmsnorm", dtype, rows, d, _here(x), _dense(residual), _dense(gamma), eps, _dense(h),
+          _dense(y), _dense(q), _dense(q_scale), group, _dense(rstd), _stream(stream))
 
 
 def moe_rmsnorm_bwd_workspace_size(rows: int, d: int) -> int:
@@ -291,41 +324,45 @@ def moe_rmsnorm_bwd(dtype, dy_dtype, dx_dtype, rows, d, dy, h, gamma, rstd, dh, 
                     stream=None, ws_bytes=None):
     """ws: a device tensor (its size becomes ws_bytes) or a pointer with ws_bytes."""
     if ws_bytes is None:
-        ws_bytes = ws.numel() * ws.element_size()
-    _call("moe_rmsnorm_bwd", dtype, dy_dtype, dx_dtype, rows, d, _ptr(dy), _ptr(h), _ptr(gamma),
-          _ptr(rstd), _ptr(dh), _ptr(dx), _ptr(dgamma), _ptr(ws), ws_bytes, _stream(stream))
+        ws_bytes = ws.nbytes
+    _call("moe_rmsnorm_bwd", dtype, dy_dtype, dx_dtype, rows, d, _here(dy), _dense(h), _dense(gamma),
+          _dense(rstd), _dense(dh), _dense(dx), _dense(dgamma), _dense(ws), ws_bytes, _stream(stream))
 
 
 def moe_balance_loss(shape, logits, topk_idx, mask, alpha, loss, counts, prob_mean, coef, ws,
                      stream=None):
-    _call("moe_balance_loss", ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(mask), alpha,
-          _ptr(loss), _ptr(counts), _ptr(prob_mean), _ptr(coef), _ptr(ws), _stream(stream))
+    _call("moe_balance_loss", ctypes.byref(shape), _here(logits), _dense(topk_idx), _dense(mask), alpha,
+          _dense(loss), _dense(counts), _dense(prob_mean), _dense(coef), _dense(ws), _stream(stream))
 
 
 def moe_balance_loss_bwd(shape, logits, mask, coef, dloss, dlogits, stream=None):
-    _call("moe_balance_loss_bwd", ctypes.byref(shape), _ptr(logits), _ptr(mask), _ptr(coef),
-          _ptr(dloss), _ptr(dlogits), _stream(stream))
+    _call("moe_balance_loss_bwd", ctypes.byref(shape), _here(logits), _dense(mask), _dense(coef),
+          _dense(dloss), _dense(dlogits), _stream(stream))
 
 
 def moe_permute_e4m3(shape, q, q_scale, group, topk_idx, keep, Xp, row_of, src_of, counts, offsets,
                      ws, stream=None):
-    _call("moe_permute_e4m3", ctypes.byref(shape), _ptr(q), _ptr(q_scale), group, _ptr(topk_idx),
-          _ptr(keep), _ptr(Xp), _ptr(row_of), _ptr(src_of), _ptr(counts), _ptr(offsets), _ptr(ws),
-          _stream(stream))
+    _call("moe_permute_e4m3", ctypes.byref(shape), _here(q), _dense(q_scale), group, _dense(topk_idx),
+          _dense(keep), _dense(Xp), _dense(row_of), _dense(src_of), _dense(counts), _dense(offsets),
+          _dense(ws), _stream(stream))
+
+
+def _list_here(grads):
+    if grads.device is not None and grads.device != _current_device():
+        raise ValueError(f"the tensors are on cuda:{grads.device}: the current CUDA device is wanted")
+    return grads.address
 
 
 def moe_grad_norm(grads, norm, ws, stream=None, ws_bytes=None):
     """grads: a TensorList. ws: a device tensor (its size becomes ws_bytes) or a pointer with ws_bytes."""
     if ws_bytes is None:
-        ws_bytes = ws.numel() * ws.element_size()
-    _call("moe_grad_norm", grads.n, grads.address, _ptr(norm), _ptr(ws), ws_bytes,
-          _stream(stream))
+        ws_bytes = ws.nbytes
+    _call("moe_grad_norm", grads.n, _list_here(grads), _here(norm), _dense(ws), ws_bytes, _stream(stream))
 
 
 def moe_grad_clip(grads, out, norm, max_norm, coef, stream=None):
     """grads: a TensorList; out: a TensorList of the same tensors' sizes and types, or None for in place."""
-    if out is not None and out.n != grads.n:
+    if out is not None and (out.n != grads.n or out.device != grads.device):
         raise MoEError("moe_grad_clip", 1)
-    _call("moe_grad_clip", grads.n, grads.address,
-          None if out is None else out.address, _ptr(norm), max_norm, _ptr(coef),
-          _stream(stream))
+    _call("moe_grad_clip", grads.n, _list_here(grads), None if out is None else out.address,
+          _here(norm), max_norm, _dense(coef), _stream(stream))

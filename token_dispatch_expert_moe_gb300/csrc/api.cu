@@ -583,6 +583,7 @@ moe_status_t moe_permute_e4m3(const moe_shape_t *shape, const void *q, const flo
   NvtxRange trace("moe_permute_e4m3");
   if (!shape_ok(shape) || group < 0) return MOE_ERR_INVALID_ARG;
   if (!group_ok(group)) return MOE_ERR_UNSUPPORTED;
+  if ((size_t)shape->d * size_of(shape->dtype) > kPermRowCap) return MOE_ERR_UNSUPPORTED;
   if (!q || !q_scale || !topk_idx || !keep || !Xp || !row_of || !src_of || !counts || !offsets || !ws)
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned4(q_scale) || !aligned16(Xp) || !aligned16(ws)) return MOE_ERR_INVALID_ARG;

@@ -295,6 +295,8 @@ size_t balance_workspace_bytes(int64_t T, int64_t S, int E);
 cudaError_t launch_balance_loss(const BalanceArgs &a, cudaStream_t s);
 cudaError_t launch_balance_loss_bwd(const BalanceArgs &a, cudaStream_t s);
 
+// Widest row in bytes that the permutation's bulk copies hold in shared memory.
+constexpr size_t kPermRowCap = 200 * 1024;
 // Rows of an e4m3 matrix with scales, permuted: Xp[row_of[t,k]] = dtype(q[t] * scale[t]).
 cudaError_t launch_permute_e4m3_rows(const PermuteArgs &a, const void *q, const float *q_scale,
                                      int group, cudaStream_t s);

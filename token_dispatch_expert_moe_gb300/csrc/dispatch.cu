@@ -215,19 +215,17 @@ __global__ void __launch_bounds__(256) pad_fill_kernel(PermuteArgs a, int vec_pe
 }
 
 // Xp[row_of[t,k]] = T(q[t] * scale[t]): one CTA per token reads the token's
-// e4m3 row once and writes it to its kept slots' rows. HBM-bound: d bytes read
-// and K d sizeof(T) written per token.
+// e4m3 row once, converts it into shared memory, and writes it to its kept
+// slots' rows with bulk stores. HBM-bound: d bytes read and K d sizeof(T)
+// written per token (16384 x 6144 to 0.9 of 8 bf16 rows each: 242 us, 6.4 TB/s
+// of a floor of 229 us; 16-byte stores by the threads in place of the bulk
+// stores 251 us). Like the bf16 row copy, it reads q before its wait.
 template <typename T>
 __global__ void __launch_bounds__(256) permute_e4m3_kernel(PermuteArgs a, const uint8_t *q,
                                                            const float *q_scale, int group, int ng) {
   constexpr int N = Vec<T>::N;
+  extern __shared__ __align__(128) uint8_t row_smem[];
   const int64_t t = blockIdx.x;
-  const int K = a.K;
-  pdl_wait();   // row_of comes from map_scatter
-  int32_t r[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) r[k] = k < K ? a.row_of[t * K + k] : -1;
-  T *Xp = reinterpret_cast<T *>(a.Xp);
   for (int v = threadIdx.x * N; v < a.d; v += blockDim.x * N) {
     const float s = q_scale[t * ng + v / group];
     float f[N];
@@ -247,10 +245,25 @@ __global__ void __launch_bounds__(256) permute_e4m3_kernel(PermuteArgs a, const 
       f[2 * i] = p.x * s;
       f[2 * i + 1] = p.y * s;
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (r[k] >= 0) store16<T>(Xp + (int64_t)r[k] * a.d + v, f);
+    store16<T>(reinterpret_cast<T *>(row_smem) + v, f);
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copy engine reads the row
+  __syncthreads();
+  pdl_wait();   // row_of comes from map_scatter
+  if (threadIdx.x != 0) return;
+  const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(row_smem));
+  const uint32_t row_bytes = (uint32_t)a.d * sizeof(T);
+  uint8_t *Xp = static_cast<uint8_t *>(a.Xp);
+  for (int k = 0; k < a.K; ++k) {
+    const int32_t r = a.row_of[t * a.K + k];
+    if (r >= 0)
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                       Xp + (int64_t)r * row_bytes),
+                   "r"(sm), "r"(row_bytes)
+                   : "memory");
+  }
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // out[t] = sum_k w[t,k] Yp[row_of[t,k]] (+ sigmoid(z_t) Ys[t]), fp32 sum in
@@ -554,21 +567,25 @@ cudaError_t launch_permute(const PermuteArgs &a, cudaStream_t s) {
 
 cudaError_t launch_permute_e4m3_rows(const PermuteArgs &a, const void *q, const float *q_scale,
                                      int group, cudaStream_t s) {
+  auto k = a.dtype == MOE_BF16 ? permute_e4m3_kernel<__nv_bfloat16> : permute_e4m3_kernel<float>;
+  const size_t smem = (size_t)a.d * (a.dtype == MOE_BF16 ? 2 : 4);
+  if (smem > kPermRowCap) return cudaErrorInvalidValue;
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPermRowCap);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.T);
   cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
   const int g = group > 0 ? group : a.d;
-  const int ng = (a.d + g - 1) / g;
-  const uint8_t *qb = static_cast<const uint8_t *>(q);
-  return a.dtype == MOE_BF16
-             ? cudaLaunchKernelEx(&cfg, permute_e4m3_kernel<__nv_bfloat16>, a, qb, q_scale, g, ng)
-             : cudaLaunchKernelEx(&cfg, permute_e4m3_kernel<float>, a, qb, q_scale, g, ng);
+  return cudaLaunchKernelEx(&cfg, k, a, static_cast<const uint8_t *>(q), q_scale, g, (a.d + g - 1) / g);
 }
 
 // Slot bound KK >= K of the un-permute kernels: 1, 2, 4 or 8.

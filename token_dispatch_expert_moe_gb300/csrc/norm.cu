@@ -408,7 +408,7 @@ cudaError_t fwd(const RmsNormArgs &a, int threads, cudaStream_t s) {
 }
 
 constexpr int round32(int v) { return (v + 31) & ~31; }
-constexpr size_t kSmem = 227 * 1024;   // per CTA; the SM holds 228 KB, 1 KB of it per CTA reserved
+constexpr size_t kSmem = 226 * 1024;   // of the 227 KB that a CTA may have; the rest for static arrays
 
 // CTAs of a persistent grid: those that fit the device at once, at most
 // `most`. The answer for the last device and size that a kernel was asked for
@@ -424,7 +424,8 @@ cudaError_t resident(K k, std::atomic<uint64_t> &kept, int threads, size_t smem,
   const uint64_t key = (uint64_t)(dev + 1) << 52 | (uint64_t)threads << 41 | (uint64_t)smem << 21;
   uint64_t word = kept.load(std::memory_order_relaxed);
   if ((word >> 21) != (key >> 21)) {
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the same limit in every call: another thread's launch never finds less
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     int per_sm = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem);
