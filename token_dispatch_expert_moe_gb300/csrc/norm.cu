@@ -173,8 +173,11 @@ __device__ __forceinline__ float rstd_of(float ss, const RmsNormArgs &a) {
 // residual and 8-bit rows: 359 us, 6.72 TB/s; persistent CTAs with the next
 // rows fetched ahead through shared memory, in 2 to 4 stages: 404 to 414 us).
 // Two vectors a thread: one takes 366 us, four 408 us.
+// 56 registers for two vectors: one fewer than the compiler takes by itself, and
+// a third CTA of 384 threads fits (16384 x 6144: 150 -> 134 us; 32768 x 8192,
+// CTAs of 512: 360 -> 362 us).
 template <typename T, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(RmsNormArgs a) {
+__global__ void __maxnreg__(WARP ? 80 : NV == 2 ? 56 : 64) rmsnorm_kernel(RmsNormArgs a) {
   constexpr int N = Vec<T>::N;
   __shared__ float red[2][32];
   int turn = 0;
