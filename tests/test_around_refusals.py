@@ -78,14 +78,14 @@ def test_balance(L):
     for kw in (dict(shape=_shape(L, E=65)), dict(shape=_shape(L, T=0)), dict(shape=_shape(L, K=9)),
                dict(shape=_shape(L, subseq_len=-1)), dict(logits=None), dict(idx=None), dict(loss=None),
                dict(counts=None), dict(coef=None), dict(ws=None), dict(alpha=float("nan")), dict(alpha=float("inf")),
-               dict(logits=A[0] + 4), dict(ws=A[7] + 8), dict(prob=A[5] + 2), dict(idx=A[1] + 1)):
+               dict(logits=A[0] + 4), dict(ws=A[7] + 8), dict(prob=A[5] + 2), dict(idx=A[1] + 1), dict(coef=A[6] + 4)):
         call(1, **kw)
 
     def back(code, shape=None, logits=A[0], mask=None, coef=A[1], dloss=None, dl=A[2]):
         refused(L, code, "moe_balance_loss_bwd", shape or _shape(L), logits, mask, coef, dloss, dl, 0)
 
     for kw in (dict(shape=_shape(L, E=0)), dict(logits=None), dict(coef=None), dict(dl=None), dict(dl=A[2] + 4),
-               dict(dloss=A[3] + 2), dict(dl=A[0] + 16)):
+               dict(dloss=A[3] + 2), dict(dl=A[0] + 16), dict(coef=A[1] + 8)):
         back(1, **kw)
     fake = A[0]
     refused(L, 1, "moe_route_bwd_add", _shape(L), fake, fake, None, fake, fake, fake, fake, fake, None, None, None, fake,

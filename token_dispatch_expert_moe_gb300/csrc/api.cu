@@ -551,7 +551,7 @@ moe_status_t moe_balance_loss(const moe_shape_t *shape, const float *logits, con
   if (!shape_ok(shape) || !std::isfinite(alpha)) return MOE_ERR_INVALID_ARG;
   if (!logits || !topk_idx || !loss || !counts || !coef || !ws) return MOE_ERR_INVALID_ARG;
   if (!aligned16(logits) || !aligned4(topk_idx) || !aligned4(loss) || !aligned4(counts) ||
-      !aligned4(prob_mean) || !aligned4(coef) || !aligned16(ws))
+      !aligned4(prob_mean) || !aligned16(coef) || !aligned16(ws))
     return MOE_ERR_INVALID_ARG;
   BalanceArgs a = balance_args(shape);
   a.logits = logits; a.topk_idx = topk_idx; a.mask = mask; a.alpha = alpha; a.loss = loss;
@@ -566,7 +566,7 @@ moe_status_t moe_balance_loss_bwd(const moe_shape_t *shape, const float *logits,
                                   moe_stream_t stream) {
   NvtxRange trace("moe_balance_loss_bwd");
   if (!shape_ok(shape) || !logits || !coef || !dlogits) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(logits) || !aligned4(coef) || !aligned4(dloss) || !aligned16(dlogits))
+  if (!aligned16(logits) || !aligned16(coef) || !aligned4(dloss) || !aligned16(dlogits))
     return MOE_ERR_INVALID_ARG;
   BalanceArgs a = balance_args(shape);
   const size_t n = (size_t)a.T * a.E * sizeof(float);

@@ -66,12 +66,13 @@ Split split_of(int64_t T, int64_t S, int lanes) {
 // gradient: 16.5 and 22.2 us; 8 lanes of two quads 20.6 and 23.4 us, 16 lanes
 // of one 31.1 and 29.4 us). Bound by instruction issue more than by HBM: half
 // the issue slots and half the bandwidth are in use.
-// A token's logits, l[4 v + i] of expert 4 (sub + v L) + i: -inf past E, and
+// A row of E values, l[4 v + i] of expert 4 (sub + v L) + i: `none` past E, and
 // throughout where `in` is false (nothing is read then).
 template <int L, int V>
-__device__ __forceinline__ void load_quads(const float *row, int sub, int E, bool in, float (&l)[4 * V]) {
+__device__ __forceinline__ void load_quads(const float *row, int sub, int E, bool in, float none,
+                                           float (&l)[4 * V]) {
 #pragma unroll
-  for (int i = 0; i < 4 * V; ++i) l[i] = -INFINITY;
+  for (int i = 0; i < 4 * V; ++i) l[i] = none;
   if (!in) return;
   if ((E & 3) == 0) {
 #pragma unroll
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kMaxThreads) balance_count_kernel(BalanceArgs 
   const int E = a.E, K = a.K;
   if (threadIdx.x < 64) cnt[threadIdx.x] = 0;
   if (threadIdx.x == 0) tok = 0;
-  pdl_trigger();   // the join may take its place: it waits for this grid's end
+  pdl_wait();
   __syncthreads();
   float acc[4 * V], next[4 * V];
 #pragma unroll
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kMaxThreads) balance_count_kernel(BalanceArgs 
   int idx[kSlots], keep = 0;
   auto fetch = [&](int64_t t) {
     const bool in = t < hi;
-    load_quads<L, V>(a.logits + t * E, sub, E, in, next);
+    load_quads<L, V>(a.logits + t * E, sub, E, in, -INFINITY, next);
     keep = in && (a.mask == nullptr || a.mask[t] != 0);
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
@@ -320,19 +321,17 @@ balance_join_kernel(BalanceArgs a, Partials w, int64_t chunks, int slices) {
 template <int L, int V>
 __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(BalanceArgs a) {
   constexpr int kPer = kBwdThreads / L;
+  pdl_wait();
   const int sub = threadIdx.x % L;
   const int64_t t = (int64_t)blockIdx.x * kPer + threadIdx.x / L;
   const int E = a.E;
   const bool in = t < a.T;
   const bool live = in && (a.mask == nullptr || a.mask[t] != 0);
-  const float *coef = a.coef + (in ? t / a.S : 0) * E;
+  // T and S fit in 32 bits; coef has the alignment of logits, so its rows too
+  const float *coef = a.coef + (int64_t)(in ? (uint32_t)t / (uint32_t)a.S : 0) * E;
   float p[4 * V], w[4 * V], dot = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4 * V; ++i) {
-    const int e = 4 * (sub + (i / 4) * L) + i % 4;
-    w[i] = e < E ? coef[e] : 0.0f;
-  }
-  load_quads<L, V>(a.logits + t * E, sub, E, live, p);
+  load_quads<L, V>(coef, sub, E, true, 0.0f, w);
+  load_quads<L, V>(a.logits + t * E, sub, E, live, -INFINITY, p);
   const float r = softmax_quads<L, V>(p);
 #pragma unroll
   for (int i = 0; i < 4 * V; ++i) {
@@ -389,8 +388,8 @@ template <int L, int V> cudaError_t fwd(const BalanceArgs &a, cudaStream_t s) {
   w.term = reinterpret_cast<float *>(p + r.term);
   w.prob = reinterpret_cast<float *>(p + r.prob);
   w.count = reinterpret_cast<int32_t *>(p + r.count);
-  balance_count_kernel<L, V><<<(unsigned)(sp.chunks * a.n_sub), sp.threads, 0, s>>>(a, w, sp.chunks, sp.len);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_pdl(balance_count_kernel<L, V>, dim3((unsigned)(sp.chunks * a.n_sub)),
+                             dim3(sp.threads), 0, s, a, w, sp.chunks, sp.len);
   if (e != cudaSuccess || sp.chunks * a.n_sub == 1) return e;
   // threads a pair: as many as fill the cluster, no more than chunks
   int slices = 1;
@@ -401,8 +400,8 @@ template <int L, int V> cudaError_t fwd(const BalanceArgs &a, cudaStream_t s) {
 
 template <int L, int V> cudaError_t bwd(const BalanceArgs &a, cudaStream_t s) {
   const int64_t per = kBwdThreads / L;
-  balance_bwd_kernel<L, V><<<(unsigned)((a.T + per - 1) / per), kBwdThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(balance_bwd_kernel<L, V>, dim3((unsigned)((a.T + per - 1) / per)),
+                    dim3(kBwdThreads), 0, s, a);
 }
 
 template <bool BWD> cudaError_t by_experts(const BalanceArgs &a, cudaStream_t s) {

@@ -117,7 +117,6 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
                                                            double *partial, int add) {
   __shared__ double red[32];
   pdl_wait();   // the gradients, and the call before that may still read `partial`
-  pdl_trigger();
   double s = 0.0;
   const int64_t chunks = b.first_chunk[b.n];
   int i = tensor_of(b, blockIdx.x);
@@ -134,7 +133,6 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
 __global__ void __launch_bounds__(kThreads) norm_kernel(const double *partial, int n, float *norm) {
   __shared__ double red[32];
   pdl_wait();
-  pdl_trigger();
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) s += partial[i];
   s = block_sum_double(s, red);
@@ -183,7 +181,6 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
                                                         const float *norm, float max_norm,
                                                         float *coef_out, int per) {
   pdl_wait();
-  pdl_trigger();
   const float coef = coef_of(norm[0], max_norm);
   if (coef_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) coef_out[0] = coef;
   if (coef == 1.0f && b.in_place) return;

@@ -5,15 +5,15 @@
 
 namespace moe {
 
-// A kernel launched with launch_pdl may start while its predecessor on the
+// A kernel launched with launch_pdl is brought up while its predecessor on the
 // stream still runs. It reads nothing that the predecessor writes, and writes
-// nothing, before pdl_wait() has returned (the predecessor has completed and
-// its writes are visible); every thread calls it, so that the kernel after it
-// may rely on the whole chain.
+// nothing to memory, before pdl_wait() has returned (the predecessor has
+// completed and its writes are visible). Every thread of every CTA waits, so
+// that this kernel's end means the end of all before it. None of these kernels
+// triggers its successor early: measured, that gained nothing (norm of 16384 x
+// 6144: 131 us with or without, 133 us without this launch) and cost up to 1
+// us where the successor's CTAs took the place of work.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_trigger() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,

@@ -181,6 +181,7 @@ __global__ void __maxnreg__(WARP ? 80 : NV == 2 ? 56 : 64) rmsnorm_kernel(RmsNor
   constexpr int N = Vec<T>::N;
   __shared__ float red[2][32];
   int turn = 0;
+  pdl_wait();
   const int W = WARP ? 32 : blockDim.x;
   const int id = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int64_t row = WARP ? ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5))
@@ -268,6 +269,7 @@ __global__ void __launch_bounds__(RING ? 512 : 1024) rmsnorm_bwd_kernel(RmsNormB
   extern __shared__ uint4 ring[];   // per stage: dy [NU][W], h [NU][W], dh [NU][W]
   __shared__ float red[2][32];
   int turn = 0;
+  pdl_wait();
   const int W = blockDim.x, id = threadIdx.x, nu = a.d / 4;
   const UY *dy = reinterpret_cast<const UY *>(a.dy);
   const UT *h = reinterpret_cast<const UT *>(a.h);
@@ -406,8 +408,8 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float *partial, int 
 template <typename T, int NV, bool WARP>
 cudaError_t fwd(const RmsNormArgs &a, int threads, cudaStream_t s) {
   const int64_t per = WARP ? threads / 32 : 1;
-  rmsnorm_kernel<T, NV, WARP><<<(unsigned)((a.rows + per - 1) / per), threads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(rmsnorm_kernel<T, NV, WARP>, dim3((unsigned)((a.rows + per - 1) / per)),
+                    dim3(threads), 0, s, a);
 }
 
 constexpr int round32(int v) { return (v + 31) & ~31; }
@@ -462,8 +464,7 @@ cudaError_t bwd(const RmsNormBwdArgs &a, int threads, cudaStream_t s) {
   int64_t grid = 0;
   cudaError_t e = resident(k, kept, threads, smem, rmsnorm_bwd_max_partials(a.rows), &grid);
   if (e != cudaSuccess) return e;
-  k<<<(unsigned)grid, threads, smem, s>>>(a);
-  e = cudaGetLastError();
+  e = launch_pdl(k, dim3((unsigned)grid), dim3(threads), smem, s, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(dgamma_kernel, dim3((a.d + 31) / 32), dim3(1024), 0, s, a.partial, (int)grid, a.d,
                     a.dgamma);
