@@ -9,6 +9,8 @@
 // fp64; where that fp32 sum leaves the safe range (gradients above 1e18 or all
 // below 1e-15) the share is summed again in fp64, so the norm is right
 // wherever it is an fp32 number. The order of the additions is fixed.
+#include <cooperative_groups.h>
+
 #include "launch.cuh"
 
 namespace moe {
@@ -113,21 +115,51 @@ __device__ __forceinline__ double block_sum_double(double v, double *smem32) {
   return r;
 }
 
+// Sum of the squares of chunks first, first + step, ...; valid in thread 0.
+__device__ __forceinline__ double squares_of(const Batch &b, int64_t first, int step, double *red) {
+  double s = 0.0;
+  const int64_t chunks = b.first_chunk[b.n];
+  if (first < chunks) {
+    int i = tensor_of(b, (int)first);
+    for (int64_t c = first; c < chunks; c += step) {
+      while (b.first_chunk[i + 1] <= c) ++i;
+      const int64_t v0 = (c - b.first_chunk[i]) * (kThreads * kNormUnroll);
+      s += b.bf16[i] ? chunk_squares(static_cast<const __nv_bfloat16 *>(b.in[i]), b.numel[i], v0)
+                     : chunk_squares(static_cast<const float *>(b.in[i]), b.numel[i], v0);
+    }
+  }
+  return block_sum_double(s, red);
+}
+
 __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ Batch b,
                                                            double *partial, int add) {
   __shared__ double red[32];
   pdl_wait();   // the gradients, and the call before that may still read `partial`
-  double s = 0.0;
-  const int64_t chunks = b.first_chunk[b.n];
-  int i = tensor_of(b, blockIdx.x);
-  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    while (b.first_chunk[i + 1] <= c) ++i;
-    const int64_t v0 = (c - b.first_chunk[i]) * (kThreads * kNormUnroll);
-    s += b.bf16[i] ? chunk_squares(static_cast<const __nv_bfloat16 *>(b.in[i]), b.numel[i], v0)
-                   : chunk_squares(static_cast<const float *>(b.in[i]), b.numel[i], v0);
-  }
-  s = block_sum_double(s, red);
+  const double s = squares_of(b, blockIdx.x, gridDim.x, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = add ? partial[blockIdx.x] + s : s;
+}
+
+// The whole norm of a short list in one launch: one cluster, whose CTAs hand
+// their sums to the first through shared memory. Up to 16 chunks it takes the
+// GPU no longer than the two kernels (3.2 to 4.4 us against 4.0 to 4.3) and the
+// host one launch less (a stream of calls: 4.3 us each against 5.8); with 32
+// chunks 6.1 us against 4.4.
+constexpr int kSmallCtas = 8, kSmallChunks = 16;
+
+__global__ void __cluster_dims__(kSmallCtas, 1, 1) __launch_bounds__(kThreads)
+small_norm_kernel(const __grid_constant__ Batch b, float *norm) {
+  cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  __shared__ double red[32], all[kSmallCtas];
+  pdl_wait();
+  const int rank = (int)cluster.block_rank();
+  const double s = squares_of(b, rank, kSmallCtas, red);
+  if (threadIdx.x == 0) *cluster.map_shared_rank(&all[rank], 0) = s;
+  cluster.sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    double t = 0.0;
+    for (int r = 0; r < kSmallCtas; ++r) t += all[r];
+    norm[0] = (float)sqrt(t);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const double *partial, int n, float *norm) {
@@ -239,6 +271,8 @@ cudaError_t launch_grad_norm(int n, const moe_tensor_t *grads, float *norm, doub
     at = fill(b, at, n, grads, nullptr, kThreads * kNormUnroll);
     if (b.n == 0) break;
     const bool first = grid == 0;
+    if (first && at == n && b.first_chunk[b.n] <= kSmallChunks)
+      return launch_pdl(small_norm_kernel, dim3(kSmallCtas), dim3(kThreads), 0, s, b, norm);
     if (first) grid = at == n && b.first_chunk[b.n] < ctas ? b.first_chunk[b.n] : ctas;
     cudaError_t e = launch_pdl(squares_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, b,
                                partial, first ? 0 : 1);   // later batches add theirs
