@@ -4,11 +4,11 @@
 //   coef = max_norm / norm if max_norm < norm < inf, else 1;  out = g coef
 //
 // Tensors are cut into chunks of 32 KB (norm) or 16 KB (clipping), so a few
-// huge tensors and many tiny ones load the grid alike. The
-// squares of a thread's share of a chunk are added in fp32 and carried on in
-// fp64; where that fp32 sum leaves the safe range (gradients above 1e18 or all
-// below 1e-15) the share is summed again in fp64, so the norm is right
-// wherever it is an fp32 number. The order of the additions is fixed.
+// huge tensors and many tiny ones load the grid alike. The squares of a
+// thread's share of a chunk are added in fp32 and carried on in fp64; where
+// that fp32 sum leaves the safe range (gradients above 1e18 or all below
+// 1e-15) the share is summed again in fp64, so the norm is right wherever it
+// is an fp32 number. The order of the additions is fixed.
 #include <cooperative_groups.h>
 
 #include "launch.cuh"
@@ -19,7 +19,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kNormUnroll = 8;   // 16-byte vectors per thread and chunk: chunks of 32 KB
 constexpr int kClipUnroll = 4;   // 16 KB
-constexpr int kBatch = 96;                               // tensors per launch
+constexpr int kBatch = 96;       // tensors per launch
 
 // Tensors of one launch, passed by value: nothing of the caller's host arrays
 // is read after the call. first_chunk[n] is the number of chunks.

@@ -19,7 +19,7 @@ namespace moe {
 namespace {
 
 constexpr float kE4m3Max = 448.0f;
-// Smallest amax a scale is made of: 448 / amax stays finite.
+// Smallest amax a scale is made of: the scale and its reciprocal stay normal numbers.
 constexpr float kAmaxFloor = 7.70372e-34f;   // 2^-110
 
 // Sum or maximum over the CTA with one barrier: every warp writes its value
@@ -223,11 +223,11 @@ __global__ void __maxnreg__(WARP ? 80 : NV == 2 ? 56 : 64) rmsnorm_kernel(RmsNor
 }
 
 // ---------------------------------------------------------------------------
-// Backward. A persistent grid: a CTA takes rows blockIdx.x, + gridDim.x, ...;
+// Backward. Persistent grids: a CTA (or a warp of it) takes row after row, and
 // a thread keeps the same columns for every row, so its share of dgamma stays
-// in registers and leaves once, as a row of `partial`. A thread's unit is 4
-// columns, 16 bytes of fp32 or 8 of bf16, so that every access of a warp is
-// contiguous whatever mixture of types the call has.
+// in registers and leaves once, in the CTA's row of `partial`. A thread's unit
+// is 4 columns, 16 bytes of fp32 or 8 of bf16, so that every access of a warp
+// is contiguous whatever mixture of types the call has.
 
 template <typename T> struct Unit;
 template <> struct Unit<float> { using type = float4; };
@@ -251,18 +251,104 @@ __device__ __forceinline__ void pack4(const float (&v)[4], uint2 *out) {
   *out = u;
 }
 
-constexpr int kStages = 3;   // rows of the ring
-
 template <typename T, typename TY> constexpr int bwd_unit_bytes(bool dh) {
   return 4 * (int)(sizeof(TY) + sizeof(T) * (dh ? 2 : 1));
 }
 
-// RING: the next kStages - 1 rows of dy, h and dh are copied to shared memory
-// in the background (rows of up to 16384 columns); otherwise they are read
-// from global memory twice, before and after the row's sum, the second time
-// from the caches.
-template <typename T, typename TY, typename TX, int NU, bool DH, bool RING>
-__global__ void __launch_bounds__(RING ? 512 : 1024) rmsnorm_bwd_kernel(RmsNormBwdArgs a) {
+// Rows of up to 512 columns: one per warp, eight warps a CTA, whose shares of
+// dgamma meet in shared memory at the end. Its many warps are what hides the
+// loads' latency.
+constexpr int kRowWarps = 8;
+
+template <typename T, typename TY, typename TX, int NU, bool DH>
+__global__ void __launch_bounds__(kRowWarps * 32) rmsnorm_bwd_warp_kernel(RmsNormBwdArgs a) {
+  using UT = typename Unit<T>::type;
+  using UY = typename Unit<TY>::type;
+  using UX = typename Unit<TX>::type;
+  __shared__ float sum[NU * 32 * 4];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nu = a.d / 4;
+  const UY *dy = reinterpret_cast<const UY *>(a.dy);
+  const UT *h = reinterpret_cast<const UT *>(a.h);
+  const UT *dh = reinterpret_cast<const UT *>(a.dh);
+  UX *dx = reinterpret_cast<UX *>(a.dx);
+  UT g[NU];
+  float acc[NU][4];
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int u = lane + i * 32;
+    g[i] = u < nu ? reinterpret_cast<const UT *>(a.gamma)[u] : UT{};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
+  }
+  const int64_t step = (int64_t)gridDim.x * kRowWarps;
+  for (int64_t row = (int64_t)blockIdx.x * kRowWarps + warp; row < a.rows; row += step) {
+    UY yv[NU];
+    UT hv[NU], dv[NU];
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = lane + i * 32;
+      yv[i] = u < nu ? dy[row * nu + u] : UY{};
+      hv[i] = u < nu ? h[row * nu + u] : UT{};
+      if (DH) dv[i] = u < nu ? dh[row * nu + u] : UT{};
+    }
+    const float rstd = a.rstd[row];
+    float xh[NU][4], gy[NU][4];   // xhat and dy gamma
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      float y4[4], gv[4];
+      unpack4(yv[i], y4);
+      unpack4(hv[i], xh[i]);
+      unpack4(g[i], gv);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        xh[i][k] *= rstd;
+        gy[i][k] = y4[k] * gv[k];
+        acc[i][k] = fmaf(y4[k], xh[i][k], acc[i][k]);
+        dot = fmaf(gy[i][k], xh[i][k], dot);
+      }
+    }
+    const float m = warp_reduce<false>(dot) * a.inv_d;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = lane + i * 32;
+      float o[4], d4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (DH) unpack4(dv[i], d4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = rstd * fmaf(-xh[i][k], m, gy[i][k]) + d4[k];
+      if (u < nu) pack4(o, dx + row * nu + u);
+    }
+  }
+  for (int w = 0; w < kRowWarps; ++w) {   // the warps add in order
+    if (warp == w) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float *p = sum + (lane + i * 32) * 4 + k;
+          *p = w == 0 ? acc[i][k] : *p + acc[i][k];
+        }
+    }
+    __syncthreads();
+  }
+  for (int j = threadIdx.x; j < a.d; j += blockDim.x) a.partial[(int64_t)blockIdx.x * a.d + j] = sum[j];
+}
+
+// Wider rows: one per CTA.
+// STAGES > 0: a ring of so many rows in shared memory. The next rows' dy, h
+// and dh are on their way while one row is reduced and written, so the loads
+// run on across the reduction's barrier (32768 x 8192, dy and dx fp32, dh
+// bf16: 471 us, 6.83 TB/s; plain loads 821 us). Three rows where they fit and
+// leave one CTA to an SM anyway (16384 x 6144: 177 us, with two 199 us), two
+// where more CTAs fit then (65536 x 1024: 121 us, with three 129 us) and where
+// three do not fit (16384 x 8192, all fp32: 313 us).
+// STAGES = 0, for rows too wide for two: dy and h are read from global memory
+// twice, before and after the row's sum, the second time from the caches
+// (16384 x 16384: 800 us, 4.0 TB/s).
+template <typename T, typename TY, typename TX, int NU, bool DH, int STAGES>
+__global__ void __launch_bounds__(STAGES > 0 ? 512 : 1024) rmsnorm_bwd_kernel(RmsNormBwdArgs a) {
+  constexpr bool RING = STAGES > 0;
   using UT = typename Unit<T>::type;
   using UY = typename Unit<TY>::type;
   using UX = typename Unit<TX>::type;
@@ -302,7 +388,7 @@ __global__ void __launch_bounds__(RING ? 512 : 1024) rmsnorm_bwd_kernel(RmsNormB
   };
   if (RING) {
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) fetch(blockIdx.x + s * step, s);
+    for (int s = 0; s < STAGES - 1; ++s) fetch(blockIdx.x + s * step, s);
   }
   UT g[NU];
   float acc[NU][4];
@@ -330,8 +416,8 @@ __global__ void __launch_bounds__(RING ? 512 : 1024) rmsnorm_bwd_kernel(RmsNormB
     };
     if (RING) {
       // the stage read one row ago is free: its values have gone into that row's dx
-      fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
-      copy_wait<kStages - 1>();   // this row's group
+      fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+      copy_wait<RING ? STAGES - 1 : 0>();   // this row's group
     }
     float dot = 0.0f;
 #pragma unroll
@@ -374,7 +460,7 @@ __global__ void __launch_bounds__(RING ? 512 : 1024) rmsnorm_bwd_kernel(RmsNormB
         pack4(o, dx + row * nu + u);
       }
     }
-    stage = stage == kStages - 1 ? 0 : stage + 1;
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
   }
   if (RING) copy_wait<0>();
   float *part = a.partial + (int64_t)blockIdx.x * a.d;
@@ -395,6 +481,7 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float *partial, int 
   const int j = blockIdx.x * 32 + lane;
   float v = 0.0f;
   if (j < d)
+#pragma unroll 8
     for (int p = warp; p < nparts; p += 32) v += partial[(int64_t)p * d + j];
   s[warp][lane] = v;
   __syncthreads();
@@ -429,9 +516,12 @@ cudaError_t resident(K k, std::atomic<uint64_t> &kept, int threads, size_t smem,
   const uint64_t key = (uint64_t)(dev + 1) << 52 | (uint64_t)threads << 41 | (uint64_t)smem << 21;
   uint64_t word = kept.load(std::memory_order_relaxed);
   if ((word >> 21) != (key >> 21)) {
-    // the same limit in every call: another thread's launch never finds less
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    if (e != cudaSuccess) return e;
+    // 48 KB with the static arrays need no leave. The same limit in every
+    // call: another thread's launch never finds less.
+    if (smem > 40 * 1024) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+      if (e != cudaSuccess) return e;
+    }
     int per_sm = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem);
     if (e != cudaSuccess) return e;
@@ -456,28 +546,44 @@ template <typename T> cudaError_t fwd_t(const RmsNormArgs &a, cudaStream_t s) {
   return fwd<T, 4, false>(a, round32((nvec + 3) / 4), s);
 }
 
-template <typename T, typename TY, typename TX, int NU, bool DH, bool RING>
-cudaError_t bwd(const RmsNormBwdArgs &a, int threads, cudaStream_t s) {
-  auto k = rmsnorm_bwd_kernel<T, TY, TX, NU, DH, RING>;
-  const size_t smem = RING ? (size_t)kStages * NU * threads * bwd_unit_bytes<T, TY>(DH) : 0;
-  static std::atomic<uint64_t> kept{0};
+// A backward kernel on as many CTAs as fit, and the sum of their partial rows.
+template <typename K>
+cudaError_t bwd(K k, std::atomic<uint64_t> &kept, const RmsNormBwdArgs &a, int threads, size_t smem,
+                int64_t most, cudaStream_t s) {
   int64_t grid = 0;
-  cudaError_t e = resident(k, kept, threads, smem, rmsnorm_bwd_max_partials(a.rows), &grid);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(k, dim3((unsigned)grid), dim3(threads), smem, s, a);
+  cudaError_t e = resident(k, kept, threads, smem, most, &grid);
+  if (e == cudaSuccess) e = launch_pdl(k, dim3((unsigned)grid), dim3(threads), smem, s, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(dgamma_kernel, dim3((a.d + 31) / 32), dim3(1024), 0, s, a.partial, (int)grid, a.d,
                     a.dgamma);
 }
 
+template <typename T, typename TY, typename TX, int NU, bool DH>
+cudaError_t bwd_warp(const RmsNormBwdArgs &a, cudaStream_t s) {
+  static std::atomic<uint64_t> kept{0};
+  const int64_t most = rmsnorm_bwd_max_partials((a.rows + kRowWarps - 1) / kRowWarps);
+  return bwd(rmsnorm_bwd_warp_kernel<T, TY, TX, NU, DH>, kept, a, kRowWarps * 32, 0, most, s);
+}
+
+template <typename T, typename TY, typename TX, int NU, bool DH, int STAGES>
+cudaError_t bwd_cta(const RmsNormBwdArgs &a, int threads, cudaStream_t s) {
+  static std::atomic<uint64_t> kept{0};
+  const size_t smem = (size_t)STAGES * NU * threads * bwd_unit_bytes<T, TY>(DH);
+  return bwd(rmsnorm_bwd_kernel<T, TY, TX, NU, DH, STAGES>, kept, a, threads, smem,
+             rmsnorm_bwd_max_partials(a.rows), s);
+}
+
 template <typename T, typename TY, typename TX, bool DH>
 cudaError_t bwd_t(const RmsNormBwdArgs &a, cudaStream_t s) {
   const int nu = a.d / 4;
-  if (nu <= 32) return bwd<T, TY, TX, 1, DH, true>(a, 32, s);
+  if (nu <= 32) return bwd_warp<T, TY, TX, 1, DH>(a, s);
+  if (nu <= 128) return bwd_warp<T, TY, TX, 4, DH>(a, s);
   const int threads = round32((nu + 3) / 4);
-  if (threads <= 512 && (size_t)kStages * 4 * threads * bwd_unit_bytes<T, TY>(DH) <= kSmem)
-    return bwd<T, TY, TX, 4, DH, true>(a, threads, s);
-  return bwd<T, TY, TX, 8, DH, false>(a, round32((nu + 7) / 8), s);
+  const size_t row = (size_t)4 * threads * bwd_unit_bytes<T, TY>(DH);   // of the ring
+  if (threads > 128 && threads <= 512 && 3 * row <= kSmem)
+    return bwd_cta<T, TY, TX, 4, DH, 3>(a, threads, s);
+  if (threads <= 512 && 2 * row <= kSmem) return bwd_cta<T, TY, TX, 4, DH, 2>(a, threads, s);
+  return bwd_cta<T, TY, TX, 8, DH, 0>(a, round32((nu + 7) / 8), s);
 }
 
 template <typename T, typename TY, typename TX>

@@ -117,7 +117,6 @@ class MoELayer:
             self.load = z(n_sub, E, dtype=torch.int32)
             self.prob_mean = z(n_sub, E, dtype=torch.float32)
             self.balance_coef = z(n_sub * E + 1, dtype=torch.float32)
-            self.dlogits = z(T, E, dtype=torch.float32)
         self.logits = z(T, E, dtype=torch.float32)
         self.topk_idx = z(T, K, dtype=torch.int32)
         self.topk_prob = z(T, K, dtype=torch.float32)
@@ -174,6 +173,8 @@ class MoELayer:
             self.db_r = z(E, dtype=torch.float32)
             self.dx_router = z(T, d, dtype=torch.float32)
             self.dx = z(T, d, dtype=torch.float32)
+            if balance:
+                self.dlogits = z(T, E, dtype=torch.float32)
             if self.norm:
                 self.dgamma = z(d, dtype=torch.float32)
                 self.dx_h = z(T, d) if dx_dtype == "act" and dt != torch.float32 else self.dx
