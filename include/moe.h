@@ -358,7 +358,8 @@ moe_status_t moe_route_bwd_add(const moe_shape_t *shape, const void *x, const vo
  * h and y may each be x or residual itself (in place); no other overlap of an
  * output with an input or with another output. rows = 0 does nothing.
  * Statistics are fp32: a row whose squares add up to more than 3.4e38 (|h| of
- * 1e17 and more) gets y = 0; a NaN or infinity in a row spoils that row only.
+ * 1e17 and more) gets y = 0. A row's results depend on that row alone: not on
+ * how many there are, nor on a NaN or infinity in another.
  * Errors: MOE_ERR_INVALID_ARG as above; MOE_ERR_UNSUPPORTED for another group,
  *   d above 32768 (bf16) or 16384 (fp32), or rows >= 2^31.                   */
 moe_status_t moe_rmsnorm(int32_t dtype, int64_t rows, int32_t d, const void *x,

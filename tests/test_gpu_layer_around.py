@@ -63,7 +63,7 @@ def _autograd_step(cfg, layer, w, x, r, dout, dh, mask, dloss):
     total = (out * dout.cpu().double()).sum() + (h * dh.cpu().double()).sum() + dloss * loss
     names = [k for k in P]
     grads = torch.autograd.grad(total, [h] + [P[k] for k in names])
-    return out.detach(), float(loss), grads[0], dict(zip(names, grads[1:]))
+    return out.detach(), loss.item(), grads[0], dict(zip(names, grads[1:]))
 
 
 GRAD = {"gamma": "dgamma", "W_r": "dW_r", "W_gu": "dW_gu", "W_down": "dW_down", "b_r": "db_r", "w_sg": "dw_sg",

@@ -172,10 +172,11 @@ __device__ __forceinline__ float rstd_of(float ss, const RmsNormArgs &a) {
 // the matrices in a narrow window, which DRAM rewards (32768 x 8192 bf16 with
 // residual and 8-bit rows: 359 us, 6.72 TB/s; persistent CTAs with the next
 // rows fetched ahead through shared memory, in 2 to 4 stages: 404 to 414 us).
-// Two vectors a thread: one takes 366 us, four 408 us.
-// 56 registers for two vectors: one fewer than the compiler takes by itself, and
-// a third CTA of 384 threads fits (16384 x 6144: 150 -> 134 us; 32768 x 8192,
-// CTAs of 512: 360 -> 362 us).
+// Two vectors a thread: one takes 366 us, four 408 us (one row alone: 1.7 us on
+// 6144 columns with two, 1.8 with one). 56 registers for two vectors: one fewer
+// than the compiler takes by itself, and a third CTA of 384 threads fits
+// (16384 x 6144: 150 -> 134 us; 32768 x 8192, CTAs of 512: 360 -> 362 us). The
+// layout goes by d alone, so a row's results do not depend on the other rows.
 template <typename T, int NV, bool WARP>
 __global__ void __maxnreg__(WARP ? 80 : NV == 2 ? 56 : 64) rmsnorm_kernel(RmsNormArgs a) {
   constexpr int N = Vec<T>::N;
@@ -538,11 +539,7 @@ template <typename T> cudaError_t fwd_t(const RmsNormArgs &a, cudaStream_t s) {
   if (nvec <= 32) return fwd<T, 1, true>(a, 128, s);
   if (nvec <= 64) return fwd<T, 2, true>(a, 128, s);
   if (nvec <= 128) return fwd<T, 4, true>(a, 128, s);
-  if (nvec <= 2048) {
-    // a row for each SM at most: the most threads a row
-    if (nvec <= 1024 && a.rows <= sm_count()) return fwd<T, 1, false>(a, round32(nvec), s);
-    return fwd<T, 2, false>(a, round32((nvec + 1) / 2), s);
-  }
+  if (nvec <= 2048) return fwd<T, 2, false>(a, round32((nvec + 1) / 2), s);
   return fwd<T, 4, false>(a, round32((nvec + 3) / 4), s);
 }
 
