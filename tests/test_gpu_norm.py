@@ -201,12 +201,14 @@ BWD_TYPES = [(torch.float32, torch.float32, torch.float32), (torch.bfloat16, tor
 @pytest.mark.gpu
 @pytest.mark.parametrize("types", BWD_TYPES, ids=lambda t: "-".join(str(x)[6:] for x in t))
 @pytest.mark.parametrize("rows,d", [(1, 8), (3, 72), (700, 256), (33, 1032), (305, 2048), (5, 3584), (400, 4104),
-                                    (2, 8192), (3, 16384), (1, 32768)])
+                                    (2, 8192), (37, 8200), (200, 12288), (3, 16384), (90, 16392),
+                                    (1, 32768), (77, 32768)])
 def test_backward(rows, d, types):
     L = lib()
     dt, dy_dt, dx_dt = types
     if dt == torch.float32:
-        d = 16384 if d == 32768 else d + (4 if d in (8, 72, 1032, 4104) else 0)
+        d = min(d, 16384)
+        d += 4 if d in (8, 72, 1032, 4104, 8200) else 0
     h, dy, dh = _rows(rows, d, dt, 1, 2.0), _rows(rows, d, dy_dt, 2, 0.3), _rows(rows, d, dt, 3, 0.3)
     gamma = (1 + 0.3 * _rows(1, d, torch.float32, 4)[0]).to(dt)
     rstd = torch.rsqrt(h.float().square().mean(1) + EPS)

@@ -257,7 +257,7 @@ balance_join_kernel(BalanceArgs a, Partials w, int64_t chunks, int slices) {
   const int rank = (int)cluster.block_rank();
   const int E = a.E;
   pdl_wait();
-  __syncthreads();
+  cluster.sync();   // all CTAs run: the first one's shared memory may be written
   uint32_t n = 0;   // at most T < 2^31
   for (int64_t i = rank * kJoinThreads + threadIdx.x; i < chunks * a.n_sub; i += kJoinCtas * kJoinThreads)
     n += w.tokens[i];

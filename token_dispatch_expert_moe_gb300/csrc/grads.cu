@@ -151,6 +151,7 @@ small_norm_kernel(const __grid_constant__ Batch b, float *norm) {
   cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
   __shared__ double red[32], all[kSmallCtas];
   pdl_wait();
+  cluster.sync();   // all CTAs run: the first one's shared memory may be written
   const int rank = (int)cluster.block_rank();
   const double s = squares_of(b, rank, kSmallCtas, red);
   if (threadIdx.x == 0) *cluster.map_shared_rank(&all[rank], 0) = s;

@@ -11,6 +11,7 @@
 //   dx = rstd (g - xhat mean_j(g_j xhat_j)) + dh,  dgamma = sum_rows dy xhat.
 #include <atomic>
 
+#include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
 #include "launch.cuh"
@@ -336,34 +337,50 @@ __global__ void __launch_bounds__(kRowWarps * 32) rmsnorm_bwd_warp_kernel(RmsNor
   for (int j = threadIdx.x; j < a.d; j += blockDim.x) a.partial[(int64_t)blockIdx.x * a.d + j] = sum[j];
 }
 
-// Wider rows: one per CTA.
-// STAGES > 0: a ring of so many rows in shared memory. The next rows' dy, h
-// and dh are on their way while one row is reduced and written, so the loads
-// run on across the reduction's barrier (32768 x 8192, dy and dx fp32, dh
-// bf16: 471 us, 6.83 TB/s; plain loads 821 us). Three rows where they fit and
-// leave one CTA to an SM anyway (16384 x 6144: 177 us, with two 199 us), two
-// where more CTAs fit then (65536 x 1024: 121 us, with three 129 us) and where
-// three do not fit (16384 x 8192, all fp32: 313 us).
-// STAGES = 0, for rows too wide for two: dy and h are read from global memory
-// twice, before and after the row's sum, the second time from the caches
-// (16384 x 16384: 800 us, 4.0 TB/s).
-template <typename T, typename TY, typename TX, int NU, bool DH, int STAGES>
-__global__ void __launch_bounds__(STAGES > 0 ? 512 : 1024) rmsnorm_bwd_kernel(RmsNormBwdArgs a) {
-  constexpr bool RING = STAGES > 0;
+// Wider rows: one per CTA, or per cluster of CTAs with a part of the columns
+// each. A ring of STAGES rows in shared memory: the next rows' dy, h and dh are
+// on their way while one row is reduced and written, so the loads run on across
+// the reduction's barrier (32768 x 8192, dy and dx fp32, dh bf16: 471 us, 6.83
+// TB/s; plain loads 821 us). Three rows where they fit and leave one CTA to an
+// SM anyway (16384 x 6144: 177 us, with two 199 us), two where more CTAs fit
+// then (65536 x 1024: 121 us, with three 129 us) and where three do not fit
+// (16384 x 8192, all fp32: 308 us).
+// WIDE: bf16 rows of more than 8192 columns, 1024 threads. dh goes to registers
+// instead of the ring, and dy and h are read from the ring twice, before and
+// after the row's sum, which leaves room for both (16384 x 16384: 481 us, 6.69
+// TB/s; plain loads that read dy and h twice 800 us, two CTAs a row 613 us).
+// CLUSTER: rows of more than 8192 (fp32) or 16384 (bf16) columns. The CTAs add
+// up their sums through each other's shared memory; that barrier takes 1 us a
+// row, so no narrower row is cut (8192 x 32768: 537 us, 6.0 TB/s).
+constexpr int kMaxCluster = 2, kNarrow = 8192, kWide = 16384;
+
+template <typename T, typename TY, typename TX, bool DH, int STAGES, bool WIDE, bool CLUSTER>
+__global__ void __launch_bounds__(WIDE ? 1024 : 512) rmsnorm_bwd_kernel(RmsNormBwdArgs a) {
   using UT = typename Unit<T>::type;
   using UY = typename Unit<TY>::type;
   using UX = typename Unit<TX>::type;
+  namespace cg = cooperative_groups;
+  constexpr int NU = 4;             // units per thread
   extern __shared__ uint4 ring[];   // per stage: dy [NU][W], h [NU][W], dh [NU][W]
-  __shared__ float red[2][32];
+  __shared__ float red[2][32 * (CLUSTER ? kMaxCluster : 1)];
   int turn = 0;
   pdl_wait();
-  const int W = blockDim.x, id = threadIdx.x, nu = a.d / 4;
-  const UY *dy = reinterpret_cast<const UY *>(a.dy);
-  const UT *h = reinterpret_cast<const UT *>(a.h);
-  const UT *dh = reinterpret_cast<const UT *>(a.dh);
-  UX *dx = reinterpret_cast<UX *>(a.dx);
-  const int64_t step = gridDim.x;
-  const size_t stage_bytes = (size_t)NU * W * bwd_unit_bytes<T, TY>(DH);
+  const int W = blockDim.x, id = threadIdx.x, units = a.d / 4;
+  int ctas = 1, rank = 0;
+  if constexpr (CLUSTER) {
+    ctas = (int)cg::this_cluster().num_blocks();
+    rank = (int)cg::this_cluster().block_rank();
+    cg::this_cluster().sync();   // all of them run: their shared memory may be written
+  }
+  // this CTA's units: [first, first + nu)
+  const int share = (units + ctas - 1) / ctas, first = rank * share;
+  const int nu = min(share, units - first);
+  const UY *dy = reinterpret_cast<const UY *>(a.dy) + first;
+  const UT *h = reinterpret_cast<const UT *>(a.h) + first;
+  const UT *dh = reinterpret_cast<const UT *>(a.dh) + first;
+  UX *dx = reinterpret_cast<UX *>(a.dx) + first;
+  const int64_t row0 = blockIdx.x / ctas, step = gridDim.x / ctas;
+  const size_t stage_bytes = (size_t)NU * W * bwd_unit_bytes<T, TY>(DH && !WIDE);
   auto dy_at = [&](int stage) {
     return reinterpret_cast<UY *>(reinterpret_cast<char *>(ring) + stage * stage_bytes) + id;
   };
@@ -379,35 +396,58 @@ __global__ void __launch_bounds__(STAGES > 0 ? 512 : 1024) rmsnorm_bwd_kernel(Rm
       for (int i = 0; i < NU; ++i) {
         const int u = id + i * W;
         if (u < nu) {
-          copy_async<sizeof(UY)>(sy + i * W, dy + row * nu + u);
-          copy_async<sizeof(UT)>(sh + i * W, h + row * nu + u);
-          if (DH) copy_async<sizeof(UT)>(sh + (NU + i) * W, dh + row * nu + u);
+          copy_async<sizeof(UY)>(sy + i * W, dy + row * units + u);
+          copy_async<sizeof(UT)>(sh + i * W, h + row * units + u);
+          if (DH && !WIDE) copy_async<sizeof(UT)>(sh + (NU + i) * W, dh + row * units + u);
         }
       }
     }
-    copy_commit();
+    copy_commit();   // an empty group past the end keeps the count
   };
-  if (RING) {
+  // sum over the row's CTAs of a value per thread
+  auto row_sum = [&](float v) {
+    if constexpr (!CLUSTER) {
+      return cta_reduce<false>(v, red, turn);
+    } else {
+      v = warp_reduce<false>(v);
+      const int lane = id & 31, slot = rank * 32 + (id >> 5);
+      if (lane < ctas) *cg::this_cluster().map_shared_rank(&red[turn][slot], lane) = v;
+      cg::this_cluster().sync();
+      const bool in = lane < (W >> 5);
+      v = 0.0f;
+      for (int r = 0; r < ctas; ++r) v += in ? red[turn][r * 32 + lane] : 0.0f;
+      turn ^= 1;
+      return warp_reduce<false>(v);
+    }
+  };
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) fetch(blockIdx.x + s * step, s);
-  }
+  for (int s = 0; s < STAGES - 1; ++s) fetch(row0 + s * step, s);
   UT g[NU];
   float acc[NU][4];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int u = id + i * W;
-    g[i] = u < nu ? reinterpret_cast<const UT *>(a.gamma)[u] : UT{};
+    g[i] = u < nu ? (reinterpret_cast<const UT *>(a.gamma) + first)[u] : UT{};
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
   }
   int stage = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += step) {
+  for (int64_t row = row0; row < a.rows; row += step) {
     const float rstd = a.rstd[row];
+    // the stage read one row ago is free: its values have gone into that row's dx
+    fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+    copy_wait<STAGES - 1>();   // this row's group
+    UT dv[NU];
+    if (DH && WIDE) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+        if (id + i * W < nu) dv[i] = dh[row * units + id + i * W];
+    }
     float xh[NU][4], gy[NU][4];   // xhat and dy gamma
-    auto read = [&](int i, int u, float (&y4)[4]) {
-      unpack4(RING ? dy_at(stage)[i * W] : dy[row * nu + u], y4);
-      unpack4(RING ? h_at(stage)[i * W] : h[row * nu + u], xh[i]);
+    auto read = [&](int i, float (&y4)[4]) {
       float gv[4];
+      unpack4(dy_at(stage)[i * W], y4);
+      unpack4(h_at(stage)[i * W], xh[i]);
       unpack4(g[i], gv);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -415,18 +455,12 @@ __global__ void __launch_bounds__(STAGES > 0 ? 512 : 1024) rmsnorm_bwd_kernel(Rm
         gy[i][k] = y4[k] * gv[k];
       }
     };
-    if (RING) {
-      // the stage read one row ago is free: its values have gone into that row's dx
-      fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
-      copy_wait<RING ? STAGES - 1 : 0>();   // this row's group
-    }
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const int u = id + i * W;
-      if (u < nu) {
+      if (id + i * W < nu) {
         float y4[4];
-        read(i, u, y4);
+        read(i, y4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           acc[i][k] = fmaf(y4[k], xh[i][k], acc[i][k]);
@@ -434,9 +468,8 @@ __global__ void __launch_bounds__(STAGES > 0 ? 512 : 1024) rmsnorm_bwd_kernel(Rm
         }
       }
     }
-    const float m = cta_reduce<false>(dot, red, turn) * a.inv_d;
-    UT dv[NU];
-    if (RING && DH) {
+    const float m = row_sum(dot) * a.inv_d;
+    if (DH && !WIDE) {
 #pragma unroll
       for (int i = 0; i < NU; ++i) dv[i] = h_at(stage)[(NU + i) * W];
     }
@@ -444,10 +477,9 @@ __global__ void __launch_bounds__(STAGES > 0 ? 512 : 1024) rmsnorm_bwd_kernel(Rm
     for (int i = 0; i < NU; ++i) {
       const int u = id + i * W;
       if (u < nu) {
-        if (!RING) {
+        if (WIDE) {   // not kept across the barrier
           float y4[4];
-          read(i, u, y4);
-          if (DH) dv[i] = dh[row * nu + u];
+          read(i, y4);
         }
         float o[4];
 #pragma unroll
@@ -458,18 +490,19 @@ __global__ void __launch_bounds__(STAGES > 0 ? 512 : 1024) rmsnorm_bwd_kernel(Rm
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[k] += d4[k];
         }
-        pack4(o, dx + row * nu + u);
+        pack4(o, dx + row * units + u);
       }
     }
     stage = stage == STAGES - 1 ? 0 : stage + 1;
   }
-  if (RING) copy_wait<0>();
-  float *part = a.partial + (int64_t)blockIdx.x * a.d;
+  copy_wait<0>();
+  float4 *part = reinterpret_cast<float4 *>(a.partial + row0 * a.d) + first;
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int u = id + i * W;
-    if (u < nu) pack4(acc[i], reinterpret_cast<float4 *>(part) + u);
+    if (u < nu) pack4(acc[i], part + u);
   }
+  if constexpr (CLUSTER) cg::this_cluster().sync();   // no CTA ends while another writes to it
 }
 
 // dgamma[j] = sum over the CTAs' partial rows, in a fixed order: 32 columns
@@ -543,13 +576,16 @@ template <typename T> cudaError_t fwd_t(const RmsNormArgs &a, cudaStream_t s) {
   return fwd<T, 4, false>(a, round32((nvec + 3) / 4), s);
 }
 
-// A backward kernel on as many CTAs as fit, and the sum of their partial rows.
+// A backward kernel on as many clusters of CTAs as fit, and the sum of their
+// partial rows.
 template <typename K>
-cudaError_t bwd(K k, std::atomic<uint64_t> &kept, const RmsNormBwdArgs &a, int threads, size_t smem,
-                int64_t most, cudaStream_t s) {
+cudaError_t bwd(K k, std::atomic<uint64_t> &kept, const RmsNormBwdArgs &a, int threads, int cluster,
+                size_t smem, int64_t most, cudaStream_t s) {
   int64_t grid = 0;
-  cudaError_t e = resident(k, kept, threads, smem, most, &grid);
-  if (e == cudaSuccess) e = launch_pdl(k, dim3((unsigned)grid), dim3(threads), smem, s, a);
+  cudaError_t e = resident(k, kept, threads, smem, most * cluster, &grid);
+  grid /= cluster;
+  if (e == cudaSuccess)
+    e = launch_pdl_clusters(k, dim3((unsigned)(grid * cluster)), dim3(threads), cluster, smem, s, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(dgamma_kernel, dim3((a.d + 31) / 32), dim3(1024), 0, s, a.partial, (int)grid, a.d,
                     a.dgamma);
@@ -559,28 +595,36 @@ template <typename T, typename TY, typename TX, int NU, bool DH>
 cudaError_t bwd_warp(const RmsNormBwdArgs &a, cudaStream_t s) {
   static std::atomic<uint64_t> kept{0};
   const int64_t most = rmsnorm_bwd_max_partials((a.rows + kRowWarps - 1) / kRowWarps);
-  return bwd(rmsnorm_bwd_warp_kernel<T, TY, TX, NU, DH>, kept, a, kRowWarps * 32, 0, most, s);
+  return bwd(rmsnorm_bwd_warp_kernel<T, TY, TX, NU, DH>, kept, a, kRowWarps * 32, 1, 0, most, s);
 }
 
-template <typename T, typename TY, typename TX, int NU, bool DH, int STAGES>
-cudaError_t bwd_cta(const RmsNormBwdArgs &a, int threads, cudaStream_t s) {
+template <typename T, typename TY, typename TX, bool DH, int STAGES, bool WIDE, bool CLUSTER>
+cudaError_t bwd_cta(const RmsNormBwdArgs &a, cudaStream_t s) {
   static std::atomic<uint64_t> kept{0};
-  const size_t smem = (size_t)STAGES * NU * threads * bwd_unit_bytes<T, TY>(DH);
-  return bwd(rmsnorm_bwd_kernel<T, TY, TX, NU, DH, STAGES>, kept, a, threads, smem,
+  const int cluster = CLUSTER ? kMaxCluster : 1;
+  const int threads = round32(((a.d / 4 + cluster - 1) / cluster + 3) / 4);
+  const size_t smem = (size_t)STAGES * 4 * threads * bwd_unit_bytes<T, TY>(DH && !WIDE);
+  return bwd(rmsnorm_bwd_kernel<T, TY, TX, DH, STAGES, WIDE, CLUSTER>, kept, a, threads, cluster, smem,
              rmsnorm_bwd_max_partials(a.rows), s);
 }
 
 template <typename T, typename TY, typename TX, bool DH>
 cudaError_t bwd_t(const RmsNormBwdArgs &a, cudaStream_t s) {
-  const int nu = a.d / 4;
-  if (nu <= 32) return bwd_warp<T, TY, TX, 1, DH>(a, s);
-  if (nu <= 128) return bwd_warp<T, TY, TX, 4, DH>(a, s);
-  const int threads = round32((nu + 3) / 4);
-  const size_t row = (size_t)4 * threads * bwd_unit_bytes<T, TY>(DH);   // of the ring
-  if (threads > 128 && threads <= 512 && 3 * row <= kSmem)
-    return bwd_cta<T, TY, TX, 4, DH, 3>(a, threads, s);
-  if (threads <= 512 && 2 * row <= kSmem) return bwd_cta<T, TY, TX, 4, DH, 2>(a, threads, s);
-  return bwd_cta<T, TY, TX, 8, DH, 0>(a, round32((nu + 7) / 8), s);
+  static_assert(2 * kNarrow * bwd_unit_bytes<float, float>(true) / 4 <= kSmem, "two narrow rows fit");
+  static_assert(2 * kWide * bwd_unit_bytes<__nv_bfloat16, float>(false) / 4 <= kSmem, "two wide rows fit");
+  if (a.d <= 128) return bwd_warp<T, TY, TX, 1, DH>(a, s);
+  if (a.d <= 512) return bwd_warp<T, TY, TX, 4, DH>(a, s);
+  if (a.d <= kNarrow) {
+    const size_t row = (size_t)round32((a.d / 4 + 3) / 4) * 4 * bwd_unit_bytes<T, TY>(DH);
+    return a.d > 2048 && 3 * row <= kSmem ? bwd_cta<T, TY, TX, DH, 3, false, false>(a, s)
+                                          : bwd_cta<T, TY, TX, DH, 2, false, false>(a, s);
+  }
+  if constexpr (sizeof(T) == 4) {
+    return bwd_cta<T, TY, TX, DH, 2, false, true>(a, s);
+  } else {
+    return a.d <= kWide ? bwd_cta<T, TY, TX, DH, 2, true, false>(a, s)
+                        : bwd_cta<T, TY, TX, DH, 2, true, true>(a, s);
+  }
 }
 
 template <typename T, typename TY, typename TX>
