@@ -442,8 +442,7 @@ typedef struct {
  * squares), fp32, right wherever that is an fp32 number (squares outside the
  * fp32 range are added in fp64); NaN or infinity among the gradients gives a
  * norm that is not finite; an empty list gives 0. `grads` is a HOST array and
- * is read before the call returns. A tensor may be listed once only if it is
- * to count once.                                                            */
+ * is read before the call returns. A tensor that is listed twice counts twice. */
 moe_status_t moe_grad_norm(int32_t n, const moe_tensor_t *grads, float *norm, void *ws,
                            size_t ws_bytes, moe_stream_t stream);
 
@@ -454,8 +453,9 @@ moe_status_t moe_grad_norm(int32_t n, const moe_tensor_t *grads, float *norm, vo
  *   max_norm >= 0 (finite); out: NULL for in place, or n tensors of the same
  *   sizes and types, each of which is its gradient itself or does not overlap
  *   any gradient; coef [1] fp32 or NULL receives coef. In place with coef = 1
- *   nothing is read or written. Both arrays are HOST arrays.
- *   norm and coef are not among the tensors.                                 */
+ *   nothing is read or written. Both arrays are HOST arrays. No output
+ *   overlaps another, so in place no tensor is listed twice; norm and coef lie
+ *   in none of them.                                                         */
 moe_status_t moe_grad_clip(int32_t n, const moe_tensor_t *grads, const moe_tensor_t *out,
                            const float *norm, float max_norm, float *coef,
                            moe_stream_t stream);

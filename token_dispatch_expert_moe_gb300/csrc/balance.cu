@@ -63,9 +63,11 @@ Split split_of(int64_t T, int64_t S, int lanes) {
 // quad v of lane `sub` starts at expert 4 (sub + v L), so that the lanes read
 // consecutive 16 bytes. At most 4 lanes: the row's maximum and sum take two
 // shuffles each, and a lane's 16 exponentials overlap (262144 x 64, loss and
-// gradient: 16.5 and 22.2 us; 8 lanes of two quads 20.6 and 23.4 us, 16 lanes
+// gradient: 16.5 and 20.7 us; 8 lanes of two quads 20.6 and 23.4 us, 16 lanes
 // of one 31.1 and 29.4 us). Bound by instruction issue more than by HBM: half
-// the issue slots and half the bandwidth are in use.
+// the issue slots and half the bandwidth are in use; logits fetched two tokens
+// ahead through shared memory took 10 % more.
+
 // A row of E values, l[4 v + i] of expert 4 (sub + v L) + i: `none` past E, and
 // throughout where `in` is false (nothing is read then).
 template <int L, int V>

@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rmsnorm_bwd_warp_kernel(RmsNor
 // Wider rows: one per CTA, or per cluster of CTAs with a part of the columns
 // each. A ring of STAGES rows in shared memory: the next rows' dy, h and dh are
 // on their way while one row is reduced and written, so the loads run on across
-// the reduction's barrier (32768 x 8192, dy and dx fp32, dh bf16: 471 us, 6.83
+// the reduction's barrier (32768 x 8192, dy and dx fp32, dh bf16: 480 us, 6.7
 // TB/s; plain loads 821 us). Three rows where they fit and leave one CTA to an
 // SM anyway (16384 x 6144: 177 us, with two 199 us), two where more CTAs fit
 // then (65536 x 1024: 121 us, with three 129 us) and where three do not fit
