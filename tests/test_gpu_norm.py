@@ -55,11 +55,9 @@ def _forward(L, x, r, gamma, group=None, y=True, h=True, stream=None):
         ng = 1 if group == 0 else -(-d // group)
         raw["q"], out["q"] = _guarded(rows, d, torch.float8_e4m3fn)
         raw["s"], out["s"] = _guarded(rows, ng, torch.float32)
-    # a row of sentinels in front keeps 16-byte alignment only for row sizes that are multiples of it
-    for k in ("q",):
-        if k in out and out[k].data_ptr() % 16:
-            raw[k] = out[k] = torch.zeros(rows, d, dtype=torch.float8_e4m3fn, device="cuda")
-            raw.pop(k)
+        if out["q"].data_ptr() % 16:   # rows of 8 (mod 16) bytes: no sentinels in front
+            del raw["q"]
+            out["q"] = torch.zeros(rows, d, dtype=torch.float8_e4m3fn, device="cuda")
     L.moe_rmsnorm(_code(L, dt), rows, d, x, r, gamma, EPS, out.get("h"), out.get("y"), out.get("q"),
                   out.get("s"), group or 0, out["rstd"], stream)
     torch.cuda.synchronize()
