@@ -328,7 +328,7 @@ moe_status_t moe_route_bwd(const moe_shape_t *shape, const void *x, const void *
 /* moe_route_bwd with the gradient of a loss on the logits: dl gains
  * dlogits_add [T,E] fp32 (for instance from moe_balance_loss_bwd) before dW_r,
  * db_r and dx_router are formed from it. Other arguments and errors as
- * moe_route_bwd; dlogits_add must not be NULL.                               */
+ * moe_route_bwd; dlogits_add must not be NULL nor overlap logits.            */
 moe_status_t moe_route_bwd_add(const moe_shape_t *shape, const void *x, const void *W_r,
                                const void *w_sg, const float *logits,
                                const int32_t *topk_idx, const float *topk_prob,
@@ -411,7 +411,8 @@ moe_status_t moe_balance_loss(const moe_shape_t *shape, const float *logits,
 /* dlogits[t,e] = dloss * d loss / d logits[t,e] (the counts are constants; 0
  * for padding), for moe_route_bwd_add. logits, mask, coef as in
  * moe_balance_loss; dloss [1] fp32 on the device, or NULL for 1; dlogits [T,E]
- * fp32, which may be logits itself.                                          */
+ * fp32, which may be logits itself where nothing reads the logits after this
+ * (moe_route_bwd_add does).                                                  */
 moe_status_t moe_balance_loss_bwd(const moe_shape_t *shape, const float *logits,
                                   const uint8_t *mask, const float *coef, const float *dloss,
                                   float *dlogits, moe_stream_t stream);

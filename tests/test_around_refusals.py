@@ -87,9 +87,16 @@ def test_balance(L):
     for kw in (dict(shape=_shape(L, E=0)), dict(logits=None), dict(coef=None), dict(dl=None), dict(dl=A[2] + 4),
                dict(dloss=A[3] + 2), dict(dl=A[0] + 16), dict(coef=A[1] + 8)):
         back(1, **kw)
-    fake = A[0]
-    refused(L, 1, "moe_route_bwd_add", _shape(L), fake, fake, None, fake, fake, fake, fake, fake, None, None, None, fake,
-            None, None, fake, fake, 0)
+
+    def route(add, logits=A[2], shape=None):
+        refused(L, 1, "moe_route_bwd_add", shape or _shape(L), A[0], A[1], None, logits, A[3], A[4], A[5], A[6], None, add,
+                None, A[7], None, None, A[8], A[9], 0)
+
+    route(None)
+    route(A[10] + 2)
+    route(A[2])              # the logits themselves, overwritten by moe_balance_loss_bwd
+    route(A[2] + 64 * 8 * 4 - 4)
+    route(A[10], shape=_shape(L, E=65))
 
 
 def test_permute_e4m3(L):

@@ -386,6 +386,12 @@ moe_status_t moe_sum_partials(int32_t dtype, int32_t n_parts, int64_t rows, int3
                                          (cudaStream_t)stream));
 }
 
+static bool overlap(const void *p, size_t np, const void *q, size_t nq) {
+  if (p == nullptr || q == nullptr) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + nq && b < a + np;
+}
+
 static moe_status_t route_bwd(const moe_shape_t *shape, const void *x, const void *W_r,
                               const void *w_sg, const float *logits, const int32_t *topk_idx,
                               const float *topk_prob, const float *topk_w, const float *dw,
@@ -430,19 +436,15 @@ moe_status_t moe_route_bwd_add(const moe_shape_t *shape, const void *x, const vo
                                float *dW_r, float *db_r, float *dw_sg, float *dx_router, void *ws,
                                moe_stream_t stream) {
   NvtxRange trace("moe_route_bwd_add");
-  if (!dlogits_add || !aligned4(dlogits_add)) return MOE_ERR_INVALID_ARG;
+  if (!shape_ok(shape) || !dlogits_add || !aligned4(dlogits_add)) return MOE_ERR_INVALID_ARG;
+  const size_t n = (size_t)shape->T * shape->E * sizeof(float);
+  if (overlap(dlogits_add, n, logits, n)) return MOE_ERR_INVALID_ARG;   // both are read
   return route_bwd(shape, x, W_r, w_sg, logits, topk_idx, topk_prob, topk_w, dw, dz, dlogits_add,
                    dx_in, dW_r, db_r, dw_sg, dx_router, ws, stream);
 }
 
 // ---------------------------------------------------------------------------
 // Around the layer
-
-static bool overlap(const void *p, size_t np, const void *q, size_t nq) {
-  if (p == nullptr || q == nullptr) return false;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + nq && b < a + np;
-}
 
 static bool dtype_ok(int32_t dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
 static size_t size_of(int32_t dtype) { return dtype == MOE_BF16 ? 2 : 4; }

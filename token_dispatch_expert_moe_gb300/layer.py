@@ -49,8 +49,8 @@ class MoELayer:
 
     With a weight "gamma" [d] (in the layer's dtype) the layer is pre-normed:
     forward(x, residual) first forms h = x + residual (kept in self.h, the
-    residual stream that goes on beside the output) and runs the MoE layer on
-    its RMS norm; backward(dout, dh=...) takes the gradient that reaches h from
+    residual stream that goes on beside the output; without a residual self.h
+    is x, which the backward reads) and runs the MoE layer on its RMS norm; backward(dout, dh=...) takes the gradient that reaches h from
     elsewhere and gives "dx", the gradient of h (so of x and residual alike),
     and "dgamma". dx_dtype="act" gives dx in the layer's dtype instead of
     fp32, which is what the layer below takes as its dout and dh.
