@@ -148,9 +148,10 @@ def test_beyond_32_bits_of_elements():
 
 
 @pytest.mark.gpu
-def test_streams_graphs_and_repeats():
+@pytest.mark.parametrize("n", [3000, 300_000])   # in one launch, and in two
+def test_streams_graphs_and_repeats(n):
     L = lib()
-    host, dev, _ = _list([(300_000, F32, 0), (12345, B16, 1)])
+    host, dev, _ = _list([(n, F32, 0), (12345, B16, 1)])
     tl = L.TensorList(dev)
     out = [torch.empty_like(t) for t in dev]
     to = L.TensorList(out)

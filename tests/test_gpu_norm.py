@@ -271,11 +271,12 @@ def test_backward_in_place_repeatable_and_empty():
 
 
 @pytest.mark.gpu
-def test_on_another_stream_and_captured():
+@pytest.mark.parametrize("d", [256, 1024, 4096, 16384, 32768])   # each kernel of the backward
+def test_on_another_stream_and_captured(d):
     """On a side stream, and in two graphs that share the workspace and are
     replayed one after the other with new contents."""
     L = lib()
-    rows, d = 65, 1024
+    rows = 65
     dt = torch.bfloat16
     x, gamma = _rows(rows, d, dt, 1).cuda(), _rows(1, d, dt, 2)[0].cuda()
     dy, dh = _rows(rows, d, torch.float32, 3).cuda(), _rows(rows, d, dt, 4).cuda()
