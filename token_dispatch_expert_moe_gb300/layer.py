@@ -50,10 +50,11 @@ class MoELayer:
     With a weight "gamma" [d] (in the layer's dtype) the layer is pre-normed:
     forward(x, residual) first forms h = x + residual (kept in self.h, the
     residual stream that goes on beside the output; without a residual self.h
-    is x, which the backward reads) and runs the MoE layer on its RMS norm; backward(dout, dh=...) takes the gradient that reaches h from
-    elsewhere and gives "dx", the gradient of h (so of x and residual alike),
-    and "dgamma". dx_dtype="act" gives dx in the layer's dtype instead of
-    fp32, which is what the layer below takes as its dout and dh.
+    is x, which the backward reads) and runs the MoE layer on its RMS norm;
+    backward(dout, dh=...) takes the gradient that reaches h from elsewhere
+    and gives "dx", the gradient of h (so of x and residual alike), and
+    "dgamma". dx_dtype="act" gives dx in the layer's dtype instead of fp32,
+    which is what the layer below takes as its dout and dh.
 
     dispatch="e4m3" (with gamma; compact layout, no gather) moves the routed
     experts' rows in 8 bits with one scale per 128 columns: the norm writes
@@ -64,7 +65,11 @@ class MoELayer:
     it in self.loss ([1], on the device) and the pre-drop counts per
     sub-sequence and expert in self.load; forward's mask ([T] uint8, 0 =
     padding) takes tokens out of it; backward adds its gradient, times dloss
-    ([1] on the device) if given, to the router's."""
+    ([1] on the device) if given, to the router's.
+
+    x, residual, dout and dh are [T, d] (or [..., d]) in the layer's dtype,
+    dense, on the layer's device; a tensor of another kind is refused with a
+    ValueError before anything is launched."""
 
     def __init__(self, cfg, weights: dict, device="cuda", backward=None, etp: int = 1,
                  layout: str = "compact", gather: bool = False, norm_eps: float = 1e-6,
@@ -104,6 +109,7 @@ class MoELayer:
         z = lambda *s, dtype=dt: torch.empty(*s, dtype=dtype, device=device)  # noqa: E731
         self.ws = torch.zeros(L.moe_workspace_size(self.shape), dtype=torch.uint8, device=device)
         if self.norm:
+            self._take("gamma", weights["gamma"], (dt,), d)
             self.h_own = z(T, d)   # x + residual; without a residual h is x
             self.y = z(T, d)
             self.rstd = z(T, dtype=torch.float32)
@@ -193,12 +199,30 @@ class MoELayer:
 
         self.grads = None   # the weight gradients' list, made by the first clip_grads
 
+    def _take(self, name, t, dtypes, numel, last=None, more=False, hint=""):
+        """Refuses a tensor that the kernels would misread: another type, size (`more`: a longer one serves, its front
+        is read), last dimension (of more than one), layout or device. None and raw pointers pass."""
+        if not isinstance(t, torch.Tensor):
+            return
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name} is {t.dtype}, not {' or '.join(map(str, dtypes))}{hint}")
+        if t.numel() < numel or (t.numel() > numel and not more) or (last and t.dim() > 1 and t.shape[-1] != last):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}: {numel} elements"
+                             + (f" in rows of {last}" if last else "") + " are wanted")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
+        if t.device != self.ws.device:
+            raise ValueError(f"{name} is on {t.device}, the layer on {self.ws.device}")
+
     def forward(self, x: torch.Tensor, stream=None, residual=None, mask=None) -> torch.Tensor:
         c, s, w = self.cfg, self.shape, self.w
         if residual is not None and not self.norm:
             raise ValueError("a residual needs the norm (weight gamma)")
         if mask is not None and not self.balance:
             raise ValueError("a mask needs the balance loss")
+        self._take("x", x, (self.dt,), c.T * c.d, more=True)
+        self._take("residual", residual, (self.dt,), c.T * c.d, last=c.d)
+        self._take("mask", mask, (torch.uint8, torch.bool, torch.int8), c.T)
         if self.norm:
             self.h = x if residual is None else self.h_own
             L.moe_rmsnorm(self.dtype_code, c.T, c.d, x, residual, w["gamma"], self.norm_eps,
@@ -270,6 +294,10 @@ class MoELayer:
             raise ValueError("dh needs the norm (weight gamma)")
         if dloss is not None and not self.balance:
             raise ValueError("dloss needs the balance loss")
+        hint = ' (a layer gives its dx in that type with dx_dtype="act")' if self.dt != torch.float32 else ""
+        self._take("dout", dout, (self.dt,), c.T * c.d, more=True, hint=hint)
+        self._take("dh", dh, (self.dt,), c.T * c.d, last=c.d, hint=hint)
+        self._take("dloss", dloss, (torch.float32,), 1)
 
         def mark(name, i):
             if name in marks:
