@@ -131,3 +131,19 @@ def test_gamma(calls):
                 torch.ones(cfg.d, dtype=BF16, device="meta")):
         with pytest.raises(ValueError):
             MoELayer(cfg, {**_weights(cfg), "gamma": bad}, device="cpu")
+
+
+def test_dx_put_in_another_buffer(calls):
+    """layer.dx may be replaced between steps (a ring of outputs): the normed
+    layer's gradient lands there, in fp32."""
+    from token_dispatch_expert_moe_gb300 import _lib
+    cfg, layer = _layer("bf16")
+    x = torch.zeros(cfg.T, cfg.d, dtype=BF16)
+    layer.forward(x)
+    for _ in range(2):
+        mine = layer.dx = torch.zeros(cfg.T, cfg.d)
+        del calls[:]
+        g = layer.backward(x)
+        args = dict(calls)["moe_rmsnorm_bwd"]
+        assert g["dx"] is mine
+        assert args[2] == _lib.MOE_F32 and args[5] == args[10] == mine.data_ptr()

@@ -183,7 +183,8 @@ class MoELayer:
                 self.dlogits = z(T, E, dtype=torch.float32)
             if self.norm:
                 self.dgamma = z(d, dtype=torch.float32)
-                self.dx_h = z(T, d) if dx_dtype == "act" and dt != torch.float32 else self.dx
+                # None: dx itself, in place
+                self.dx_h = z(T, d) if dx_dtype == "act" and dt != torch.float32 else None
                 self.norm_ws = z(L.moe_rmsnorm_bwd_workspace_size(T, d), dtype=torch.uint8)
             self.grad_ws = z(L.MOE_GRAD_NORM_WORKSPACE_BYTES, dtype=torch.uint8)
             self.grad_norm = z(1, dtype=torch.float32)
@@ -337,8 +338,10 @@ class MoELayer:
         dx = self.dx
         if self.norm:
             mark("norm_bwd", 0)
-            dx = self.dx_h   # self.dx itself, in place, unless dx leaves in the layer's dtype
-            L.moe_rmsnorm_bwd(self.dtype_code, L.MOE_F32, self.dtype_code if dx is not self.dx else L.MOE_F32,
+            code = L.MOE_F32
+            if self.dx_h is not None:   # dx leaves in the layer's dtype
+                dx, code = self.dx_h, self.dtype_code
+            L.moe_rmsnorm_bwd(self.dtype_code, L.MOE_F32, code,
                               c.T, c.d, self.dx, self.h, w["gamma"], self.rstd, dh, dx, self.dgamma,
                               self.norm_ws, stream)
             mark("norm_bwd", 1)
