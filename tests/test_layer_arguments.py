@@ -147,3 +147,24 @@ def test_dx_put_in_another_buffer(calls):
         args = dict(calls)["moe_rmsnorm_bwd"]
         assert g["dx"] is mine
         assert args[2] == _lib.MOE_F32 and args[5] == args[10] == mine.data_ptr()
+
+
+def test_clipping_follows_the_gradients_buffers(calls, L, monkeypatch):  # noqa: F811
+    """A gradient put in another buffer after a first clip_grads is the one
+    that is clipped."""
+    listed = []
+
+    class List:
+        def __init__(self, tensors):
+            self.tensors = list(tensors)
+            listed.append([t.data_ptr() for t in self.tensors])
+            self.n, self.address, self.device = len(self.tensors), 0, None
+
+    monkeypatch.setattr(L, "TensorList", List)
+    cfg, layer = _layer("bf16")
+    layer.clip_grads(1.0)
+    layer.clip_grads(1.0)
+    assert len(listed) == 1   # the list is laid out once
+    layer.dW_gu = torch.zeros_like(layer.dW_gu)
+    layer.clip_grads(1.0)
+    assert len(listed) == 2 and listed[1] == [t.data_ptr() for t in layer.weight_grads()]

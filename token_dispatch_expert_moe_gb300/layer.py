@@ -372,8 +372,10 @@ class MoELayer:
         """Clips the weight gradients in place to a global norm of max_norm and
         returns their norm before it, [1] on the device; a norm that is not
         finite leaves them as they are."""
-        if self.grads is None:
-            self.grads = L.TensorList(self.weight_grads())
+        now = self.weight_grads()
+        old = [] if self.grads is None else self.grads.tensors
+        if len(now) != len(old) or any(a is not b for a, b in zip(now, old)):
+            self.grads = L.TensorList(now)   # the first call, or a buffer was replaced
         L.moe_grad_norm(self.grads, self.grad_norm, self.grad_ws, stream)
         L.moe_grad_clip(self.grads, None, self.grad_norm, max_norm, None, stream)
         return self.grad_norm
