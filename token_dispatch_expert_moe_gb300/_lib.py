@@ -174,22 +174,22 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _dense(t):
-    """_ptr of a tensor that has to be contiguous: the operators around the layer
-    know no strides."""
-    if t is None or t.__class__ is int:
-        return t
-    if not t.is_contiguous():
-        raise ValueError(f"a tensor of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
-    return t.data_ptr()
-
-
-def _here(t):
-    """_dense of a call's first tensor, which says where its tensors lie: it has to
-    be the current device, whose stream the call takes."""
-    if t is not None and t.__class__ is not int and t.get_device() != _current_device():
-        raise ValueError(f"a tensor on {t.device}: the current CUDA device is wanted")
-    return _dense(t)
+def _pointers(*tensors):
+    """Addresses of a call's tensors: all of them contiguous (the operators around
+    the layer know no strides) and on the current device, whose stream the call
+    takes. None and raw pointers pass as they are."""
+    current, out = None, []
+    for t in tensors:
+        if t is not None and t.__class__ is not int:
+            if current is None:
+                current = _current_device()
+            if t.get_device() != current:
+                raise ValueError(f"a tensor of shape {tuple(t.shape)} on {t.device}: the current CUDA device is wanted")
+            if not t.is_contiguous():
+                raise ValueError(f"a tensor of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
+            t = t.data_ptr()
+        out.append(t)
+    return out
 
 
 def _call(name, *args):
@@ -304,16 +304,16 @@ def moe_route_bwd(shape, x, W_r, w_sg, logits, topk_idx, topk_prob, topk_w, dw, 
 
 def moe_route_bwd_add(shape, x, W_r, w_sg, logits, topk_idx, topk_prob, topk_w, dw, dz, dlogits_add,
                       dx_in, dW_r, db_r, dw_sg, dx_router, ws, stream=None):
-    _call("moe_route_bwd_add", ctypes.byref(shape), _here(x), _dense(W_r), _dense(w_sg),
-          _dense(logits), _dense(topk_idx), _dense(topk_prob), _dense(topk_w), _dense(dw), _dense(dz),
-          _dense(dlogits_add), _dense(dx_in), _dense(dW_r), _dense(db_r), _dense(dw_sg),
-          _dense(dx_router), _dense(ws), _stream(stream))
+    _call("moe_route_bwd_add", ctypes.byref(shape),
+          *_pointers(x, W_r, w_sg, logits, topk_idx, topk_prob, topk_w, dw, dz, dlogits_add, dx_in,
+                     dW_r, db_r, dw_sg, dx_router, ws), _stream(stream))
 
 
 def moe_rmsnorm(dtype, rows, d, x, residual, gamma, eps, h, y, q, q_scale, group, rstd,
                 stream=None):
-    _call("moe_rmsnorm", dtype, rows, d, _here(x), _dense(residual), _dense(gamma), eps, _dense(h),
-          _dense(y), _dense(q), _dense(q_scale), group, _dense(rstd), _stream(stream))
+    x, residual, gamma, h, y, q, q_scale, rstd = _pointers(x, residual, gamma, h, y, q, q_scale, rstd)
+    _call("moe_rmsnorm", dtype, rows, d, x, residual, gamma, eps, h, y, q, q_scale, group, rstd,
+          _stream(stream))
 
 
 def moe_rmsnorm_bwd_workspace_size(rows: int, d: int) -> int:
@@ -325,26 +325,26 @@ def moe_rmsnorm_bwd(dtype, dy_dtype, dx_dtype, rows, d, dy, h, gamma, rstd, dh, 
     """ws: a device tensor (its size becomes ws_bytes) or a pointer with ws_bytes."""
     if ws_bytes is None:
         ws_bytes = ws.nbytes
-    _call("moe_rmsnorm_bwd", dtype, dy_dtype, dx_dtype, rows, d, _here(dy), _dense(h), _dense(gamma),
-          _dense(rstd), _dense(dh), _dense(dx), _dense(dgamma), _dense(ws), ws_bytes, _stream(stream))
+    _call("moe_rmsnorm_bwd", dtype, dy_dtype, dx_dtype, rows, d,
+          *_pointers(dy, h, gamma, rstd, dh, dx, dgamma, ws), ws_bytes, _stream(stream))
 
 
 def moe_balance_loss(shape, logits, topk_idx, mask, alpha, loss, counts, prob_mean, coef, ws,
                      stream=None):
-    _call("moe_balance_loss", ctypes.byref(shape), _here(logits), _dense(topk_idx), _dense(mask), alpha,
-          _dense(loss), _dense(counts), _dense(prob_mean), _dense(coef), _dense(ws), _stream(stream))
+    logits, topk_idx, mask, *outs = _pointers(logits, topk_idx, mask, loss, counts, prob_mean, coef, ws)
+    _call("moe_balance_loss", ctypes.byref(shape), logits, topk_idx, mask, alpha, *outs,
+          _stream(stream))
 
 
 def moe_balance_loss_bwd(shape, logits, mask, coef, dloss, dlogits, stream=None):
-    _call("moe_balance_loss_bwd", ctypes.byref(shape), _here(logits), _dense(mask), _dense(coef),
-          _dense(dloss), _dense(dlogits), _stream(stream))
+    _call("moe_balance_loss_bwd", ctypes.byref(shape), *_pointers(logits, mask, coef, dloss, dlogits),
+          _stream(stream))
 
 
 def moe_permute_e4m3(shape, q, q_scale, group, topk_idx, keep, Xp, row_of, src_of, counts, offsets,
                      ws, stream=None):
-    _call("moe_permute_e4m3", ctypes.byref(shape), _here(q), _dense(q_scale), group, _dense(topk_idx),
-          _dense(keep), _dense(Xp), _dense(row_of), _dense(src_of), _dense(counts), _dense(offsets),
-          _dense(ws), _stream(stream))
+    q, q_scale, *rest = _pointers(q, q_scale, topk_idx, keep, Xp, row_of, src_of, counts, offsets, ws)
+    _call("moe_permute_e4m3", ctypes.byref(shape), q, q_scale, group, *rest, _stream(stream))
 
 
 def _list_here(grads):
@@ -357,12 +357,13 @@ def moe_grad_norm(grads, norm, ws, stream=None, ws_bytes=None):
     """grads: a TensorList. ws: a device tensor (its size becomes ws_bytes) or a pointer with ws_bytes."""
     if ws_bytes is None:
         ws_bytes = ws.nbytes
-    _call("moe_grad_norm", grads.n, _list_here(grads), _here(norm), _dense(ws), ws_bytes, _stream(stream))
+    _call("moe_grad_norm", grads.n, _list_here(grads), *_pointers(norm, ws), ws_bytes, _stream(stream))
 
 
 def moe_grad_clip(grads, out, norm, max_norm, coef, stream=None):
     """grads: a TensorList; out: a TensorList of the same tensors' sizes and types, or None for in place."""
     if out is not None and (out.n != grads.n or out.device != grads.device):
         raise MoEError("moe_grad_clip", 1)
+    norm, coef = _pointers(norm, coef)
     _call("moe_grad_clip", grads.n, _list_here(grads), None if out is None else out.address,
-          _here(norm), max_norm, _dense(coef), _stream(stream))
+          norm, max_norm, coef, _stream(stream))
