@@ -539,7 +539,9 @@ constexpr size_t kSmem = 226 * 1024;   // of the 227 KB that a CTA may have; the
 // CTAs of a persistent grid: those that fit the device at once, at most
 // `most`. The answer for the last device and size that a kernel was asked for
 // is kept (one word, so that threads may race for it): the two calls behind it
-// cost the host 1 us, half of what the launch does.
+// cost the host 1 us, half of what the launch does. The limit that is set here
+// belongs to the kernel and the device: it holds in the device's other contexts
+// and past a reset of the primary one (tests/test_gpu_norm_contexts.py).
 template <typename K>
 cudaError_t resident(K k, std::atomic<uint64_t> &kept, int threads, size_t smem, int64_t most,
                      int64_t *grid) {
