@@ -400,7 +400,8 @@ moe_status_t moe_rmsnorm_bwd(int32_t dtype, int32_t dy_dtype, int32_t dx_dtype, 
  *   out: loss [1] fp32; counts [n_sub,E] int32; prob_mean [n_sub,E] fp32 or
  *   NULL; coef [n_sub * E + 1] fp32: kept for the backward. n_sub = ceil(T/S).
  *   ws: workspace of moe_workspace_size(shape) bytes. shape: T, E, K,
- *   subseq_len are used, all fields are checked.
+ *   subseq_len are used, all fields are checked. No output overlaps another,
+ *   an input or ws.
  * Errors: an unmasked topk_idx outside [0, E) is not counted and records
  *   MOE_ERR_DEVICE in the status word.                                       */
 moe_status_t moe_balance_loss(const moe_shape_t *shape, const float *logits,
@@ -412,7 +413,7 @@ moe_status_t moe_balance_loss(const moe_shape_t *shape, const float *logits,
  * for padding), for moe_route_bwd_add. logits, mask, coef as in
  * moe_balance_loss; dloss [1] fp32 on the device, or NULL for 1; dlogits [T,E]
  * fp32, which may be logits itself where nothing reads the logits after this
- * (moe_route_bwd_add does).                                                  */
+ * (moe_route_bwd_add does); no other overlap.                                */
 moe_status_t moe_balance_loss_bwd(const moe_shape_t *shape, const float *logits,
                                   const uint8_t *mask, const float *coef, const float *dloss,
                                   float *dlogits, moe_stream_t stream);

@@ -1,0 +1,46 @@
+"""Buffers that share memory where the operators around the layer would race or
+overwrite what they still read: refused before anything is launched. No GPU is
+needed; the addresses are never dereferenced."""
+import pytest
+
+from tests.test_around_refusals import A, L, _shape, refused  # noqa: F401
+
+T, D, E, K, N_SUB = 64, 64, 8, 2, 4   # _shape's; sub-sequences of 16 tokens
+
+
+def over(address, bytes_, other_bytes):
+    """Places of a buffer of `other_bytes` that touch one of `bytes_` at `address`: at its start, over its first and
+    over its last 16 bytes."""
+    return [address, address + 16 - other_bytes // 16 * 16 if other_bytes >= 16 else address, address + (bytes_ - 1) // 16 * 16]
+
+
+def test_balance_loss(L):  # noqa: F811
+    s = _shape(L)
+    size = dict(logits=T * E * 4, idx=T * K * 4, mask=T, loss=4, counts=N_SUB * E * 4, prob=N_SUB * E * 4,
+                coef=(N_SUB * E + 1) * 4, ws=L.moe_workspace_size(s))
+    at = dict(zip(size, A))
+
+    def call(**kw):
+        a = {**at, **kw}
+        refused(L, 1, "moe_balance_loss", s, a["logits"], a["idx"], a["mask"], 0.1, a["loss"], a["counts"], a["prob"],
+                a["coef"], a["ws"], 0)
+
+    outs = ["loss", "counts", "prob", "coef"]
+    for i, o in enumerate(outs):
+        for other in ["logits", "idx", "mask"] + outs[i + 1:]:
+            for place in over(at[other], size[other], size[o]):
+                call(**{o: place})
+        call(**{o: at["ws"]})                       # the status word
+        call(**{o: at["ws"] + size["ws"] - 256})    # the partial sums, which lie last
+    for i in ("logits", "idx", "mask"):
+        call(**{i: at["ws"] + size["ws"] - 256})
+
+
+def test_balance_loss_bwd(L):  # noqa: F811
+    s = _shape(L)
+    size = dict(logits=T * E * 4, mask=T, coef=(N_SUB * E + 1) * 4, dloss=4)
+    at = dict(zip(size, A))
+    for other in size:
+        for place in over(at[other], size[other], T * E * 4):
+            if place != at["logits"]:               # the logits' own place is allowed
+                refused(L, 1, "moe_balance_loss_bwd", s, at["logits"], at["mask"], at["coef"], at["dloss"], place, 0)

@@ -26,6 +26,30 @@ constexpr size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+bool overlap(const void *p, size_t np, const void *q, size_t nq) {
+  if (p == nullptr || q == nullptr) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + nq && b < a + np;
+}
+
+struct Span {
+  const void *p;
+  size_t n;
+};
+
+// Whether one of the buffers that a call writes shares memory with another of
+// them or with one that it reads. NULL shares none.
+template <size_t W, size_t R>
+bool any_overlap(const Span (&written)[W], const Span (&read)[R]) {
+  for (size_t i = 0; i < W; ++i) {
+    for (size_t j = i + 1; j < W; ++j)
+      if (overlap(written[i].p, written[i].n, written[j].p, written[j].n)) return true;
+    for (size_t j = 0; j < R; ++j)
+      if (overlap(written[i].p, written[i].n, read[j].p, read[j].n)) return true;
+  }
+  return false;
+}
+
 bool shape_ok(const moe_shape_t *s) {
   if (s == nullptr) return false;
   if (s->T < 1 || s->d < 1 || s->E < 1 || s->E > 64 || s->K < 1 || s->K > 8 || s->K > s->E)
@@ -386,12 +410,6 @@ moe_status_t moe_sum_partials(int32_t dtype, int32_t n_parts, int64_t rows, int3
                                          (cudaStream_t)stream));
 }
 
-static bool overlap(const void *p, size_t np, const void *q, size_t nq) {
-  if (p == nullptr || q == nullptr) return false;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + nq && b < a + np;
-}
-
 static moe_status_t route_bwd(const moe_shape_t *shape, const void *x, const void *W_r,
                               const void *w_sg, const float *logits, const int32_t *topk_idx,
                               const float *topk_prob, const float *topk_w, const float *dw,
@@ -556,9 +574,16 @@ moe_status_t moe_balance_loss(const moe_shape_t *shape, const float *logits, con
       !aligned4(prob_mean) || !aligned16(coef) || !aligned16(ws))
     return MOE_ERR_INVALID_ARG;
   BalanceArgs a = balance_args(shape);
+  const size_t pairs = (size_t)a.n_sub * a.E * 4;
+  char *partial = static_cast<char *>(ws) + layout(shape).bal;
+  const Span written[] = {{loss, 4}, {counts, pairs}, {prob_mean, pairs}, {coef, pairs + 4},
+                          {ws, kStatusBytes}, {partial, balance_workspace_bytes(a.T, a.S, a.E)}};
+  const Span read[] = {{logits, (size_t)a.T * a.E * 4}, {topk_idx, (size_t)a.T * a.K * 4},
+                       {mask, (size_t)a.T}};
+  if (any_overlap(written, read)) return MOE_ERR_INVALID_ARG;
   a.logits = logits; a.topk_idx = topk_idx; a.mask = mask; a.alpha = alpha; a.loss = loss;
   a.counts = counts; a.prob_mean = prob_mean; a.coef = coef;
-  a.partial = static_cast<char *>(ws) + layout(shape).bal;
+  a.partial = partial;
   a.status = status_word(ws);
   return cuda_status(launch_balance_loss(a, (cudaStream_t)stream));
 }
@@ -572,7 +597,10 @@ moe_status_t moe_balance_loss_bwd(const moe_shape_t *shape, const float *logits,
     return MOE_ERR_INVALID_ARG;
   BalanceArgs a = balance_args(shape);
   const size_t n = (size_t)a.T * a.E * sizeof(float);
-  if (dlogits != logits && overlap(dlogits, n, logits, n)) return MOE_ERR_INVALID_ARG;
+  const Span written[] = {{dlogits, n}};
+  const Span read[] = {{dlogits == logits ? nullptr : logits, n}, {mask, (size_t)a.T},
+                       {coef, (size_t)(a.n_sub * a.E + 1) * 4}, {dloss, 4}};
+  if (any_overlap(written, read)) return MOE_ERR_INVALID_ARG;
   a.logits = logits; a.mask = mask; a.coef = const_cast<float *>(coef); a.dloss = dloss;
   a.dlogits = dlogits;
   return cuda_status(launch_balance_loss_bwd(a, (cudaStream_t)stream));
