@@ -328,7 +328,7 @@ moe_status_t moe_route_bwd(const moe_shape_t *shape, const void *x, const void *
 /* moe_route_bwd with the gradient of a loss on the logits: dl gains
  * dlogits_add [T,E] fp32 (for instance from moe_balance_loss_bwd) before dW_r,
  * db_r and dx_router are formed from it. Other arguments and errors as
- * moe_route_bwd; dlogits_add must not be NULL nor overlap logits.            */
+ * moe_route_bwd; dlogits_add must not be NULL nor overlap logits or ws.      */
 moe_status_t moe_route_bwd_add(const moe_shape_t *shape, const void *x, const void *W_r,
                                const void *w_sg, const float *logits,
                                const int32_t *topk_idx, const float *topk_prob,

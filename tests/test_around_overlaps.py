@@ -44,3 +44,13 @@ def test_balance_loss_bwd(L):  # noqa: F811
         for place in over(at[other], size[other], T * E * 4):
             if place != at["logits"]:               # the logits' own place is allowed
                 refused(L, 1, "moe_balance_loss_bwd", s, at["logits"], at["mask"], at["coef"], at["dloss"], place, 0)
+
+
+def test_route_bwd_add(L):  # noqa: F811
+    """dlogits_add inside the workspace, where the logits' gradient is written
+    while it is read."""
+    s = _shape(L)
+    ws, n = A[9], L.moe_workspace_size(_shape(L))
+    for add in range(ws - T * E * 4 + 16, ws + n, 256):
+        refused(L, 1, "moe_route_bwd_add", s, A[0], A[1], None, A[2], A[3], A[4], A[5], A[6], None, add, None, A[7], None, None,
+                A[8], ws, 0)

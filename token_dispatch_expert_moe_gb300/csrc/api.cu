@@ -457,6 +457,8 @@ moe_status_t moe_route_bwd_add(const moe_shape_t *shape, const void *x, const vo
   if (!shape_ok(shape) || !dlogits_add || !aligned4(dlogits_add)) return MOE_ERR_INVALID_ARG;
   const size_t n = (size_t)shape->T * shape->E * sizeof(float);
   if (overlap(dlogits_add, n, logits, n)) return MOE_ERR_INVALID_ARG;   // both are read
+  // dl is written there while dlogits_add is read
+  if (overlap(dlogits_add, n, ws, layout(shape).total)) return MOE_ERR_INVALID_ARG;
   return route_bwd(shape, x, W_r, w_sg, logits, topk_idx, topk_prob, topk_w, dw, dz, dlogits_add,
                    dx_in, dW_r, db_r, dw_sg, dx_router, ws, stream);
 }
