@@ -422,8 +422,9 @@ moe_status_t moe_balance_loss_bwd(const moe_shape_t *shape, const float *logits,
  *   Xp[row_of[t,k]] = dtype(q[t] * scale of its group), dtype = shape->dtype.
  *   q [T,d] e4m3 bytes; q_scale [T, ceil(d / group)] fp32 (group 32, 64, 128,
  *   or 0: one per row). Other arguments and the map as moe_permute; Xp is
- *   required. Errors: as moe_permute; MOE_ERR_UNSUPPORTED for another group or
- *   rows of more than 200 KB in dtype (d above 102400 bf16, 51200 fp32).     */
+ *   required. No output overlaps another, an input or ws. Errors: as
+ *   moe_permute; MOE_ERR_UNSUPPORTED for another group or rows of more than
+ *   200 KB in dtype (d above 102400 bf16, 51200 fp32).                       */
 moe_status_t moe_permute_e4m3(const moe_shape_t *shape, const void *q, const float *q_scale,
                               int32_t group, const int32_t *topk_idx, const uint8_t *keep,
                               void *Xp, int32_t *row_of, int32_t *src_of, int32_t *counts,

@@ -54,3 +54,25 @@ def test_route_bwd_add(L):  # noqa: F811
     for add in range(ws - T * E * 4 + 16, ws + n, 256):
         refused(L, 1, "moe_route_bwd_add", s, A[0], A[1], None, A[2], A[3], A[4], A[5], A[6], None, add, None, A[7], None, None,
                 A[8], ws, 0)
+
+
+@pytest.mark.parametrize("dtype,group", [(0, 32), (1, 0)])
+def test_permute_e4m3(L, dtype, group):  # noqa: F811
+    s = _shape(L, dtype=dtype)
+    ng = -(-D // group) if group else 1
+    size = dict(q=T * D, s=T * ng * 4, idx=T * K * 4, keep=T * K, Xp=T * K * D * (2 if dtype else 4), row=T * K * 4,
+                src=T * K * 4, cnt=E * 4, off=(E + 1) * 4, ws=L.moe_workspace_size(s))
+    at = dict(zip(size, A))
+
+    def call(**kw):
+        refused(L, 1, "moe_permute_e4m3", s, *[{**at, **kw}[k] for k in ("q", "s")], group,
+                *[{**at, **kw}[k] for k in ("idx", "keep", "Xp", "row", "src", "cnt", "off", "ws")], 0)
+
+    outs = ["Xp", "row", "src", "cnt", "off"]
+    for i, o in enumerate(outs):
+        for other in ["q", "s", "idx", "keep"] + outs[i + 1:]:
+            for place in over(at[other], size[other], size[o]):
+                call(**{o: place})
+        call(**{o: at["ws"]})         # the status word and the counts behind it
+    for i in ("q", "s", "idx", "keep"):
+        call(**{i: at["ws"]})

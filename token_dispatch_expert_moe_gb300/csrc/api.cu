@@ -619,11 +619,19 @@ moe_status_t moe_permute_e4m3(const moe_shape_t *shape, const void *q, const flo
   if (!q || !q_scale || !topk_idx || !keep || !Xp || !row_of || !src_of || !counts || !offsets || !ws)
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned4(q_scale) || !aligned16(Xp) || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  const Layout L = layout(shape);
+  const size_t T = (size_t)shape->T, d = (size_t)shape->d, slots = T * shape->K;
+  const size_t scales = group > 0 ? (d + group - 1) / group : 1;
+  const Span written[] = {{Xp, slots * d * size_of(shape->dtype)}, {row_of, slots * 4}, {src_of, slots * 4},
+                          {counts, (size_t)shape->E * 4}, {offsets, (size_t)(shape->E + 1) * 4},
+                          {ws, kStatusBytes}, {static_cast<char *>(ws) + L.map, L.cap - L.map}};
+  const Span read[] = {{q, T * d}, {q_scale, T * scales * 4}, {topk_idx, slots * 4}, {keep, slots}};
+  if (any_overlap(written, read)) return MOE_ERR_INVALID_ARG;
   PermuteArgs a{};
   a.T = shape->T; a.d = shape->d; a.E = shape->E; a.K = shape->K; a.dtype = shape->dtype;
   a.topk_idx = topk_idx; a.keep = keep; a.row_of = row_of; a.src_of = src_of;
   a.counts = counts; a.offsets = offsets;
-  a.blk_counts = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + layout(shape).map);
+  a.blk_counts = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + L.map);
   a.status = status_word(ws);
   cudaError_t e = launch_permute(a, (cudaStream_t)stream);   // Xp NULL: the map
   a.Xp = Xp;
