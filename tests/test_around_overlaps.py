@@ -76,3 +76,11 @@ def test_permute_e4m3(L, dtype, group):  # noqa: F811
         call(**{o: at["ws"]})         # the status word and the counts behind it
     for i in ("q", "s", "idx", "keep"):
         call(**{i: at["ws"]})
+
+
+def test_permute_e4m3_misplaced_words(L):  # noqa: F811
+    """32-bit words that do not start on 4 bytes would fault."""
+    at = dict(zip(("q", "s", "idx", "keep", "Xp", "row", "src", "cnt", "off", "ws"), A))
+    for k in ("s", "idx", "row", "src", "cnt", "off"):
+        v = {**at, k: at[k] + 2}
+        refused(L, 1, "moe_permute_e4m3", _shape(L), v["q"], v["s"], 32, *list(v.values())[2:], 0)

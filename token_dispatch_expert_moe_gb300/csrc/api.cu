@@ -618,7 +618,9 @@ moe_status_t moe_permute_e4m3(const moe_shape_t *shape, const void *q, const flo
   if ((size_t)shape->d * size_of(shape->dtype) > kPermRowCap) return MOE_ERR_UNSUPPORTED;
   if (!q || !q_scale || !topk_idx || !keep || !Xp || !row_of || !src_of || !counts || !offsets || !ws)
     return MOE_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned4(q_scale) || !aligned16(Xp) || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned4(q_scale) || !aligned16(Xp) || !aligned16(ws) || !aligned4(topk_idx) ||
+      !aligned4(row_of) || !aligned4(src_of) || !aligned4(counts) || !aligned4(offsets))
+    return MOE_ERR_INVALID_ARG;
   const Layout L = layout(shape);
   const size_t T = (size_t)shape->T, d = (size_t)shape->d, slots = T * shape->K;
   const size_t scales = group > 0 ? (d + group - 1) / group : 1;
