@@ -445,7 +445,8 @@ typedef struct {
  * squares), fp32, right wherever that is an fp32 number (squares outside the
  * fp32 range are added in fp64); NaN or infinity among the gradients gives a
  * norm that is not finite; an empty list gives 0. `grads` is a HOST array and
- * is read before the call returns. A tensor that is listed twice counts twice. */
+ * is read before the call returns. A tensor that is listed twice counts twice;
+ * ws overlaps none of them.                                                  */
 moe_status_t moe_grad_norm(int32_t n, const moe_tensor_t *grads, float *norm, void *ws,
                            size_t ws_bytes, moe_stream_t stream);
 
@@ -457,8 +458,9 @@ moe_status_t moe_grad_norm(int32_t n, const moe_tensor_t *grads, float *norm, vo
  *   sizes and types, each of which is its gradient itself or does not overlap
  *   any gradient; coef [1] fp32 or NULL receives coef. In place with coef = 1
  *   nothing is read or written. Both arrays are HOST arrays. No output
- *   overlaps another, so in place no tensor is listed twice; norm and coef lie
- *   in none of them.                                                         */
+ *   overlaps another, so in place no tensor is listed twice; norm lies in no
+ *   output, coef in no output or gradient, and the two are not one. A call
+ *   that breaks this is MOE_ERR_INVALID_ARG.                                 */
 moe_status_t moe_grad_clip(int32_t n, const moe_tensor_t *grads, const moe_tensor_t *out,
                            const float *norm, float max_norm, float *coef,
                            moe_stream_t stream);

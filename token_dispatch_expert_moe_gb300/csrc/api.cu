@@ -3,7 +3,9 @@
 // Every call that launches work opens an NVTX range named after itself, so
 // profilers that record NVTX show where each layer step starts and ends
 // (without a profiler attached the range calls return at once).
+#include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include <nvtx3/nvToolsExt.h>
@@ -653,6 +655,57 @@ static moe_status_t list_check(int32_t n, const moe_tensor_t *list) {
   return MOE_OK;
 }
 
+static size_t bytes_of(const moe_tensor_t &t) { return (size_t)t.numel * size_of(t.dtype); }
+
+// Whether clipping would write to what it still reads, or twice to one place:
+// two outputs, or an output and another gradient, or norm or coef and an
+// output, or coef and a gradient. The outputs are sorted by address, so that
+// long lists cost n log n; only without host memory for that is every pair
+// looked at.
+static bool clip_overlap(int32_t n, const moe_tensor_t *grads, const moe_tensor_t *out,
+                         const float *norm, const float *coef) {
+  const moe_tensor_t *w = out != nullptr ? out : grads;
+  if (overlap(norm, 4, coef, 4)) return true;
+  for (int32_t i = 0; i < n; ++i) {
+    if (grads[i].numel == 0) continue;   // nowhere
+    const size_t b = bytes_of(grads[i]);
+    if (overlap(norm, 4, w[i].data, b) || overlap(coef, 4, w[i].data, b) ||
+        overlap(coef, 4, grads[i].data, b) ||
+        (w[i].data != grads[i].data && overlap(w[i].data, b, grads[i].data, b)))
+      return true;
+  }
+  constexpr int32_t kFew = 64;
+  int32_t few[kFew];
+  int32_t *order = n <= kFew ? few : static_cast<int32_t *>(std::malloc((size_t)n * sizeof(int32_t)));
+  bool found = false;
+  if (order == nullptr) {
+    for (int32_t i = 0; i < n && !found; ++i)
+      for (int32_t j = 0; j < n && !found; ++j)
+        if (i != j && grads[i].numel > 0 && grads[j].numel > 0)
+          found = overlap(w[i].data, bytes_of(w[i]), w[j].data, bytes_of(w[j])) ||
+                  overlap(w[i].data, bytes_of(w[i]), grads[j].data, bytes_of(grads[j]));
+    return found;
+  }
+  int32_t m = 0;
+  for (int32_t i = 0; i < n; ++i)
+    if (grads[i].numel > 0) order[m++] = i;
+  const auto start = [&](int32_t i) { return reinterpret_cast<uintptr_t>(w[i].data); };
+  std::sort(order, order + m, [&](int32_t i, int32_t j) { return start(i) < start(j); });
+  for (int32_t k = 1; k < m && !found; ++k) found = start(order[k]) < start(order[k - 1]) + bytes_of(w[order[k - 1]]);
+  if (out != nullptr)
+    for (int32_t j = 0; j < n && !found; ++j) {
+      if (grads[j].numel == 0) continue;
+      // the outputs that start before this gradient's end, from the last: they
+      // do not overlap each other, so the first that ends before it ends the search
+      const uintptr_t at = reinterpret_cast<uintptr_t>(grads[j].data), end = at + bytes_of(grads[j]);
+      int32_t k = (int32_t)(std::lower_bound(order, order + m, end,
+                                             [&](int32_t i, uintptr_t v) { return start(i) < v; }) - order);
+      while (--k >= 0 && start(order[k]) + bytes_of(w[order[k]]) > at && !found) found = order[k] != j;
+    }
+  if (order != few) std::free(order);
+  return found;
+}
+
 moe_status_t moe_grad_norm(int32_t n, const moe_tensor_t *grads, float *norm, void *ws,
                            size_t ws_bytes, moe_stream_t stream) {
   NvtxRange trace("moe_grad_norm");
@@ -662,6 +715,9 @@ moe_status_t moe_grad_norm(int32_t n, const moe_tensor_t *grads, float *norm, vo
   if (st != MOE_OK) return st;
   if (!norm || !aligned4(norm) || !ws || !aligned16(ws) || ws_bytes < MOE_GRAD_NORM_WORKSPACE_BYTES)
     return MOE_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < n; ++i)
+    if (grads[i].numel > 0 && overlap(ws, MOE_GRAD_NORM_WORKSPACE_BYTES, grads[i].data, bytes_of(grads[i])))
+      return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_grad_norm(n, grads, norm, static_cast<double *>(ws), (cudaStream_t)stream));
 }
 
@@ -674,12 +730,9 @@ moe_status_t moe_grad_clip(int32_t n, const moe_tensor_t *grads, const moe_tenso
   if (!norm || !aligned4(norm) || !aligned4(coef) || !(max_norm >= 0.0f) || !std::isfinite(max_norm))
     return MOE_ERR_INVALID_ARG;
   if (out != nullptr)
-    for (int32_t i = 0; i < n; ++i) {
+    for (int32_t i = 0; i < n; ++i)
       if (out[i].numel != grads[i].numel || out[i].dtype != grads[i].dtype) return MOE_ERR_INVALID_ARG;
-      const size_t b = (size_t)grads[i].numel * size_of(grads[i].dtype);
-      if (out[i].data != grads[i].data && overlap(out[i].data, b, grads[i].data, b))
-        return MOE_ERR_INVALID_ARG;
-    }
+  if (clip_overlap(n, grads, out, norm, coef)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_grad_clip(n, grads, out, norm, max_norm, coef, (cudaStream_t)stream));
 }
 
