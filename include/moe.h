@@ -357,9 +357,13 @@ moe_status_t moe_route_bwd_add(const moe_shape_t *shape, const void *x, const vo
  *   group: 32, 64, 128, or 0 for one scale per row.
  * h and y may each be x or residual itself (in place); no other overlap of an
  * output with an input or with another output. rows = 0 does nothing.
- * Statistics are fp32: a row whose squares add up to more than 3.4e38 (|h| of
- * 1e17 and more) gets y = 0. A row's results depend on that row alone: not on
- * how many there are, nor on a NaN or infinity in another.
+ * Statistics are fp32: a row whose squares add up to more than 3.4e38 (a root
+ * mean square of h above sqrt(3.4e38 / d): 2.3e18 at d = 64, 1e17 at 32768)
+ * gets rstd = 0 and y = 0, and squares below 1e-45 count as 0. A row's results
+ * depend on that row alone: not on how many there are, nor on a NaN or infinity
+ * in another.
+ * y / s is formed with the reciprocal of s: a quotient within 2^-20 of itself
+ * from the middle between two e4m3 values may go to either of them.
  * Errors: MOE_ERR_INVALID_ARG as above; MOE_ERR_UNSUPPORTED for another group,
  *   d above 32768 (bf16) or 16384 (fp32), or rows >= 2^31.                   */
 moe_status_t moe_rmsnorm(int32_t dtype, int64_t rows, int32_t d, const void *x,
