@@ -64,9 +64,10 @@ Split split_of(int64_t T, int64_t S, int lanes) {
 // consecutive 16 bytes. At most 4 lanes: the row's maximum and sum take two
 // shuffles each, and a lane's 16 exponentials overlap (262144 x 64, loss and
 // gradient: 16.5 and 20.7 us; 8 lanes of two quads 20.6 and 23.4 us, 16 lanes
-// of one 31.1 and 29.4 us). Bound by instruction issue more than by HBM: half
-// the issue slots and half the bandwidth are in use; logits fetched two tokens
-// ahead through shared memory took 10 % more.
+// of one 31.1 and 29.4 us). Their bytes take 11.1 and 19.8 us: the gradient is
+// bound by HBM, the loss waits for latency, with 16 warps an SM (98 registers),
+// half the issue slots and two thirds of the bandwidth in use; logits fetched
+// two tokens ahead through shared memory took 10 % more.
 
 // A row of E values, l[4 v + i] of expert 4 (sub + v L) + i: `none` past E, and
 // throughout where `in` is false (nothing is read then).

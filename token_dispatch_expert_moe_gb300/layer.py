@@ -59,7 +59,9 @@ class MoELayer:
     dispatch="e4m3" (with gamma; compact layout, no gather) moves the routed
     experts' rows in 8 bits with one scale per 128 columns: the norm writes
     them and moe_permute_e4m3 reads them. Router and shared expert still read
-    the norm's output; the gradient passes the rounding as if it were not there.
+    the norm's output, so on one GPU this saves no memory traffic: it computes
+    what a dispatch of 8-bit rows between ranks would. The gradient passes the
+    rounding as if it were not there.
 
     balance > 0 adds the router's balance loss with that factor: forward leaves
     it in self.loss ([1], on the device) and the pre-drop counts per
