@@ -469,6 +469,104 @@ moe_status_t moe_grad_clip(int32_t n, const moe_tensor_t *grads, const moe_tenso
                            const float *norm, float max_norm, float *coef,
                            moe_stream_t stream);
 
+/* ---- fine-tuning and serving many users ----------------------------------
+ * Dropout whose mask is never stored, and low-rank adapters that every token
+ * chooses for itself, for training beside weights that stay as they are and for
+ * serving the adapters of many users in one batch. Conventions as above.
+ *
+ * Random numbers. rng is {seed, offset}: two 64-bit words on the DEVICE, so that
+ * a captured step draws new masks when they are rewritten. Element i of a dense
+ * matrix (row-major, counted from its first element) belongs to block b = i / 8
+ * of Philox4x32-10 (Salmon, Moraes, Dror, Shaw 2011), counter words (low b,
+ * high b, low offset, high offset), key (low seed, high seed), and takes the
+ * (i % 8)-th 16 bits of the four output words, low halves first. With t =
+ * round(65536 p), at most 65535, it is kept if its 16 bits are >= t, and
+ *   drop(x)_i = x_i * 65536 / (65536 - t)  if kept, else 0 (whatever x_i is).
+ * So p is rounded to 1/65536, the expectation is exact, p = 0 keeps everything
+ * (rng may then be NULL), and one rng gives one mask: the backward rebuilds it,
+ * and another use of the same step takes another offset or seed.              */
+
+/* out = dtype(residual + drop(x)), residual NULL: 0.
+ *   x, residual, out: n >= 0 elements of dtype; 0 <= p < 1; rng 8-byte aligned.
+ *   out may be x or residual itself; no other overlap.                         */
+moe_status_t moe_dropout(int32_t dtype, int64_t n, const void *x, const void *residual, float p,
+                         const uint64_t *rng, void *out, moe_stream_t stream);
+
+/* dx = dx_dtype(drop(dy)), the mask of moe_dropout for the same n, p and rng;
+ * the residual's gradient is dy itself.
+ *   dy [n] dy_dtype, dx [n] dx_dtype, MOE_F32 or MOE_BF16 each; dx may be dy
+ *   itself when the types agree; no other overlap.                             */
+moe_status_t moe_dropout_bwd(int32_t dy_dtype, int32_t dx_dtype, int64_t n, const void *dy, float p,
+                             const uint64_t *rng, void *dx, moe_stream_t stream);
+
+/* A set of n low-rank adapters beside one linear map of T tokens. Adapter a:
+ * A[a] [rank, d_in], B[a] [d_out, rank] and a factor scale[a]; adapters of lower
+ * rank are padded with zeros.                                                  */
+typedef struct {
+  int64_t T;       /* tokens, 0 <= T < 2^31                                     */
+  int32_t d_in;    /* multiples of 8 (bf16) or 4 (fp32)                         */
+  int32_t d_out;
+  int32_t n;       /* adapters in memory, 1..4096                               */
+  int32_t rank;    /* a multiple of 8 (bf16) or 4 (fp32), at most 128           */
+  int32_t dtype;   /* MOE_BF16 or MOE_F32: x, A, B, base, y, dy                 */
+  float dropout;   /* p of the dropout on the adapters' input, 0 <= p < 1       */
+  int64_t ld_in;   /* elements from row to row of x, and of base, y and dy: a   */
+  int64_t ld_out;  /* slice of a wider matrix; multiples of 8 (bf16) or 4       */
+                   /* (fp32) not below d_in or d_out; 0: dense                  */
+} moe_adapter_shape_t;
+
+/* Bytes of the workspace `ws` of the calls below (status word first, read with
+ * moe_get_status; zero it once), and of the map. 0 for an invalid shape.       */
+size_t moe_adapter_workspace_size(const moe_adapter_shape_t *shape);
+size_t moe_adapter_map_size(const moe_adapter_shape_t *shape);
+
+/* 1 if moe_adapter is faster without a map (few tokens, each read with its
+ * adapter on its own), else 0. A rule on the shape alone; both ways are right.  */
+int32_t moe_adapter_rowwise(const moe_adapter_shape_t *shape);
+
+/* Groups the tokens by adapter: once per batch, for every call on it (shapes of
+ * the same T and n, whatever their widths, rank or dtype).
+ *   adapter_of [T] int32: the adapter of each token, -1 for none;
+ *   map: moe_adapter_map_size bytes, 16-byte aligned, opaque.
+ * Errors: an index outside [-1, n) counts as none and records MOE_ERR_DEVICE.   */
+moe_status_t moe_adapter_map(const moe_adapter_shape_t *shape, const int32_t *adapter_of, void *map,
+                             void *ws, moe_stream_t stream);
+
+/* For the adapter a of token t:
+ *   u[t] = A[a] drop(x[t])                                fp32
+ *   y[t] = dtype(base[t] + scale[a] B[a] u[t])            one rounding
+ * without an adapter y[t] = base[t] and u[t] = 0; base NULL counts as 0.
+ *   x [T, d_in] (ld_in); A [n, rank, d_in], B [n, d_out, rank] dtype, dense;
+ *   scale [n] fp32 or NULL (1); base, y [T, d_out] (ld_out), base may be y itself
+ *   (tokens without an adapter are then not touched); u [T, rank] fp32 or NULL:
+ *   kept for the backward; rng: see above, for the dense [T, d_in] matrix.
+ *   The tokens' adapters: map; or map NULL and adapter_of, row by row; or both
+ *   NULL: adapter 0 for all of them. adapter_of is not read beside a map.
+ * In bf16 the products run on the tensor cores with u held in two bf16 parts
+ * (2^-17 of it), accumulated in fp32. No output overlaps another, an input or
+ * ws, but columns of one wider matrix may be x here and y there.
+ * Errors: a map of another T or n records MOE_ERR_DEVICE and leaves rows out.   */
+moe_status_t moe_adapter(const moe_adapter_shape_t *shape, const void *x, const void *A,
+                         const void *B, const float *scale, const int32_t *adapter_of,
+                         const void *map, const uint64_t *rng, const void *base, void *y, float *u,
+                         void *ws, moe_stream_t stream);
+
+/* Backward of moe_adapter; base's gradient is dy. For the tokens t of adapter a:
+ *   du[t] = scale[a] B[a]^T dy[t];      dx[t] = dx_dtype(dx_in[t] + drop(A[a]^T du[t]))
+ *   dA[a] = sum_t du[t] drop(x[t])^T;   dB[a] = scale[a] sum_t dy[t] u[t]^T
+ * (zero for an adapter without tokens; overwritten). Without an adapter dx[t] =
+ * dx_in[t]; dx_in NULL counts as 0.
+ *   dy [T, d_out] (ld_out); x [T, d_in] (ld_in); u as moe_adapter wrote it;
+ *   dx_in, dx [T, d_in] dense in dx_dtype (MOE_F32, or MOE_BF16 for a bf16
+ *   shape), dx NULL: not wanted, dx_in may be dx itself; dA [n, rank, d_in], dB
+ *   [n, d_out, rank] fp32, both or neither NULL. map: as moe_adapter_map wrote
+ *   it, or NULL for adapter 0 throughout.                                       */
+moe_status_t moe_adapter_bwd(const moe_adapter_shape_t *shape, int32_t dx_dtype, const void *dy,
+                             const void *x, const void *A, const void *B, const float *scale,
+                             const void *map, const uint64_t *rng, const float *u,
+                             const void *dx_in, void *dx, float *dA, float *dB, void *ws,
+                             moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

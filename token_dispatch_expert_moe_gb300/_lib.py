@@ -36,6 +36,12 @@ class MoEShape(ctypes.Structure):
                 ("subseq_len", ctypes.c_int64), ("renorm", ctypes.c_int32), ("Fs", ctypes.c_int32)]
 
 
+class MoEAdapterShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("dtype", ctypes.c_int32), ("dropout", ctypes.c_float),
+                ("ld_in", ctypes.c_int64), ("ld_out", ctypes.c_int64)]
+
+
 class MoETensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
@@ -83,6 +89,7 @@ lib = ctypes.CDLL(LIB_PATH)
 
 _P = ctypes.c_void_p
 _S = ctypes.POINTER(MoEShape)
+_A = ctypes.POINTER(MoEAdapterShape)
 _I32, _I64, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 _SIGS = {
@@ -110,6 +117,12 @@ _SIGS = {
     "moe_permute_e4m3": [_S, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P],
     "moe_grad_norm": [_I32, _P, _P, _P, ctypes.c_size_t, _P],
     "moe_grad_clip": [_I32, _P, _P, _P, _F, _P, _P],
+    "moe_dropout": [_I32, _I64, _P, _P, _F, _P, _P, _P],
+    "moe_dropout_bwd": [_I32, _I32, _I64, _P, _F, _P, _P, _P],
+    "moe_adapter_rowwise": [_A],
+    "moe_adapter_map": [_A, _P, _P, _P, _P],
+    "moe_adapter": [_A, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "moe_adapter_bwd": [_A, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
     "moe_clear_status": [_P, _P],
     "moe_get_status": [_P, _P, ctypes.POINTER(ctypes.c_uint32)],
 }
@@ -123,12 +136,17 @@ lib.moe_padded_capacity.argtypes = [_S]
 lib.moe_padded_capacity.restype = ctypes.c_int64
 lib.moe_rmsnorm_bwd_workspace_size.argtypes = [_I64, _I32]
 lib.moe_rmsnorm_bwd_workspace_size.restype = ctypes.c_size_t
+lib.moe_adapter_workspace_size.argtypes = [_A]
+lib.moe_adapter_workspace_size.restype = ctypes.c_size_t
+lib.moe_adapter_map_size.argtypes = [_A]
+lib.moe_adapter_map_size.restype = ctypes.c_size_t
 lib.moe_version.restype = ctypes.c_char_p
 lib.moe_status_string.argtypes = [ctypes.c_int]
 lib.moe_status_string.restype = ctypes.c_char_p
 
 EXPORTED = sorted(list(_SIGS) + ["moe_workspace_size", "moe_version", "moe_status_string",
-                                  "moe_padded_capacity", "moe_rmsnorm_bwd_workspace_size"])
+                                  "moe_padded_capacity", "moe_rmsnorm_bwd_workspace_size",
+                                  "moe_adapter_workspace_size", "moe_adapter_map_size"])
 
 
 def _ptr(t):
@@ -367,3 +385,61 @@ def moe_grad_clip(grads, out, norm, max_norm, coef, stream=None):
     norm, coef = _pointers(norm, coef)
     _call("moe_grad_clip", grads.n, _list_here(grads), None if out is None else out.address,
           norm, max_norm, coef, _stream(stream))
+
+
+def moe_dropout(dtype, n, x, residual, p, rng, out, stream=None):
+    x, residual, rng, out = _pointers(x, residual, rng, out)
+    _call("moe_dropout", dtype, n, x, residual, p, rng, out, _stream(stream))
+
+
+def moe_dropout_bwd(dy_dtype, dx_dtype, n, dy, p, rng, dx, stream=None):
+    dy, rng, dx = _pointers(dy, rng, dx)
+    _call("moe_dropout_bwd", dy_dtype, dx_dtype, n, dy, p, rng, dx, _stream(stream))
+
+
+def moe_adapter_workspace_size(shape: MoEAdapterShape) -> int:
+    return int(lib.moe_adapter_workspace_size(ctypes.byref(shape)))
+
+
+def moe_adapter_map_size(shape: MoEAdapterShape) -> int:
+    return int(lib.moe_adapter_map_size(ctypes.byref(shape)))
+
+
+def moe_adapter_rowwise(shape: MoEAdapterShape) -> bool:
+    return bool(lib.moe_adapter_rowwise(ctypes.byref(shape)))
+
+
+def _rows(t, T, d, ld):
+    """Address of a [T, d] matrix whose rows lie ld elements apart (0: dense), on the current device: the slice of a wider
+    matrix that the shape says. None and raw pointers pass as they are."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.get_device() != _current_device():
+        raise ValueError(f"a tensor of shape {tuple(t.shape)} on {t.device}: the current CUDA device is wanted")
+    if t.is_contiguous():
+        if T > 1 and ld not in (0, d):
+            raise ValueError(f"a dense tensor of shape {tuple(t.shape)}: rows {ld} elements apart are wanted")
+    elif t.dim() != 2 or t.stride(1) != 1 or t.stride(0) != (ld or d):
+        raise ValueError(f"a tensor of shape {tuple(t.shape)} and strides {t.stride()}: rows {ld or d} elements apart are wanted")
+    return t.data_ptr()
+
+
+def moe_adapter_map(shape, adapter_of, map, ws, stream=None):
+    adapter_of, map, ws = _pointers(adapter_of, map, ws)
+    _call("moe_adapter_map", ctypes.byref(shape), adapter_of, map, ws, _stream(stream))
+
+
+def moe_adapter(shape, x, A, B, scale, adapter_of, map, rng, base, y, u, ws, stream=None):
+    """x, base and y: dense, or slices [T, d] of wider matrices with shape.ld_in and shape.ld_out from row to row."""
+    A, B, scale, adapter_of, map, rng, u, ws = _pointers(A, B, scale, adapter_of, map, rng, u, ws)
+    x = _rows(x, shape.T, shape.d_in, shape.ld_in)
+    base, y = (_rows(t, shape.T, shape.d_out, shape.ld_out) for t in (base, y))
+    _call("moe_adapter", ctypes.byref(shape), x, A, B, scale, adapter_of, map, rng, base, y, u, ws, _stream(stream))
+
+
+def moe_adapter_bwd(shape, dx_dtype, dy, x, A, B, scale, map, rng, u, dx_in, dx, dA, dB, ws, stream=None):
+    """dy and x: as in moe_adapter; dx_in and dx are dense."""
+    A, B, scale, map, rng, u, dx_in, dx, dA, dB, ws = _pointers(A, B, scale, map, rng, u, dx_in, dx, dA, dB, ws)
+    dy, x = _rows(dy, shape.T, shape.d_out, shape.ld_out), _rows(x, shape.T, shape.d_in, shape.ld_in)
+    _call("moe_adapter_bwd", ctypes.byref(shape), dx_dtype, dy, x, A, B, scale, map, rng, u, dx_in, dx, dA, dB, ws,
+          _stream(stream))

@@ -1,0 +1,691 @@
+// Low-rank adapters chosen per token: the map of a batch, the row-by-row form
+// for few tokens, the fp32 kernels, and the launches of both types.
+//
+//   u_t = A_a drop(x_t),  y_t = base_t + s_a B_a u_t,  a = adapter of t,
+// and backward
+//   du_t = s_a B_a^T dy_t,  dx_t = dx_in_t + drop(A_a^T du_t),
+//   dA_a = sum_t du_t drop(x_t)^T,  dB_a = s_a sum_t dy_t u_t^T.
+// The mask goes on x as zeros and its factor 65536 / (65536 - t) on the fp32
+// sums, so x itself is never rounded a second time.
+#include "adapter.cuh"
+
+namespace moe {
+
+size_t adapter_scratch_bytes(int64_t T, int d_in, int d_out, int rank) {
+  return scratch_of(T, d_in, d_out, rank).bytes;
+}
+size_t adapter_map_bytes(int64_t T, int n) { return (size_t)map_layout(T, n).words * 4; }
+
+// Row by row every token reads its adapter (rank * (d_in + d_out) elements)
+// from L2; by tiles one reading serves up to 128 tokens, after a map.
+bool adapter_rowwise(int64_t T, int, int, int, int) { return T <= 64; }
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// The map: a stable counting sort by adapter in one launch. A cluster of CTAs
+// cuts the tokens into one run per warp; every warp counts its run, the counts
+// are added up over warps and CTAs, and every warp places its run.
+constexpr int kMapThreads = 1024;
+constexpr int kMapCtas = 8;
+constexpr size_t kMapSmem = 220 * 1024;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote_addr(const void *p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(r)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ int remote_int(const void *p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float remote_float(const void *p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote_addr(p, rank)) : "memory");
+  return v;
+}
+
+// largest e with first[e] <= i
+__device__ __forceinline__ int find_bin(const int *first, int bins, int i) {
+  int lo = 0, hi = bins - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kMapThreads) map_kernel(int64_t T, int n, int runs, const int32_t *adapter_of,
+                                                          int32_t *map, uint32_t *status) {
+  pdl_wait();
+  extern __shared__ int sm[];
+  const int bins = n + 1;   // the last: no adapter
+  int *hist = sm;                    // [runs][bins]
+  int *total = hist + runs * bins;   // of this CTA
+  int *all = total + bins;
+  int *off = all + bins;
+  int *tile0 = off + bins, *chunk0 = tile0 + bins, *slot0 = chunk0 + bins;
+  __shared__ int4 warp_sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int me = (int)cluster_rank(), ctas = (int)cluster_size();
+  const int64_t len = ((T + (int64_t)ctas * runs - 1) / ((int64_t)ctas * runs) + 31) / 32 * 32;
+  const int64_t lo = ((int64_t)me * runs + warp) * len, hi = lo + len < T ? lo + len : T;
+  const int64_t C = chunk_rows(T);
+
+  for (int i = tid; i < runs * bins; i += kMapThreads) hist[i] = 0;
+  __syncthreads();
+  if (warp < runs)
+    for (int64_t t = lo + lane; t < hi; t += 32) {
+      int e = adapter_of[t];
+      if (e < -1 || e >= n) report(status, MOE_ERR_DEVICE, kInfoAdapterRange);
+      if (e < 0 || e >= n) e = n;
+      atomicAdd(&hist[warp * bins + e], 1);
+    }
+  __syncthreads();
+  for (int e = tid; e < bins; e += kMapThreads) {
+    int sum = 0;
+    for (int w = 0; w < runs; ++w) {
+      const int c = hist[w * bins + e];
+      hist[w * bins + e] = sum;
+      sum += c;
+    }
+    total[e] = sum;
+  }
+  cluster_sync();
+  for (int e = tid; e < bins; e += kMapThreads) {
+    int before = 0, sum = 0;
+    for (int r = 0; r < ctas; ++r) {
+      const int c = remote_int(&total[e], (uint32_t)r);
+      if (r < me) before += c;
+      sum += c;
+    }
+    all[e] = sum;
+    for (int w = 0; w < runs; ++w) hist[w * bins + e] += before;
+  }
+  __syncthreads();
+  // exclusive sums over the bins of tokens, tiles, chunks and slots
+  const int per = (bins + kMapThreads - 1) / kMapThreads;
+  const int e0 = tid * per, e1 = e0 + per < bins ? e0 + per : bins;
+  auto counts = [&](int e) {
+    const int c = all[e];
+    const int k = e < n ? (int)((c + C - 1) / C) : 0;
+    return make_int4(c, (c + kTileRows - 1) / kTileRows, k, k > 1 ? k : 0);
+  };
+  int4 mine = make_int4(0, 0, 0, 0);
+  for (int e = e0; e < e1; ++e) {
+    const int4 c = counts(e);
+    mine.x += c.x; mine.y += c.y; mine.z += c.z; mine.w += c.w;
+  }
+  int4 inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
+    const int z = __shfl_up_sync(0xffffffffu, inc.z, o), w = __shfl_up_sync(0xffffffffu, inc.w, o);
+    if (lane >= o) { inc.x += x; inc.y += y; inc.z += z; inc.w += w; }
+  }
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int4 run = make_int4(inc.x - mine.x, inc.y - mine.y, inc.z - mine.z, inc.w - mine.w);
+  int4 sums = make_int4(0, 0, 0, 0);
+  for (int w = 0; w < 32; ++w) {
+    const int4 v = warp_sums[w];
+    if (w < warp) { run.x += v.x; run.y += v.y; run.z += v.z; run.w += v.w; }
+    sums.y += v.y;
+    sums.z += v.z;
+  }
+  for (int e = e0; e < e1; ++e) {
+    off[e] = run.x; tile0[e] = run.y; chunk0[e] = run.z; slot0[e] = run.w;
+    const int4 c = counts(e);
+    run.x += c.x; run.y += c.y; run.z += c.z; run.w += c.w;
+  }
+  __syncthreads();
+
+  if (warp < runs)
+    for (int64_t t0 = lo; t0 < hi; t0 += 32) {
+      const int64_t t = t0 + lane;
+      int e = t < hi ? adapter_of[t] : -2;
+      if (t < hi && (e < 0 || e >= n)) e = n;
+      const uint32_t same = __match_any_sync(0xffffffffu, e);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      int at = 0;
+      if (t < hi) {
+        at = hist[warp * bins + e];
+        map[kMapHeader + off[e] + at + rank] = (int32_t)t;
+      }
+      __syncwarp();
+      if (t < hi && rank == 0) hist[warp * bins + e] = at + __popc(same);
+      __syncwarp();
+    }
+  const MapLayout m = map_layout(T, n);
+  int4 *tiles = reinterpret_cast<int4 *>(map + m.tiles), *chunks = reinterpret_cast<int4 *>(map + m.chunks);
+  int2 *groups = reinterpret_cast<int2 *>(map + m.groups);
+  const int all_threads = ctas * kMapThreads, id = me * kMapThreads + tid;
+  for (int i = id; i < sums.y; i += all_threads) {
+    const int e = find_bin(tile0, bins, i), at = (i - tile0[e]) * kTileRows, left = all[e] - at;
+    tiles[i] = make_int4(e < n ? e : -1, off[e] + at, left < kTileRows ? left : kTileRows, 0);
+  }
+  for (int i = id; i < sums.z; i += all_threads) {
+    const int e = find_bin(chunk0, bins, i), k = i - chunk0[e];
+    const int64_t at = k * C, left = all[e] - at;
+    chunks[i] = make_int4(e, off[e] + (int)at, (int)(left < C ? left : C), all[e] > C ? slot0[e] + k : -1);
+  }
+  for (int e = id; e < n; e += all_threads) groups[e] = make_int2(slot0[e], (int)((all[e] + C - 1) / C));
+  if (id == 0) {
+    map[kMapT] = (int32_t)T;
+    map[kMapN] = n;
+    map[kMapTiles] = sums.y;
+    map[kMapChunks] = sums.z;
+  }
+  cluster_sync();   // no CTA leaves while another reads its counts
+}
+
+// ---------------------------------------------------------------------------
+// Elements in fours: 16 bytes of fp32, 8 of bf16.
+__device__ __forceinline__ void load4(const float *p, float (&v)[4]) {
+  const float4 q = *reinterpret_cast<const float4 *>(p);
+  v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&v)[4]) {
+  const uint2 q = *reinterpret_cast<const uint2 *>(p);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q.y));
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+__device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  uint2 q;
+  q.x = *reinterpret_cast<const uint32_t *>(&a);
+  q.y = *reinterpret_cast<const uint32_t *>(&b);
+  *reinterpret_cast<uint2 *>(p) = q;
+}
+// zeros in the dropped ones' place; i: index of the first in the dense matrix, a multiple of 4
+__device__ __forceinline__ void mask4(const Philox &g, int64_t i, float (&v)[4]) {
+  const uint4 w = g.block((uint64_t)i >> 3);
+  const bool high = (i & 4) != 0;
+  const uint32_t a = high ? w.z : w.x, b = high ? w.w : w.y;
+  if (a << 16 < g.threshold) v[0] = 0.0f;
+  if (a < g.threshold) v[1] = 0.0f;
+  if (b << 16 < g.threshold) v[2] = 0.0f;
+  if (b < g.threshold) v[3] = 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// Row by row: a cluster of 8 CTAs a token. Every CTA takes a part of d_in for u,
+// the parts meet in shared memory, and every CTA takes a part of d_out for y.
+constexpr int kRowCtas = 8, kRowThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) row_kernel(const AdapterArgs a, float keep_scale) {
+  pdl_wait();
+  __shared__ float part[128], us[128];
+  const int64_t t = blockIdx.x / kRowCtas;
+  const int q = (int)cluster_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = a.rank;
+  int ad = 0;
+  if (a.adapter_of != nullptr) {
+    ad = a.adapter_of[t];
+    if (ad < -1 || ad >= a.n) {
+      if (q == 0 && tid == 0) report(a.status, MOE_ERR_DEVICE, kInfoAdapterRange);
+      ad = -1;
+    }
+  }
+  const T *base = a.base != nullptr ? static_cast<const T *>(a.base) + t * a.ld_out : nullptr;
+  T *y = static_cast<T *>(a.y) + t * a.ld_out;
+  const int c0 = (int)((int64_t)a.d_out * q / kRowCtas), c1 = (int)((int64_t)a.d_out * (q + 1) / kRowCtas);
+  if (ad < 0) {   // the whole cluster
+    if (base != y)
+      for (int c = c0 + tid; c < c1; c += kRowThreads) y[c] = base != nullptr ? base[c] : from_f32<T>(0.0f);
+    if (a.u != nullptr && q == 0)
+      for (int j = tid; j < r; j += kRowThreads) a.u[t * r + j] = 0.0f;
+    return;
+  }
+  const T *x = static_cast<const T *>(a.x) + t * a.ld_in;
+  const T *A = static_cast<const T *>(a.A) + (int64_t)ad * r * a.d_in;
+  const T *B = static_cast<const T *>(a.B) + (int64_t)ad * a.d_out * r;
+  const Philox g(a.rng, a.threshold);
+  const int k0 = (int)((int64_t)(a.d_in / 4) * q / kRowCtas), k1 = (int)((int64_t)(a.d_in / 4) * (q + 1) / kRowCtas);
+  for (int j = warp; j < r; j += kRowThreads / 32) {
+    float sum = 0.0f;
+    for (int k = k0 + lane; k < k1; k += 32) {
+      float v[4], w[4];
+      load4(x + 4 * k, v);
+      if (a.threshold != 0) mask4(g, t * a.d_in + 4 * k, v);
+      load4(A + (int64_t)j * a.d_in + 4 * k, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum = fmaf(v[i], w[i], sum);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) part[j] = sum;
+  }
+  cluster_sync();
+  const float s = a.scale != nullptr ? a.scale[ad] : 1.0f;
+  for (int j = tid; j < r; j += kRowThreads) {
+    float v = 0.0f;
+    for (int c = 0; c < kRowCtas; ++c) v += remote_float(&part[j], (uint32_t)c);
+    v *= keep_scale;
+    if (a.u != nullptr && q == 0) a.u[t * r + j] = v;
+    us[j] = v;
+  }
+  cluster_sync();   // us is whole, and no CTA leaves while another reads its part
+  for (int c = c0 + tid; c < c1; c += kRowThreads) {
+    float sum = 0.0f;
+    for (int j = 0; j < r; j += 4) {
+      float w[4];
+      load4(B + (int64_t)c * r + j, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum = fmaf(us[j + i], w[i], sum);
+    }
+    y[c] = from_f32<T>(fmaf(s, sum, base != nullptr ? to_f32(base[c]) : 0.0f));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tiles on the CUDA cores.
+constexpr int kSimtThreads = 256;
+constexpr int kSimtRows = 32;   // positions a CTA: a quarter of a tile
+constexpr int kStep = 64, kPad = kStep + 4;
+
+struct Shrink {   // v[pos] = factor W_a drop(x[token]), W_a [rank, d], or [d, rank] (WT)
+  Plan plan;
+  const void *x, *W;
+  int64_t ld;
+  int d, rank;
+  uint32_t threshold;
+  const uint64_t *rng;
+  const float *scale;   // per adapter, or NULL
+  float factor;
+  float *by_pos;        // [T, rank]
+  float *by_token;      // [T, rank], or NULL; 0 without an adapter
+};
+
+template <typename T, bool WT>
+__global__ void __launch_bounds__(kSimtThreads) shrink_kernel(const Shrink p) {
+  pdl_wait();
+  __shared__ __align__(16) float xs[kSimtRows * kPad];
+  __shared__ __align__(16) float ws[128 * kPad];
+  __shared__ int64_t tok[kSimtRows];
+  const int64_t ti = blockIdx.x / 4;
+  if (ti >= p.plan.tiles()) return;
+  const int4 tile = p.plan.tile(ti);
+  const int r0 = (int)(blockIdx.x % 4) * kSimtRows, rows = min(kSimtRows, tile.z - r0), tid = threadIdx.x;
+  if (rows <= 0) return;
+  if (tid < kSimtRows) tok[tid] = tid < rows ? p.plan.token(tile.y + r0 + tid) : -1;
+  __syncthreads();
+  const int r = p.rank;
+  if (tile.x < 0) {
+    if (p.by_token != nullptr)
+      for (int i = tid; i < rows * r; i += kSimtThreads) p.by_token[tok[i / r] * r + i % r] = 0.0f;
+    return;
+  }
+  const T *W = static_cast<const T *>(p.W) + (int64_t)tile.x * r * p.d;
+  const T *x = static_cast<const T *>(p.x);
+  const Philox g(p.rng, p.threshold);
+  // 4 x 4 results a thread; the threads beyond one set of them share the steps' k
+  const int set = 8 * (r / 4), sets = kSimtThreads / set, mine = tid / set, at = tid % set;
+  const int jr = (at % (r / 4)) * 4, rr = (at / (r / 4)) * 4;
+  float acc[4][4] = {};
+  for (int k0 = 0; k0 < p.d; k0 += kStep) {
+    for (int i = tid; i < kSimtRows * (kStep / 4); i += kSimtThreads) {
+      const int row = i / (kStep / 4), k = (i % (kStep / 4)) * 4;
+      float v[4] = {};
+      if (tok[row] >= 0 && k0 + k < p.d) {
+        load4(x + tok[row] * p.ld + k0 + k, v);
+        if (p.threshold != 0) mask4(g, tok[row] * p.d + k0 + k, v);
+      }
+      store4(xs + row * kPad + k, v);
+    }
+    if constexpr (!WT) {
+      for (int i = tid; i < r * (kStep / 4); i += kSimtThreads) {
+        const int j = i / (kStep / 4), k = (i % (kStep / 4)) * 4;
+        float v[4] = {};
+        if (k0 + k < p.d) load4(W + (int64_t)j * p.d + k0 + k, v);
+        store4(ws + j * kPad + k, v);
+      }
+    } else {
+      for (int i = tid; i < (r / 4) * kStep; i += kSimtThreads) {
+        const int j = (i % (r / 4)) * 4, k = i / (r / 4);
+        float v[4] = {};
+        if (k0 + k < p.d) load4(W + (int64_t)(k0 + k) * r + j, v);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ws[(j + c) * kPad + k] = v[c];
+      }
+    }
+    __syncthreads();
+    if (mine < sets)
+      for (int k = mine * 4; k < kStep; k += sets * 4) {
+        float xv[4][4], wv[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          load4(xs + (rr + i) * kPad + k, xv[i]);
+          load4(ws + (jr + i) * kPad + k, wv[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][j] = fmaf(xv[i][c], wv[j][c], acc[i][j]);
+      }
+    __syncthreads();
+  }
+  // sets in order: [set][row][rank] in ws (at most 256 / set sets of 32 rank floats)
+  if (mine < sets)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store4(ws + (mine * kSimtRows + rr + i) * r + jr, acc[i]);
+  __syncthreads();
+  const float f = p.factor * (p.scale != nullptr ? p.scale[tile.x] : 1.0f);
+  for (int i = tid; i < rows * r; i += kSimtThreads) {
+    float v = 0.0f;
+    for (int c = 0; c < sets; ++c) v += ws[c * kSimtRows * r + i];
+    v *= f;
+    if (p.by_pos != nullptr) p.by_pos[(int64_t)(tile.y + r0) * r + i] = v;
+    if (p.by_token != nullptr) p.by_token[tok[i / r] * r + i % r] = v;
+  }
+}
+
+struct Expand {   // out[token] = base[token] + factor mask(V_a v[pos]), V_a [d, rank], or [rank, d] (VT)
+  Plan plan;
+  const float *v;   // [T, rank] by position
+  const void *V, *base;
+  void *out;
+  int64_t ld;
+  int d, rank;
+  uint32_t threshold;
+  const uint64_t *rng;
+  const float *scale;
+  float factor;
+};
+constexpr int kExpandCols = 128;
+
+template <typename T, typename TO, bool VT>
+__global__ void __launch_bounds__(kSimtThreads) expand_kernel(const Expand p) {
+  pdl_wait();
+  __shared__ __align__(16) float us[kSimtRows][36];
+  __shared__ __align__(16) float wt[32][kExpandCols + 4];
+  __shared__ int64_t tok[kSimtRows];
+  const int64_t ti = blockIdx.x / 4;
+  if (ti >= p.plan.tiles()) return;
+  const int4 tile = p.plan.tile(ti);
+  const int r0 = (int)(blockIdx.x % 4) * kSimtRows, rows = min(kSimtRows, tile.z - r0), tid = threadIdx.x;
+  if (rows <= 0) return;
+  const TO *base = static_cast<const TO *>(p.base);
+  TO *out = static_cast<TO *>(p.out);
+  if (tile.x < 0 && base == out) return;
+  if (tid < kSimtRows) tok[tid] = tid < rows ? p.plan.token(tile.y + r0 + tid) : -1;
+  __syncthreads();
+  const int r = p.rank, c0 = blockIdx.y * kExpandCols, cc = (tid % 32) * 4, rr = (tid / 32) * 4;
+  const Philox g(p.rng, p.threshold);
+  float acc[4][4] = {};
+  float f = 0.0f;
+  if (tile.x >= 0) {
+    f = p.factor * (p.scale != nullptr ? p.scale[tile.x] : 1.0f);
+    const T *V = static_cast<const T *>(p.V) + (int64_t)tile.x * r * p.d;
+    for (int j0 = 0; j0 < r; j0 += 32) {
+      const int nj = min(32, r - j0);
+      for (int i = tid; i < kSimtRows * 8; i += kSimtThreads) {
+        const int row = i / 8, j = (i % 8) * 4;
+        float v[4] = {};
+        if (row < rows && j < nj) load4(p.v + (int64_t)(tile.y + r0 + row) * r + j0 + j, v);
+        store4(&us[row][j], v);
+      }
+      if constexpr (!VT) {
+        for (int i = tid; i < kExpandCols * 8; i += kSimtThreads) {
+          const int c = i / 8, j = (i % 8) * 4;
+          float v[4] = {};
+          if (j < nj && c0 + c < p.d) load4(V + (int64_t)(c0 + c) * r + j0 + j, v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) wt[j + k][c] = v[k];
+        }
+      } else {
+        for (int i = tid; i < 32 * (kExpandCols / 4); i += kSimtThreads) {
+          const int j = i / (kExpandCols / 4), c = (i % (kExpandCols / 4)) * 4;
+          float v[4] = {};
+          if (j < nj && c0 + c < p.d) load4(V + (int64_t)(j0 + j) * p.d + c0 + c, v);
+          store4(&wt[j][c], v);
+        }
+      }
+      __syncthreads();
+      for (int j = 0; j < nj; ++j) {
+        float w[4];
+        load4(&wt[j][cc], w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[i][c] = fmaf(us[rr + i][j], w[c], acc[i][c]);
+      }
+      __syncthreads();
+    }
+  }
+  if (c0 + cc >= p.d) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (rr + i >= rows) break;
+    const int64_t t = tok[rr + i];
+    float b[4] = {};
+    if (base != nullptr) load4(base + t * p.ld + c0 + cc, b);
+    if (p.threshold != 0 && tile.x >= 0) mask4(g, t * p.d + c0 + cc, acc[i]);
+    if (tile.x >= 0)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) b[c] = fmaf(f, acc[i][c], b[c]);
+    store4(out + t * p.ld + c0 + cc, b);
+  }
+}
+
+struct Wgrad {   // G_a = factor sum_t v_t z_t^T over a chunk: [rank, d], or [d, rank] (GT)
+  Plan plan;
+  const void *z;
+  const float *v;
+  int v_by_token;
+  int64_t ld;
+  int d, rank;
+  uint32_t threshold;
+  const uint64_t *rng;
+  const float *scale;
+  float factor;
+  float *out, *partial;   // [n, rank d], [slots, rank d]
+};
+constexpr int kGradCols = 64;
+
+template <typename T, bool GT>
+__global__ void __launch_bounds__(kSimtThreads) wgrad_kernel(const Wgrad p) {
+  pdl_wait();
+  __shared__ __align__(16) float buf[256 / 2 * 64];   // 32 KB: 32 rows of z and of v, then the sets' sums
+  float (*zs)[kGradCols + 4] = reinterpret_cast<float(*)[kGradCols + 4]>(buf);
+  float (*vs)[128] = reinterpret_cast<float(*)[128]>(buf + 32 * (kGradCols + 4));
+  __shared__ int64_t tok[32];
+  if (blockIdx.x >= p.plan.chunks()) return;
+  const int4 ch = p.plan.chunk(blockIdx.x);
+  if (ch.z <= 0) return;
+  const int r = p.rank, r8 = (r + 7) / 8, c0 = blockIdx.y * kGradCols, tid = threadIdx.x;
+  const int set = r8 * 16, sets = kSimtThreads / set, mine = tid / set, at = tid % set;
+  const int jj = (at / 16) * 8, cc = (at % 16) * 4;
+  const T *z = static_cast<const T *>(p.z);
+  const Philox g(p.rng, p.threshold);
+  float acc[8][4] = {};
+  for (int i0 = 0; i0 < ch.z; i0 += 32) {
+    const int rows = min(32, ch.z - i0);
+    if (tid < 32) tok[tid] = tid < rows ? p.plan.token(ch.y + i0 + tid) : -1;
+    __syncthreads();
+    for (int i = tid; i < 32 * (kGradCols / 4); i += kSimtThreads) {
+      const int row = i / (kGradCols / 4), c = (i % (kGradCols / 4)) * 4;
+      float v[4] = {};
+      if (row < rows && c0 + c < p.d) {
+        load4(z + tok[row] * p.ld + c0 + c, v);
+        if (p.threshold != 0) mask4(g, tok[row] * p.d + c0 + c, v);
+      }
+      store4(&zs[row][c], v);
+    }
+    for (int i = tid; i < 32 * 2 * r8; i += kSimtThreads) {
+      const int row = i / (2 * r8), j = (i % (2 * r8)) * 4;
+      float v[4] = {};
+      if (row < rows && j < r) load4(p.v + (p.v_by_token ? tok[row] : (int64_t)(ch.y + i0 + row)) * r + j, v);
+      store4(&vs[row][j], v);
+    }
+    __syncthreads();
+    if (mine < sets)
+      for (int row = mine; row < 32; row += sets) {
+        float w[4], a[4], b[4];
+        load4(&zs[row][cc], w);
+        load4(&vs[row][jj], a);
+        load4(&vs[row][jj + 4], b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            acc[i][c] = fmaf(a[i], w[c], acc[i][c]);
+            acc[4 + i][c] = fmaf(b[i], w[c], acc[4 + i][c]);
+          }
+      }
+    __syncthreads();
+  }
+  if (mine < sets)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) store4(buf + ((mine * r8 * 8 + jj + i) * kGradCols + cc), acc[i]);
+  __syncthreads();
+  const float f = p.factor * (p.scale != nullptr ? p.scale[ch.x] : 1.0f);
+  float *out = ch.w < 0 ? p.out + (int64_t)ch.x * r * p.d : p.partial + (int64_t)ch.w * r * p.d;
+  for (int i = tid; i < r * kGradCols; i += kSimtThreads) {
+    const int j = GT ? i % r : i / kGradCols, c = GT ? i / r : i % kGradCols;
+    if (c0 + c >= p.d) continue;
+    float v = 0.0f;
+    for (int k = 0; k < sets; ++k) v += buf[(k * r8 * 8 + j) * kGradCols + c];
+    out[GT ? (int64_t)(c0 + c) * r + j : (int64_t)j * p.d + c0 + c] = f * v;
+  }
+}
+
+// The second pass: zeros for adapters without tokens, the chunks' sums in order
+// for those of several; nothing to do for one chunk.
+constexpr int kJoinThreads = 256, kJoinEach = 4;
+
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(Plan plan, int64_t na, int64_t nb, float *dA, float *dB,
+                                                            const float *pa, const float *pb) {
+  pdl_wait();
+  if (!plan.of_this_batch()) return;
+  const int a = blockIdx.y;
+  const int2 g = plan.group(a);
+  if (g.y == 1) return;
+  const int64_t step = (int64_t)gridDim.x * kJoinThreads * 4;
+  for (int64_t i = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 4; i < na + nb; i += step) {
+    const bool second = i >= na;   // na and nb are multiples of 4
+    const int64_t n = second ? nb : na, k = second ? i - na : i;
+    const float *p = second ? pb : pa;
+    float v[4] = {};
+    for (int c = 0; c < g.y; ++c) {
+      float w[4];
+      load4(p + (g.x + c) * n + k, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += w[j];
+    }
+    store4((second ? dB : dA) + a * n + k, v);
+  }
+}
+
+template <typename T, bool WT>
+cudaError_t shrink(const AdapterArgs &a, const Shrink &p, cudaStream_t s) {
+  return launch_pdl(shrink_kernel<T, WT>, dim3((unsigned)(host_tiles(a) * 4)), dim3(kSimtThreads), 0, s, p);
+}
+template <typename T, typename TO, bool VT>
+cudaError_t expand(const AdapterArgs &a, const Expand &p, cudaStream_t s) {
+  return launch_pdl(expand_kernel<T, TO, VT>,
+                    dim3((unsigned)(host_tiles(a) * 4), (unsigned)((p.d + kExpandCols - 1) / kExpandCols)),
+                    dim3(kSimtThreads), 0, s, p);
+}
+template <typename T, bool GT>
+cudaError_t wgrad(const AdapterArgs &a, const Wgrad &p, cudaStream_t s) {
+  return launch_pdl(wgrad_kernel<T, GT>,
+                    dim3((unsigned)host_chunks(a), (unsigned)((p.d + kGradCols - 1) / kGradCols)),
+                    dim3(kSimtThreads), 0, s, p);
+}
+
+template <typename T> cudaError_t forward(const AdapterArgs &a, cudaStream_t s) {
+  const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
+  float *u = reinterpret_cast<float *>(a.ws + sc.u);
+  const Plan plan = plan_of(a);
+  const Shrink sh{plan, a.x, a.A, a.ld_in, a.d_in, a.rank, a.threshold, a.rng, nullptr, drop_scale(a.threshold), u, a.u};
+  cudaError_t e = shrink<T, false>(a, sh, s);
+  if (e != cudaSuccess) return e;
+  const Expand ex{plan, u, a.B, a.base, a.y, a.ld_out, a.d_out, a.rank, 0, nullptr, a.scale, 1.0f};
+  return expand<T, T, false>(a, ex, s);
+}
+
+template <typename T> cudaError_t backward(const AdapterArgs &a, cudaStream_t s) {
+  const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
+  float *du = reinterpret_cast<float *>(a.ws + sc.du);
+  const Plan plan = plan_of(a);
+  const float keep = drop_scale(a.threshold);
+  const Shrink sh{plan, a.dy, a.B, a.ld_out, a.d_out, a.rank, 0, nullptr, a.scale, 1.0f, du, nullptr};
+  cudaError_t e = shrink<T, true>(a, sh, s);
+  if (e == cudaSuccess && a.dA != nullptr) {
+    const Wgrad wa{plan, a.x, du, 0, a.ld_in, a.d_in, a.rank, a.threshold, a.rng, nullptr, keep, a.dA,
+                   reinterpret_cast<float *>(a.ws + sc.dA)};
+    const Wgrad wb{plan, a.dy, a.u_in, 1, a.ld_out, a.d_out, a.rank, 0, nullptr, a.scale, 1.0f, a.dB,
+                   reinterpret_cast<float *>(a.ws + sc.dB)};
+    e = wgrad<T, false>(a, wa, s);
+    if (e == cudaSuccess) e = wgrad<T, true>(a, wb, s);
+    if (e == cudaSuccess) e = launch_adapter_join(a, s);
+  }
+  if (e == cudaSuccess && a.dx != nullptr) {
+    const Expand ex{plan, du, a.A, a.dx_in, a.dx, a.d_in, a.d_in, a.rank, a.threshold, a.rng, nullptr, keep};
+    e = a.dx_dtype == MOE_F32 ? expand<T, float, true>(a, ex, s) : expand<T, __nv_bfloat16, true>(a, ex, s);
+  }
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_adapter_join(const AdapterArgs &a, cudaStream_t s) {
+  const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
+  const int64_t na = (int64_t)a.rank * a.d_in, nb = (int64_t)a.rank * a.d_out;
+  const int64_t each = kJoinThreads * 4 * kJoinEach, ctas = (na + nb + each - 1) / each;
+  return launch_pdl(join_kernel, dim3((unsigned)ctas, (unsigned)a.n), dim3(kJoinThreads), 0, s, plan_of(a), na, nb, a.dA,
+                    a.dB, reinterpret_cast<const float *>(a.ws + sc.dA), reinterpret_cast<const float *>(a.ws + sc.dB));
+}
+
+cudaError_t launch_adapter_map(int64_t T, int n, const int32_t *adapter_of, int32_t *map, uint32_t *status,
+                               cudaStream_t s) {
+  const int bins = n + 1;
+  int runs = (int)(kMapSmem / 4 / bins) - 6;
+  if (runs > 32) runs = 32;
+  const size_t smem = (size_t)(runs + 6) * bins * 4;
+  cudaError_t e = cudaFuncSetAttribute(map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMapSmem);
+  if (e != cudaSuccess) return e;
+  const int ctas = T <= 4096 ? 1 : kMapCtas;   // a run of up to 128 tokens a warp
+  return launch_pdl_clusters(map_kernel, dim3((unsigned)ctas), dim3(kMapThreads), ctas, smem, s, T, n, runs, adapter_of,
+                             map, status);
+}
+
+cudaError_t launch_adapter(const AdapterArgs &a, cudaStream_t s) {
+  if (a.map == nullptr && (a.adapter_of != nullptr || adapter_rowwise(a.T, a.d_in, a.d_out, a.n, a.rank))) {
+    const float keep = drop_scale(a.threshold);
+    const dim3 grid((unsigned)(a.T * kRowCtas));
+    if (a.dtype == MOE_F32) return launch_pdl_clusters(row_kernel<float>, grid, dim3(kRowThreads), kRowCtas, 0, s, a, keep);
+    return launch_pdl_clusters(row_kernel<__nv_bfloat16>, grid, dim3(kRowThreads), kRowCtas, 0, s, a, keep);
+  }
+  return a.dtype == MOE_F32 ? forward<float>(a, s) : forward<__nv_bfloat16>(a, s);
+}
+
+cudaError_t launch_adapter_bwd(const AdapterArgs &a, cudaStream_t s) {
+  return a.dtype == MOE_F32 ? backward<float>(a, s) : backward<__nv_bfloat16>(a, s);
+}
+
+}  // namespace moe

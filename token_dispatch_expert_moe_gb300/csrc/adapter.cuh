@@ -1,0 +1,145 @@
+// What the kernels of the adapters share: the map of a batch, its tiles and
+// chunks, and where the scratch lies in the workspace.
+#pragma once
+#include "launch.cuh"
+#include "philox.cuh"
+
+namespace moe {
+
+constexpr int kTileRows = 128;   // tokens of a tile, all of one adapter
+
+// Tokens of a chunk: the weight gradients are summed over a chunk's tokens in
+// one CTA, and over an adapter's chunks in a second pass. An eighth of the
+// batch gives that pass few partial sums and the first enough CTAs.
+__host__ __device__ constexpr int64_t chunk_rows(int64_t T) {
+  const int64_t e = (T / 8 + kTileRows - 1) / kTileRows * kTileRows;
+  return e < 512 ? 512 : e;
+}
+// An adapter of several chunks has more than one chunk's tokens, so at most
+// twice as many chunks as full ones.
+constexpr int kMaxSlots = 16;
+
+// The map, in 32-bit words: a header, order [T] (the tokens by adapter, in
+// their order inside one; those without an adapter last), and, 16-byte aligned,
+// tiles, chunks and groups.
+constexpr int kMapHeader = 16;
+enum { kMapT = 0, kMapN = 1, kMapTiles = 2, kMapChunks = 3 };
+// tile: {adapter or -1, first position, rows, 0};
+// chunk: {adapter, first position, rows, slot of its partial sum, or -1: the only one of its adapter}
+// group: {first slot, chunks} of an adapter
+struct MapLayout {
+  int64_t order, tiles, chunks, groups, words;
+  int64_t max_tiles, max_chunks;
+};
+__host__ __device__ inline MapLayout map_layout(int64_t T, int n) {
+  MapLayout m;
+  const int64_t few = n + 1 < T ? n + 1 : T, used = n < T ? n : T;
+  m.max_tiles = T / kTileRows + few;
+  m.max_chunks = T / chunk_rows(T) + used;
+  m.order = kMapHeader;
+  m.tiles = m.order + (T + 3) / 4 * 4;
+  m.chunks = m.tiles + 4 * m.max_tiles;
+  m.groups = m.chunks + 4 * m.max_chunks;
+  m.words = m.groups + 2 * (int64_t)n;
+  return m;
+}
+
+// The tokens' grouping as a kernel reads it: a map, or none: adapter 0 for all
+// tokens in their order. Whatever the map's words hold, tiles and chunks stay
+// inside the batch.
+struct Plan {
+  const int32_t *map;   // NULL: none
+  int64_t T;
+  int n;
+  uint32_t *status;
+
+  __device__ __forceinline__ bool of_this_batch() const {
+    if (map == nullptr) return true;
+    if (map[kMapT] == (int32_t)T && map[kMapN] == n) return true;
+    report(status, MOE_ERR_DEVICE, kInfoAdapterMap);
+    return false;
+  }
+  __device__ __forceinline__ int64_t tiles() const {
+    if (map == nullptr) return (T + kTileRows - 1) / kTileRows;
+    if (!of_this_batch()) return 0;
+    const int64_t m = map_layout(T, n).max_tiles, k = map[kMapTiles];
+    return k < m ? k : m;
+  }
+  __device__ __forceinline__ int64_t chunks() const {
+    if (map == nullptr) return (T + chunk_rows(T) - 1) / chunk_rows(T);
+    if (!of_this_batch()) return 0;
+    const int64_t m = map_layout(T, n).max_chunks, k = map[kMapChunks];
+    return k < m ? k : m;
+  }
+  __device__ __forceinline__ int4 checked(int4 t, int64_t most) const {
+    if (t.x < -1 || t.x >= n || t.y < 0 || t.z < 0 || t.z > most || (int64_t)t.y + t.z > T) {
+      report(status, MOE_ERR_DEVICE, kInfoAdapterMap);
+      t = make_int4(-1, 0, 0, -1);
+    }
+    return t;
+  }
+  __device__ __forceinline__ int4 tile(int64_t i) const {
+    if (map == nullptr) {
+      const int64_t left = T - i * kTileRows;
+      return make_int4(0, (int)(i * kTileRows), (int)(left < kTileRows ? left : kTileRows), 0);
+    }
+    return checked(reinterpret_cast<const int4 *>(map + map_layout(T, n).tiles)[i], kTileRows);
+  }
+  __device__ __forceinline__ int4 chunk(int64_t i) const {
+    const int64_t C = chunk_rows(T);
+    if (map == nullptr) {
+      const int64_t left = T - i * C;
+      return make_int4(0, (int)(i * C), (int)(left < C ? left : C), T > C ? (int)i : -1);
+    }
+    int4 c = checked(reinterpret_cast<const int4 *>(map + map_layout(T, n).chunks)[i], C);
+    if (c.x < 0 || c.w >= kMaxSlots) c.z = 0;
+    return c;
+  }
+  __device__ __forceinline__ int2 group(int a) const {
+    if (map == nullptr) {
+      const int64_t k = (T + chunk_rows(T) - 1) / chunk_rows(T);
+      return a == 0 ? make_int2(0, (int)k) : make_int2(0, 0);
+    }
+    int2 g = reinterpret_cast<const int2 *>(map + map_layout(T, n).groups)[a];
+    if (g.y > 1 && (g.x < 0 || g.x + g.y > kMaxSlots)) g = make_int2(0, 0);
+    return g;
+  }
+  __device__ __forceinline__ int64_t token(int64_t pos) const {
+    if (map == nullptr) return pos;
+    const int64_t t = map[kMapHeader + pos];
+    if ((uint64_t)t < (uint64_t)T) return t;
+    report(status, MOE_ERR_DEVICE, kInfoAdapterMap);
+    return 0;
+  }
+};
+
+inline Plan plan_of(const AdapterArgs &a) { return Plan{a.map, a.T, a.n, a.status}; }
+inline int64_t host_tiles(const AdapterArgs &a) {
+  return a.map != nullptr ? map_layout(a.T, a.n).max_tiles : (a.T + kTileRows - 1) / kTileRows;
+}
+inline int64_t host_chunks(const AdapterArgs &a) {
+  return a.map != nullptr ? map_layout(a.T, a.n).max_chunks : (a.T + chunk_rows(a.T) - 1) / chunk_rows(a.T);
+}
+
+// Scratch: u and du by position, then the chunks' partial sums.
+struct Scratch {
+  size_t u, du, dA, dB, bytes;
+};
+__host__ inline Scratch scratch_of(int64_t T, int d_in, int d_out, int rank) {
+  auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+  Scratch s;
+  // fp32 [T, rank], or bf16 [T, 2 rank rounded up to 16]: the two parts of u
+  const size_t each = up((size_t)T * ((rank + 15) / 16 * 16) * 4);
+  const size_t slots = T > chunk_rows(T) ? kMaxSlots : 0;
+  s.u = 0;
+  s.du = each;
+  s.dA = 2 * each;
+  s.dB = s.dA + up(slots * rank * (size_t)d_in * 4);
+  s.bytes = s.dB + up(slots * rank * (size_t)d_out * 4);
+  return s;
+}
+
+// The second pass of the weight gradients (adapter.cu).
+cudaError_t launch_adapter_join(const AdapterArgs &a, cudaStream_t s);
+
+}  // namespace moe

@@ -11,6 +11,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "common.cuh"
+#include "philox.cuh"
 
 using namespace moe;
 
@@ -734,6 +735,187 @@ moe_status_t moe_grad_clip(int32_t n, const moe_tensor_t *grads, const moe_tenso
       if (out[i].numel != grads[i].numel || out[i].dtype != grads[i].dtype) return MOE_ERR_INVALID_ARG;
   if (clip_overlap(n, grads, out, norm, coef)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_grad_clip(n, grads, out, norm, max_norm, coef, (cudaStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------
+// Dropout and adapters
+
+static bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+static bool p_ok(float p) { return p >= 0.0f && p < 1.0f; }   // false for a NaN
+
+static moe_status_t dropout(int32_t in_dtype, int32_t out_dtype, int64_t n, const void *x,
+                            const void *residual, float p, const uint64_t *rng, void *out,
+                            moe_stream_t stream) {
+  if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype) || n < 0 || !p_ok(p)) return MOE_ERR_INVALID_ARG;
+  if (n >= (int64_t(1) << 42)) return MOE_ERR_UNSUPPORTED;
+  const uint32_t threshold = drop_threshold(p);
+  if (n == 0) return MOE_OK;
+  if (!x || !out || (threshold != 0 && !rng)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(out) || !aligned8(rng)) return MOE_ERR_INVALID_ARG;
+  const size_t nb = (size_t)n * size_of(out_dtype), xb = (size_t)n * size_of(in_dtype);
+  const bool on_x = out == x && in_dtype == out_dtype;
+  if ((!on_x && overlap(out, nb, x, xb)) || (out != residual && overlap(out, nb, residual, nb)) ||
+      overlap(out, nb, rng, 16))
+    return MOE_ERR_INVALID_ARG;
+  DropoutArgs a{};
+  a.n = n; a.in_dtype = in_dtype; a.out_dtype = out_dtype; a.threshold = threshold; a.x = x;
+  a.residual = residual; a.rng = threshold != 0 ? rng : nullptr; a.out = out;
+  return cuda_status(launch_dropout(a, (cudaStream_t)stream));
+}
+
+moe_status_t moe_dropout(int32_t dtype, int64_t n, const void *x, const void *residual, float p,
+                         const uint64_t *rng, void *out, moe_stream_t stream) {
+  NvtxRange trace("moe_dropout");
+  return dropout(dtype, dtype, n, x, residual, p, rng, out, stream);
+}
+
+moe_status_t moe_dropout_bwd(int32_t dy_dtype, int32_t dx_dtype, int64_t n, const void *dy, float p,
+                             const uint64_t *rng, void *dx, moe_stream_t stream) {
+  NvtxRange trace("moe_dropout_bwd");
+  return dropout(dy_dtype, dx_dtype, n, dy, nullptr, p, rng, dx, stream);
+}
+
+// MOE_OK for a set of adapters that the kernels take
+static moe_status_t adapter_check(const moe_adapter_shape_t *s) {
+  if (s == nullptr || !dtype_ok(s->dtype)) return MOE_ERR_INVALID_ARG;
+  const int v = s->dtype == MOE_BF16 ? 8 : 4;
+  if (s->T < 0 || s->d_in < 1 || s->d_out < 1 || s->n < 1 || s->rank < 1 || s->d_in % v != 0 ||
+      s->d_out % v != 0 || s->rank % v != 0 || !p_ok(s->dropout))
+    return MOE_ERR_INVALID_ARG;
+  if ((s->ld_in != 0 && (s->ld_in < s->d_in || s->ld_in % v != 0)) ||
+      (s->ld_out != 0 && (s->ld_out < s->d_out || s->ld_out % v != 0)))
+    return MOE_ERR_INVALID_ARG;
+  if (s->T >= (int64_t(1) << 31) || s->n > 4096 || s->rank > 128 || s->d_in > (1 << 20) ||
+      s->d_out > (1 << 20) || s->ld_in >= (int64_t(1) << 31) || s->ld_out >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// A matrix of rows whose starts lie ld bytes apart.
+struct Rows {
+  const void *p;
+  size_t ld, width;
+};
+// Whether two matrices of T rows share memory. Columns of one wider matrix do
+// not, where neither's lie in the other's.
+static bool rows_overlap(int64_t T, const Rows &a, const Rows &b) {
+  if (!overlap(a.p, (size_t)(T - 1) * a.ld + a.width, b.p, (size_t)(T - 1) * b.ld + b.width)) return false;
+  if (a.ld != b.ld) return true;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const size_t shift = pb >= pa ? (pb - pa) % a.ld : (a.ld - (pa - pb) % a.ld) % a.ld;
+  return shift < a.width || shift + b.width > a.ld;
+}
+
+size_t moe_adapter_workspace_size(const moe_adapter_shape_t *shape) {
+  if (adapter_check(shape) != MOE_OK) return 0;
+  return kStatusBytes + align256(adapter_scratch_bytes(shape->T, shape->d_in, shape->d_out, shape->rank));
+}
+
+size_t moe_adapter_map_size(const moe_adapter_shape_t *shape) {
+  if (adapter_check(shape) != MOE_OK) return 0;
+  return align256(adapter_map_bytes(shape->T, shape->n));
+}
+
+int32_t moe_adapter_rowwise(const moe_adapter_shape_t *shape) {
+  if (adapter_check(shape) != MOE_OK) return 0;
+  return adapter_rowwise(shape->T, shape->d_in, shape->d_out, shape->n, shape->rank) ? 1 : 0;
+}
+
+moe_status_t moe_adapter_map(const moe_adapter_shape_t *shape, const int32_t *adapter_of, void *map,
+                             void *ws, moe_stream_t stream) {
+  NvtxRange trace("moe_adapter_map");
+  const moe_status_t st = adapter_check(shape);
+  if (st != MOE_OK) return st;
+  if (shape->T == 0) return MOE_OK;
+  if (!adapter_of || !map || !ws || !aligned4(adapter_of) || !aligned16(map) || !aligned16(ws))
+    return MOE_ERR_INVALID_ARG;
+  const Span written[] = {{map, moe_adapter_map_size(shape)}, {ws, kStatusBytes}};
+  const Span read[] = {{adapter_of, (size_t)shape->T * 4}};
+  if (any_overlap(written, read)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_adapter_map(shape->T, shape->n, adapter_of, static_cast<int32_t *>(map),
+                                        status_word(ws), (cudaStream_t)stream));
+}
+
+static AdapterArgs adapter_args(const moe_adapter_shape_t *s, void *ws) {
+  AdapterArgs a{};
+  a.T = s->T; a.d_in = s->d_in; a.d_out = s->d_out; a.n = s->n; a.rank = s->rank; a.dtype = s->dtype;
+  a.ld_in = s->ld_in != 0 ? s->ld_in : s->d_in;
+  a.ld_out = s->ld_out != 0 ? s->ld_out : s->d_out;
+  a.threshold = drop_threshold(s->dropout);
+  a.ws = static_cast<char *>(ws) + kStatusBytes;
+  a.status = status_word(ws);
+  return a;
+}
+
+moe_status_t moe_adapter(const moe_adapter_shape_t *shape, const void *x, const void *A,
+                         const void *B, const float *scale, const int32_t *adapter_of,
+                         const void *map, const uint64_t *rng, const void *base, void *y, float *u,
+                         void *ws, moe_stream_t stream) {
+  NvtxRange trace("moe_adapter");
+  const moe_status_t st = adapter_check(shape);
+  if (st != MOE_OK) return st;
+  if (shape->T == 0) return MOE_OK;
+  AdapterArgs a = adapter_args(shape, ws);
+  if (!x || !A || !B || !y || !ws || (a.threshold != 0 && !rng)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(A) || !aligned16(B) || !aligned4(scale) || !aligned4(adapter_of) ||
+      !aligned16(map) || !aligned8(rng) || !aligned16(base) || !aligned16(y) || !aligned16(u) || !aligned16(ws))
+    return MOE_ERR_INVALID_ARG;
+  if (map == nullptr && a.T >= (int64_t(1) << 28)) return MOE_ERR_UNSUPPORTED;   // 8 CTAs a row
+  const size_t b = size_of(a.dtype), T = (size_t)a.T, r = (size_t)a.rank;
+  const Rows in{x, a.ld_in * b, a.d_in * b}, out{y, a.ld_out * b, a.d_out * b}, add{base, a.ld_out * b, a.d_out * b};
+  if (rows_overlap(a.T, out, in) || (base != y && base != nullptr && rows_overlap(a.T, out, add)))
+    return MOE_ERR_INVALID_ARG;
+  const size_t ny = (T - 1) * out.ld + out.width, nx = (T - 1) * in.ld + in.width;
+  const size_t nA = (size_t)a.n * r * a.d_in * b, nB = (size_t)a.n * r * a.d_out * b;
+  const Span written[] = {{y, ny}, {u, T * r * 4}, {ws, moe_adapter_workspace_size(shape)}};
+  const Span read[] = {{A, nA}, {B, nB}, {scale, (size_t)a.n * 4}, {map != nullptr ? nullptr : adapter_of, T * 4},
+                       {map, moe_adapter_map_size(shape)}, {rng, 16}};
+  if (any_overlap(written, read)) return MOE_ERR_INVALID_ARG;
+  for (int i = 1; i < 3; ++i)
+    if (overlap(written[i].p, written[i].n, x, nx) || overlap(written[i].p, written[i].n, base, ny))
+      return MOE_ERR_INVALID_ARG;
+  a.x = x; a.A = A; a.B = B; a.scale = scale; a.adapter_of = adapter_of; a.map = static_cast<const int32_t *>(map);
+  a.rng = a.threshold != 0 ? rng : nullptr; a.base = base; a.y = y; a.u = u;
+  return cuda_status(launch_adapter(a, (cudaStream_t)stream));
+}
+
+moe_status_t moe_adapter_bwd(const moe_adapter_shape_t *shape, int32_t dx_dtype, const void *dy,
+                             const void *x, const void *A, const void *B, const float *scale,
+                             const void *map, const uint64_t *rng, const float *u,
+                             const void *dx_in, void *dx, float *dA, float *dB, void *ws,
+                             moe_stream_t stream) {
+  NvtxRange trace("moe_adapter_bwd");
+  const moe_status_t st = adapter_check(shape);
+  if (st != MOE_OK) return st;
+  if (!dtype_ok(dx_dtype) || (shape->dtype == MOE_F32 && dx_dtype != MOE_F32)) return MOE_ERR_INVALID_ARG;
+  AdapterArgs a = adapter_args(shape, ws);
+  if ((dA == nullptr) != (dB == nullptr) || !aligned16(dA) || !aligned16(dB) || (dx == nullptr && dA == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  const size_t b = size_of(a.dtype), T = (size_t)a.T, r = (size_t)a.rank;
+  const size_t gA = (size_t)a.n * r * a.d_in * 4, gB = (size_t)a.n * r * a.d_out * 4;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (a.T == 0) {
+    if (dA == nullptr) return MOE_OK;
+    if (overlap(dA, gA, dB, gB)) return MOE_ERR_INVALID_ARG;
+    cudaError_t e = cudaMemsetAsync(dA, 0, gA, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dB, 0, gB, s);
+    return cuda_status(e);
+  }
+  if (!dy || !x || !A || !B || !ws || (dA != nullptr && !u) || (a.threshold != 0 && !rng)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(A) || !aligned16(B) || !aligned4(scale) || !aligned16(map) ||
+      !aligned8(rng) || !aligned16(u) || !aligned16(dx_in) || !aligned16(dx) || !aligned16(ws))
+    return MOE_ERR_INVALID_ARG;
+  const size_t nx = (T - 1) * a.ld_in * b + a.d_in * b, ny = (T - 1) * a.ld_out * b + a.d_out * b;
+  const size_t ndx = T * a.d_in * size_of(dx_dtype);
+  const Span written[] = {{dx, ndx}, {dA, gA}, {dB, gB}, {ws, moe_adapter_workspace_size(shape)}};
+  const Span read[] = {{dy, ny}, {x, nx}, {A, (size_t)a.n * r * a.d_in * b}, {B, (size_t)a.n * r * a.d_out * b},
+                       {scale, (size_t)a.n * 4}, {map, moe_adapter_map_size(shape)}, {rng, 16}, {u, T * r * 4},
+                       {dx_in == dx ? nullptr : dx_in, ndx}};
+  if (any_overlap(written, read)) return MOE_ERR_INVALID_ARG;
+  a.dx_dtype = dx_dtype; a.dy = dy; a.x = x; a.A = A; a.B = B; a.scale = scale;
+  a.map = static_cast<const int32_t *>(map); a.rng = a.threshold != 0 ? rng : nullptr; a.u_in = u;
+  a.dx_in = dx_in; a.dx = dx; a.dA = dA; a.dB = dB;
+  return cuda_status(launch_adapter_bwd(a, s));
 }
 
 }  // extern "C"

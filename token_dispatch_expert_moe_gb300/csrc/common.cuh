@@ -30,7 +30,10 @@ enum : uint32_t {
   kInfoExpertRange = 0x200,   // an expert index outside [0, E)
   kInfoOffsets = 0x300,       // offsets not monotone or beyond max_rows
   kInfoPadOverflow = 0x400,   // padded layout: more kept rows for an expert than its capacity
+  kInfoAdapterRange = 0x500,  // an adapter index outside [-1, n)
+  kInfoAdapterMap = 0x600,    // a map of another T or n, or not one of moe_adapter_map's
   kInfoGemmTimeout = 0x1000,  // + role: a GEMM pipeline wait gave up
+  kInfoAdapterTimeout = 0x2000,  // + role: a wait of the adapters' kernels gave up
 };
 
 // ---------------------------------------------------------------------------
@@ -306,5 +309,40 @@ cudaError_t launch_grad_norm(int n, const moe_tensor_t *grads, float *norm, doub
                              cudaStream_t s);
 cudaError_t launch_grad_clip(int n, const moe_tensor_t *grads, const moe_tensor_t *out,
                              const float *norm, float max_norm, float *coef, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Dropout and adapters (dropout.cu, adapter.cu, adapter_tc.cu).
+
+struct DropoutArgs {
+  int64_t n;
+  int in_dtype, out_dtype;
+  uint32_t threshold;   // drop_threshold(p)
+  const void *x, *residual;
+  const uint64_t *rng;
+  void *out;
+};
+cudaError_t launch_dropout(const DropoutArgs &a, cudaStream_t s);
+
+struct AdapterArgs {
+  int64_t T;
+  int d_in, d_out, n, rank, dtype, dx_dtype;
+  int64_t ld_in, ld_out;
+  uint32_t threshold;          // of the dropout on the input, 0: none
+  const void *x, *A, *B, *base, *dy, *dx_in;
+  const float *scale, *u_in;   // u_in: the backward's u
+  const int32_t *adapter_of, *map;
+  const uint64_t *rng;
+  void *y, *dx;
+  float *u, *dA, *dB;
+  char *ws;                    // behind the status word, adapter_scratch_bytes
+  uint32_t *status;
+};
+size_t adapter_scratch_bytes(int64_t T, int d_in, int d_out, int rank);
+size_t adapter_map_bytes(int64_t T, int n);
+bool adapter_rowwise(int64_t T, int d_in, int d_out, int n, int rank);
+cudaError_t launch_adapter_map(int64_t T, int n, const int32_t *adapter_of, int32_t *map,
+                               uint32_t *status, cudaStream_t s);
+cudaError_t launch_adapter(const AdapterArgs &a, cudaStream_t s);
+cudaError_t launch_adapter_bwd(const AdapterArgs &a, cudaStream_t s);
 
 }  // namespace moe
