@@ -23,7 +23,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + INCLUDE, "-I" + CSRC]
 SOURCES = ["api.cu", "route.cu", "route_bwd.cu", "dispatch.cu", "gemm_simt.cu", "gemm_tc.cu",
-           "norm.cu", "balance.cu", "grads.cu", "dropout.cu", "adapter.cu"]
+           "norm.cu", "balance.cu", "grads.cu", "dropout.cu", "adapter.cu",
+           "adapter_tc.cu"]
 
 
 def nvcc() -> str:

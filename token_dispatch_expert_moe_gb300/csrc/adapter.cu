@@ -30,37 +30,11 @@ constexpr int kMapThreads = 1024;
 constexpr int kMapCtas = 8;
 constexpr size_t kMapSmem = 220 * 1024;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t remote_addr(const void *p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-               : "=r"(r)
-               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ int remote_int(const void *p, uint32_t rank) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote_addr(p, rank)) : "memory");
-  return v;
-}
-__device__ __forceinline__ float remote_float(const void *p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote_addr(p, rank)) : "memory");
-  return v;
-}
-
 // largest e with first[e] <= i
 __device__ __forceinline__ int find_bin(const int *first, int bins, int i) {
   int lo = 0, hi = bins - 1;
@@ -681,11 +655,11 @@ cudaError_t launch_adapter(const AdapterArgs &a, cudaStream_t s) {
     if (a.dtype == MOE_F32) return launch_pdl_clusters(row_kernel<float>, grid, dim3(kRowThreads), kRowCtas, 0, s, a, keep);
     return launch_pdl_clusters(row_kernel<__nv_bfloat16>, grid, dim3(kRowThreads), kRowCtas, 0, s, a, keep);
   }
-  return a.dtype == MOE_F32 ? forward<float>(a, s) : forward<__nv_bfloat16>(a, s);
+  return a.dtype == MOE_F32 ? forward<float>(a, s) : launch_adapter_tc(a, s);
 }
 
 cudaError_t launch_adapter_bwd(const AdapterArgs &a, cudaStream_t s) {
-  return a.dtype == MOE_F32 ? backward<float>(a, s) : backward<__nv_bfloat16>(a, s);
+  return a.dtype == MOE_F32 ? backward<float>(a, s) : launch_adapter_bwd_tc(a, s);
 }
 
 }  // namespace moe

@@ -3,6 +3,7 @@
 #pragma once
 #include "launch.cuh"
 #include "philox.cuh"
+#include "tc.cuh"
 
 namespace moe {
 
@@ -113,6 +114,18 @@ struct Plan {
   }
 };
 
+// a word of another CTA's shared memory
+__device__ __forceinline__ int remote_int(const void *p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_to_cta(smem_u32(p), rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float remote_float(const void *p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_cta(smem_u32(p), rank)) : "memory");
+  return v;
+}
+
 inline Plan plan_of(const AdapterArgs &a) { return Plan{a.map, a.T, a.n, a.status}; }
 inline int64_t host_tiles(const AdapterArgs &a) {
   return a.map != nullptr ? map_layout(a.T, a.n).max_tiles : (a.T + kTileRows - 1) / kTileRows;
@@ -138,6 +151,10 @@ __host__ inline Scratch scratch_of(int64_t T, int d_in, int d_out, int rank) {
   s.bytes = s.dB + up(slots * rank * (size_t)d_out * 4);
   return s;
 }
+
+// bf16 on the tensor cores (adapter_tc.cu)
+cudaError_t launch_adapter_tc(const AdapterArgs &a, cudaStream_t s);
+cudaError_t launch_adapter_bwd_tc(const AdapterArgs &a, cudaStream_t s);
 
 // The second pass of the weight gradients (adapter.cu).
 cudaError_t launch_adapter_join(const AdapterArgs &a, cudaStream_t s);
