@@ -134,6 +134,12 @@ inline int64_t host_chunks(const AdapterArgs &a) {
   return a.map != nullptr ? map_layout(a.T, a.n).max_chunks : (a.T + chunk_rows(a.T) - 1) / chunk_rows(a.T);
 }
 
+// Columns of one part of u: whole steps of K = 16, and, where three parts are
+// wider than one product (256 columns), a second product's at whole 64 columns.
+__host__ __device__ constexpr int padded_rank(int rank) {
+  return rank <= 80 ? (rank + 15) / 16 * 16 : (rank + 31) / 32 * 32;
+}
+
 // Scratch: u and du by position, then the chunks' partial sums.
 struct Scratch {
   size_t u, du, dA, dB, bytes;
@@ -141,8 +147,8 @@ struct Scratch {
 __host__ inline Scratch scratch_of(int64_t T, int d_in, int d_out, int rank) {
   auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
   Scratch s;
-  // fp32 [T, rank], or bf16 [T, 2 rank rounded up to 16]: the two parts of u
-  const size_t each = up((size_t)T * ((rank + 15) / 16 * 16) * 4);
+  // fp32 [T, rank], or bf16 [T, 3 padded_rank]: the three parts of u
+  const size_t each = up((size_t)T * padded_rank(rank) * 6);
   const size_t slots = T > chunk_rows(T) ? kMaxSlots : 0;
   s.u = 0;
   s.du = each;

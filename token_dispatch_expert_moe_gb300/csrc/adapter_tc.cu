@@ -1,38 +1,36 @@
-// The bf16 adapters' tiles on the tensor cores (tcgen05, accumulators in TMEM).
+// The bf16 adapters' tiles on the tensor cores (tcgen05, TMA, accumulators in
+// TMEM).
 //
 // Three products over a batch grouped by adapter, each bound by the memory
-// traffic of its token rows (2 rank flops a byte, 4 with the parts):
+// traffic of its token rows (rank flops a byte, two or three times that with
+// the parts):
 //   shrink  v = x W^T       128 tokens of one adapter x rank, K = the width
-//   expand  out += v V^T    128 tokens x 128 columns, K = 2 rank
-//   wgrad   G = x^T v       128 columns x 2 rank, K = a chunk's tokens
+//   expand  out += v V^T    128 tokens x 128 columns, K = 2 or 3 rank
+//   wgrad   G = x^T v       128 columns x 3 rank, K = a chunk's tokens
 // x, W and V are bf16 as they are. v (u or du) is an fp32 sum; it goes into the
-// second products as two bf16 parts, hi = bf16(v) and lo = bf16(v - hi), side by
-// side along K (expand) or N (wgrad): 2^-16 of v is left out where one part
-// alone would leave 2^-8, and the products stay below the memory time.
+// second products as three bf16 parts that add up to it within 2^-24, p0 =
+// bf16(v), p1 = bf16(v - p0), p2 = bf16(v - p0 - p1), side by side along K
+// (expand) or N (wgrad). A bf16 result of expand takes the first two (2^-16 of
+// the product next to 2^-8 of the result). The products stay below the memory
+// time (rank 128: 1536 of 2700 clocks a 128 x 128 block).
 //
-// Rows are gathered (a tile's tokens lie anywhere in the batch), so the loader
-// threads copy 16 bytes at a time with cp.async into the 128-byte-swizzled
-// layout that the products read; the same thread takes dropped elements out of
-// what it copied itself, before it passes the stage on.
+// Rows of one tile may lie anywhere in the batch. Where they follow one another
+// (packed requests, one adapter) a TMA box fetches them at once, elsewhere
+// tile::gather4 four rows at a time; rows past the tile's end are row -1, which
+// the copy fills with zeros.
 #include "adapter.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kLoaders = 128;             // threads that copy, and then read the accumulator
-constexpr int kPipeThreads = kLoaders + 32;   // and a warp that issues the products
-constexpr int kMaxStages = 5;
+constexpr int kMaxRing = 12;
+constexpr int kCols = 128;   // columns of a block of expand and wgrad
 
 // Roles in kInfoAdapterTimeout + role
-enum { kRoleEmpty = 1, kRoleFull = 2, kRoleDone = 3, kRoleExpand = 4 };
-
-struct Shared {
-  uint64_t full[kMaxStages], empty[kMaxStages], done;
-  uint32_t tmem;
-  volatile int abort;
-};
+enum { kRoleEmpty = 1, kRoleFull = 2, kRoleReady = 3, kRoleDone = 4, kRoleSlab = 5, kRoleAcc = 6 };
 
 __device__ __forceinline__ bool wait(volatile int *abort, uint64_t *bar, uint32_t parity, uint32_t *status,
                                      uint32_t role) {
@@ -51,27 +49,39 @@ __device__ __forceinline__ bool wait(volatile int *abort, uint64_t *bar, uint32_
     }
   }
 }
-
-// 16 bytes from global memory, or zeros
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
-  const int n = in ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// before a CTA ends: copies that have started must land, whatever else gave up
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(smem_u32(bar), parity) && globaltimer() - t0 < kTimeoutNs) {
+  }
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm, uint64_t *bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+// four rows of a map whose box is one row high, one after another
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *tm, uint64_t *bar, int c0, const int (&r)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+      : "memory");
 }
 
 // byte of 16-byte chunk c of row r in rows of 128 swizzled bytes
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-template <int COLS> __device__ __forceinline__ void tmem_alloc(uint32_t *at) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(at)), "r"(COLS)
+__device__ __forceinline__ void tmem_alloc(uint32_t *at, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(at)), "r"(cols)
                : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
-template <int COLS> __device__ __forceinline__ void tmem_free(uint32_t at) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(COLS) : "memory");
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
@@ -87,11 +97,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Eight elements (16 bytes of bf16), zeros in the dropped ones' place. Two
-// elements a word at once: the low 15 bits of both halves against the
-// threshold's by one addition (a carry into bit 15 or 31 says >=), the top bits
-// by the majority with the threshold's, the resulting bits spread over their
-// halves.
+// Eight bf16 elements, zeros in the dropped ones' place. Two elements a word at
+// once: the low 15 bits of both halves against the threshold's by one addition
+// (a carry into bit 15 or 31 says >=), the top bits by the majority with the
+// threshold's, the resulting bits spread over their halves.
 struct Mask {
   Philox g;
   uint32_t add, maj;
@@ -112,119 +121,87 @@ struct Mask {
   }
 };
 
-// hi and lo parts of eight values
-__device__ __forceinline__ void split8(const float (&v)[8], uint4 &hi, uint4 &lo) {
-  uint32_t h[4], l[4];
+// the three parts of eight values, written rp columns apart
+__device__ __forceinline__ void store_parts(bf16 *dst, int rp, float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    const float2 f = __bfloat1622float2(a);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i] - f.x, v[2 * i + 1] - f.y);
-    h[i] = *reinterpret_cast<const uint32_t *>(&a);
-    l[i] = *reinterpret_cast<const uint32_t *>(&b);
-  }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
-__device__ __forceinline__ void setup(Shared &st, int stages) {
-  if (threadIdx.x == 0) {
-    st.abort = 0;
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(smem_u32(&st.full[s]), kLoaders);
-      mbar_init(smem_u32(&st.empty[s]), 1);
+  for (int k = 0; k < 3; ++k) {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      const float2 f = __bfloat1622float2(a);
+      v[2 * i] -= f.x;
+      v[2 * i + 1] -= f.y;
+      h[i] = *reinterpret_cast<const uint32_t *>(&a);
     }
-    mbar_init(smem_u32(&st.done), 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    fence_proxy_async();
+    *reinterpret_cast<uint4 *>(dst + k * rp) = make_uint4(h[0], h[1], h[2], h[3]);
   }
 }
 
-// The loaders' loop over `steps` stages: copy(step, stage) starts a step's
-// copies, own(step, stage) takes out what is dropped from this thread's copies
-// once they have landed. A step is passed on NST - 2 steps after its copies
-// started, so that many stages are in flight.
-template <int NST, typename Copy, typename Own>
-__device__ __forceinline__ bool load_loop(Shared &st, int steps, uint32_t *status, Copy copy, Own own) {
-  constexpr int LAG = NST - 2;
-  bool ok = true;
-  for (int i = 0; i < steps + LAG; ++i) {
-    if (i < steps) {
-      if (i >= NST && !wait(&st.abort, &st.empty[i % NST], (uint32_t)((i / NST - 1) & 1), status, kRoleEmpty)) {
-        ok = false;
-        break;
-      }
-      copy(i, i % NST);
-    }
-    copies_commit();
-    const int j = i - LAG;
-    if (j >= 0) {
-      copies_wait<LAG>();
-      own(j, j % NST);
-      fence_proxy_async();
-      mbar_arrive(smem_u32(&st.full[j % NST]));
-    }
-  }
-  copies_wait<0>();
-  return ok;
-}
-
-// The issuing warp's loop: mma(step, stage) by one lane for every stage passed on.
-template <int NST, typename Mma>
-__device__ __forceinline__ void mma_loop(Shared &st, int steps, int lane, uint32_t *status, Mma mma) {
-  for (int i = 0; i < steps; ++i) {
-    if (!__all_sync(0xffffffffu, wait(&st.abort, &st.full[i % NST], (uint32_t)((i / NST) & 1), status, kRoleFull))) break;
-    tc_fence_after();
-    if (lane == 0) {
-      mma(i, i % NST);
-      tc_commit(smem_u32(&st.empty[i % NST]));
-    }
-    __syncwarp();
-  }
-  if (lane == 0) {   // after every product issued so far
-    if (steps > 0) tc_commit(smem_u32(&st.done));
-    else mbar_arrive(smem_u32(&st.done));
-  }
-  __syncwarp();
+// Positions first .. first + 4 of a lane as tokens, -1 from `rows` on
+__device__ __forceinline__ void lane_tokens(const Plan &plan, int start, int first, int rows, int (&t)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = first + i < rows ? (int)plan.token(start + first + i) : -1;
 }
 
 // ---------------------------------------------------------------------------
 // Shrink. A cluster of `split` CTAs takes a tile; each runs through a part of
 // the width, the fp32 sums meet in shared memory and every CTA finishes a part
-// of the rows, adding in the CTAs' order.
+// of the rows, adding in the CTAs' order. Warp 0 fetches, warp 1 issues the
+// products, the others take the accumulators, and before that, with dropout,
+// the dropped elements out of each stage.
+// The steps of K take turns over several accumulators, which are added at the
+// end: the tensor core truncates each addition, and a short chain loses less.
 struct ShrinkTc {
+  CUtensorMap mx, mx_row, mw;   // x in boxes of 128 rows and of one; W [n, rank, d] or [n, d, rank]
   Plan plan;
-  const bf16 *x, *W;    // W_a [rank, d], or [d, rank] (WT)
-  int64_t ld;
-  int d, rank, rp;      // rp: rank rounded up to 16
-  int split, per;       // CTAs a tile, 64-column steps a CTA
+  int d, rank, rp;              // rp: padded_rank
+  int split, per;               // CTAs a tile, 64-column steps a CTA
   uint32_t threshold;
   const uint64_t *rng;
-  const float *scale;   // per adapter, or NULL
+  const float *scale;           // per adapter, or NULL
   float factor;
-  bf16 *parts;          // [T, 2 rp] by position: hi | lo
-  float *by_token;      // [T, rank], or NULL; 0 without an adapter
-  const float *u_in;    // [T, rank] by token, or NULL: parts_in gets its parts
+  bf16 *parts;                  // [T, 3 rp] by position
+  float *by_token;              // [T, rank], or NULL; 0 without an adapter
+  const float *u_in;            // [T, rank] by token, or NULL: parts_in gets its parts
   bf16 *parts_in;
 };
 
 template <int RPMAX, bool WT> struct ShrinkSize {
   static constexpr int kW = WT ? 8192 * ((RPMAX + 63) / 64) : RPMAX * 128;
   static constexpr int kStage = 16384 + kW;
-  static constexpr int kStages = RPMAX <= 32 ? 5 : RPMAX <= 64 ? 4 : 3;
+  static constexpr int kStages = (100 * 1024) / kStage;   // two CTAs an SM
+  static constexpr int kAcc = RPMAX <= 64 ? 4 : 2;
+  static constexpr int kTmem = kAcc * RPMAX;
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
 };
 
-template <int RPMAX, bool WT>
-__global__ void __launch_bounds__(kPipeThreads) shrink_tc_kernel(const ShrinkTc p) {
+struct Shared {
+  uint64_t full[kMaxRing], ready[kMaxRing], empty[kMaxRing], done;
+  uint32_t tmem;
+  volatile int abort;
+  int tok[kTileRows];
+};
+
+template <int RPMAX, bool WT, bool DROP>
+__global__ void __launch_bounds__(DROP ? 320 : 192) shrink_tc_kernel(const __grid_constant__ ShrinkTc p) {
   using Z = ShrinkSize<RPMAX, WT>;
-  constexpr int NST = Z::kStages, COLS = RPMAX;   // 32, 64 or 128 columns of TMEM
+  constexpr int NST = Z::kStages, WORK = DROP ? 256 : 128, THREADS = WORK + 64;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ Shared st;
-  __shared__ int64_t tok[kTileRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  setup(st, NST);
+  if (tid == 0) {
+    st.abort = 0;
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(smem_u32(&st.full[s]), 1);
+      mbar_init(smem_u32(&st.ready[s]), WORK / 32);
+      mbar_init(smem_u32(&st.empty[s]), 1);
+    }
+    mbar_init(smem_u32(&st.done), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async();
+  }
   pdl_wait();
   const int64_t ti = blockIdx.x / p.split;
   const int q = (int)(blockIdx.x % p.split);   // the CTA's rank in its cluster
@@ -232,112 +209,132 @@ __global__ void __launch_bounds__(kPipeThreads) shrink_tc_kernel(const ShrinkTc 
   const int4 tile = on ? p.plan.tile(ti) : make_int4(-1, 0, 0, 0);
   if (tile.x < 0) {   // the whole cluster
     if (p.by_token != nullptr && q == 0)
-      for (int i = tid; i < tile.z * p.rank; i += kPipeThreads)
+      for (int i = tid; i < tile.z * p.rank; i += THREADS)
         p.by_token[p.plan.token(tile.y + i / p.rank) * p.rank + i % p.rank] = 0.0f;
     return;
   }
-  if (tid < kTileRows) tok[tid] = tid < tile.z ? p.plan.token(tile.y + tid) : -1;
-  if (warp == 4) tmem_alloc<COLS>(&st.tmem);
+  if (tid < kTileRows) st.tok[tid] = tid < tile.z ? (int)p.plan.token(tile.y + tid) : -1;
+  if (warp == 1) tmem_alloc(&st.tmem, Z::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = st.tmem;
   const int k0 = q * p.per, all = (p.d + 63) / 64, steps = max(0, min(p.per, all - k0));
-  const bf16 *W = p.W + (int64_t)tile.x * p.rank * p.d;
 
-  if (warp < 4) {
-    const int c = tid & 7, r0 = tid >> 3;   // this thread's chunk and first row of 16 apart
-    int64_t at[8];
+  if (warp == 0) {
+    const int row0 = st.tok[0];
+    // ascending inside an adapter, so the ends tell
+    const bool run = tile.z > 0 && st.tok[tile.z - 1] - row0 == tile.z - 1;
+    int t[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) at[i] = tok[r0 + 16 * i];
-    const Mask mask(p.rng, p.threshold);
-    const bool drops = p.threshold != 0;
-    auto copy = [&](int step, int s) {
-      const int k = (k0 + step) * 64 + c * 8;
+    for (int i = 0; i < 4; ++i) t[i] = st.tok[4 * lane + i];
+    const uint32_t bytes = 16384 + (WT ? 8192 * ((p.rp + 63) / 64) : p.rp * 128);
+    int i = 0;
+    for (; i < steps; ++i) {
+      const int s = i % NST;
+      bool ok = true;
+      if (i >= NST) ok = wait(&st.abort, &st.empty[s], (uint32_t)((i / NST - 1) & 1), p.plan.status, kRoleEmpty);
+      if (!__all_sync(0xffffffffu, ok)) break;
       const uint32_t xs = smem_u32(smem + s * Z::kStage), ws = xs + 16384;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool in = at[i] >= 0 && k < p.d;
-        copy16(xs + swz(r0 + 16 * i, c), in ? p.x + at[i] * p.ld + k : p.x, in);
-      }
-      if constexpr (!WT) {
-        for (int j = r0; j < p.rp; j += 16) {
-          const bool in = j < p.rank && k < p.d;
-          copy16(ws + swz(j, c), in ? W + (int64_t)j * p.d + k : W, in);
-        }
-      } else {
-        // rows of the width, rank in chunks of 64
-        const int chunks = p.rp / 8;
-        for (int i = tid; i < 64 * chunks; i += kLoaders) {
-          const int kr = i / chunks, jc = i % chunks, kk = (k0 + step) * 64 + kr;
-          const bool in = jc * 8 < p.rank && kk < p.d;
-          copy16(ws + (jc >> 3) * 8192 + swz(kr, jc & 7), in ? W + (int64_t)kk * p.rank + jc * 8 : W, in);
+      const int k = (k0 + i) * 64;
+      if (lane == 0) {
+        mbar_expect_tx(smem_u32(&st.full[s]), bytes);
+        if (run) tma_load_2d(xs, &p.mx, smem_u32(&st.full[s]), k, row0);
+        if constexpr (WT) {
+          for (int b = 0; b * 64 < p.rp; ++b) tma_load_3d(ws + b * 8192, &p.mw, &st.full[s], b * 64, k, tile.x);
+        } else {
+          tma_load_3d(ws, &p.mw, &st.full[s], k, 0, tile.x);
         }
       }
-    };
-    auto own = [&](int step, int s) {
-      if (!drops) return;
-      const int k = (k0 + step) * 64 + c * 8;
-      if (k >= p.d) return;
-      uint8_t *xs = smem + s * Z::kStage;
-#pragma unroll 2
-      for (int i = 0; i < 8; ++i) {
-        if (at[i] < 0) continue;
-        uint4 *v = reinterpret_cast<uint4 *>(xs + swz(r0 + 16 * i, c));
-        uint4 w = *v;
-        mask.apply((uint64_t)(at[i] * p.d + k) >> 3, w);
-        *v = w;
-      }
-    };
-    load_loop<NST>(st, steps, p.plan.status, copy, own);
-  } else {
+      __syncwarp();
+      if (!run) tma_gather4(xs + lane * 512, &p.mx_row, &st.full[s], k, t);
+    }
+    if (lane == 0)
+      for (int s = 0; s < NST && s < i; ++s) drain(&st.full[s], (uint32_t)(((i - 1 - s) / NST) & 1));
+    __syncwarp();
+  } else if (warp == 1) {
     const uint32_t idesc = instr_desc(128, p.rp, 0, WT ? 1 : 0);
-    mma_loop<NST>(st, steps, lane, p.plan.status, [&](int step, int s) {
-      const uint32_t xs = smem_u32(smem + s * Z::kStage), ws = xs + 16384;
+    for (int i = 0; i < steps; ++i) {
+      const int s = i % NST;
+      if (!__all_sync(0xffffffffu, wait(&st.abort, DROP ? &st.ready[s] : &st.full[s], (uint32_t)((i / NST) & 1),
+                                        p.plan.status, kRoleFull)))
+        break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t xs = smem_u32(smem + s * Z::kStage), ws = xs + 16384;
+        const uint32_t acc = tmem + (uint32_t)(i % Z::kAcc) * RPMAX;
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const uint64_t ad = smem_desc(xs + ks * 32, 16, 1024);
-        const uint64_t bd = WT ? smem_desc(ws + ks * 2048, 8192, 1024) : smem_desc(ws + ks * 32, 16, 1024);
-        tc_mma(tmem, ad, bd, idesc, (step > 0 || ks > 0) ? 1u : 0u);
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint64_t ad = smem_desc(xs + ks * 32, 16, 1024);
+          const uint64_t bd = WT ? smem_desc(ws + ks * 2048, 8192, 1024) : smem_desc(ws + ks * 32, 16, 1024);
+          tc_mma(acc, ad, bd, idesc, (i >= Z::kAcc || ks > 0) ? 1u : 0u);
+        }
+        tc_commit(smem_u32(&st.empty[s]));
       }
-    });
+      __syncwarp();
+    }
+    if (lane == 0) {   // after every product issued so far
+      if (steps > 0) tc_commit(smem_u32(&st.done));
+      else mbar_arrive(smem_u32(&st.done));
+    }
+    __syncwarp();
+  } else if constexpr (DROP) {
+    const int id = tid - 64, c = id & 7, r0 = id >> 3;
+    const Mask mask(p.rng, p.threshold);
+    for (int i = 0; i < steps; ++i) {
+      const int s = i % NST, k = (k0 + i) * 64 + c * 8;
+      if (!__all_sync(0xffffffffu, wait(&st.abort, &st.full[s], (uint32_t)((i / NST) & 1), p.plan.status, kRoleReady)))
+        break;
+      uint8_t *xs = smem + s * Z::kStage;
+      if (k < p.d)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int64_t t = st.tok[r0 + 32 * h];
+          uint4 *at = reinterpret_cast<uint4 *>(xs + swz(r0 + 32 * h, c));
+          uint4 w = *at;
+          mask.apply((uint64_t)(t * p.d + k) >> 3, w);   // rows past the end count for nothing
+          *at = w;
+        }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&st.ready[s]));
+    }
   }
-  // every product has ended: the ring is free, the accumulator whole
-  wait(&st.abort, &st.done, 0, p.plan.status, kRoleDone);
+  // every product has ended: the ring is free, the accumulators whole
+  if (!wait(&st.abort, &st.done, 0, p.plan.status, kRoleDone)) st.abort = 1;
   tc_fence_after();
   __syncthreads();
   const bool good = st.abort == 0;
   const int ls = p.rp + 4;   // floats from row to row of the sums
   float *sums = reinterpret_cast<float *>(smem);
-  if (warp < 4) {
+  if (warp >= 2 && warp < 6 && good) {
+    const int quarter = warp & 3, row = quarter * 32 + lane, accs = min(steps, Z::kAcc);
     for (int j = 0; j < p.rp; j += 16) {
-      float v[16];
-      if (steps > 0 && good) {
-        tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + j, v);
-      } else {
+      float v[16] = {};
+      for (int a = 0; a < accs; ++a) {
+        float w[16];
+        tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + a * RPMAX + j, w);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+        for (int i = 0; i < 16; ++i) v[i] += w[i];
       }
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<float4 *>(sums + tid * ls + j + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        *reinterpret_cast<float4 *>(sums + row * ls + j + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     }
   }
   tc_fence_before();
   if (p.split > 1) cluster_sync();
   else __syncthreads();
   tc_fence_after();
-  if (warp == 4) tmem_free<COLS>(tmem);
+  if (warp == 1) tmem_free(tmem, Z::kTmem);
   // rows of this CTA, eight values a thread at a time
   const int rows = kTileRows / p.split, g8 = p.rp / 8;
   const float f = p.factor * (p.scale != nullptr ? p.scale[tile.x] : 1.0f);
   if (good)
-    for (int i = tid; i < rows * g8; i += kPipeThreads) {
+    for (int i = tid; i < rows * g8; i += THREADS) {
       const int row = q * rows + i / g8, j = (i % g8) * 8;
       if (row >= tile.z) break;
-      float v[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = 0.0f;
+      float v[8] = {};
       for (int z = 0; z < p.split; ++z) {
         const uint32_t a = map_to_cta(smem_u32(sums + row * ls + j), (uint32_t)z);
         float w[8];
@@ -353,17 +350,13 @@ __global__ void __launch_bounds__(kPipeThreads) shrink_tc_kernel(const ShrinkTc 
       const bool in = j < p.rank;   // rank is a multiple of 8
 #pragma unroll
       for (int c = 0; c < 8; ++c) v[c] = in ? v[c] * f : 0.0f;
-      uint4 hi, lo;
-      split8(v, hi, lo);
-      bf16 *dst = p.parts + (int64_t)(tile.y + row) * 2 * p.rp + j;
-      *reinterpret_cast<uint4 *>(dst) = hi;
-      *reinterpret_cast<uint4 *>(dst + p.rp) = lo;
-      const int64_t t = tok[row];
+      const int64_t t = st.tok[row], pos = (int64_t)(tile.y + row) * 3 * p.rp + j;
       if (p.by_token != nullptr && in) {
         float4 *o = reinterpret_cast<float4 *>(p.by_token + t * p.rank + j);
         o[0] = make_float4(v[0], v[1], v[2], v[3]);
         o[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
+      store_parts(p.parts + pos, p.rp, v);
       if (p.u_in != nullptr) {
         float w[8] = {};
         if (in) {
@@ -371,313 +364,503 @@ __global__ void __launch_bounds__(kPipeThreads) shrink_tc_kernel(const ShrinkTc 
           const float4 a = o[0], b = o[1];
           w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
         }
-        split8(w, hi, lo);
-        dst = p.parts_in + (int64_t)(tile.y + row) * 2 * p.rp + j;
-        *reinterpret_cast<uint4 *>(dst) = hi;
-        *reinterpret_cast<uint4 *>(dst + p.rp) = lo;
+        store_parts(p.parts_in + pos, p.rp, w);
       }
     }
   if (p.split > 1) cluster_sync();   // no CTA leaves while another reads its sums
 }
 
 // ---------------------------------------------------------------------------
-// Expand: a CTA takes 128 columns of a tile.
+// Expand. One CTA an SM runs through items: a tile and up to `span` blocks of
+// 128 columns. Base rows come by TMA into slabs of 128 rows x 128 bytes, the
+// product of a block into one of two accumulators; two sets of four warps take
+// the blocks in turn: a thread adds its row of the accumulator to its row of
+// the slab, and the slab leaves by TMA, or row by row where the tile's rows do
+// not follow one another. Each set has an accumulator and a ring of slabs of its
+// own, so that it sees every phase of the barriers it waits on.
 struct ExpandTc {
+  CUtensorMap mp, mv, mb, mb_row, mo;   // parts, V [n, d, rank] or [n, rank, d], base (128 rows; one), out (32 rows)
   Plan plan;
-  const bf16 *parts, *V;   // V_a [d, rank], or [rank, d] (VT)
   const void *base;
   void *out;
   int64_t ld;
-  int d, rank, rp;
+  int d, rank, rp, nparts, span;
+  int p_bytes, v_bytes, n_p, n_v, n_slab;   // shared memory: parts, V, how many of each, and slabs of a set
   uint32_t threshold;
   const uint64_t *rng;
   const float *scale;
   float factor;
 };
-constexpr int kCols = 128;
+constexpr int kExpandThreads = 64 + 256;
 
-template <int RPMAX, typename TO, bool VT> struct ExpandSize {
-  static constexpr int kParts = 16384 * ((2 * RPMAX + 63) / 64);
-  static constexpr int kV = VT ? RPMAX * 256 : 16384 * ((RPMAX + 63) / 64);
-  static constexpr int kPer = 128 / sizeof(TO);      // columns of a slab: rows of 128 bytes
-  static constexpr int kSlabs = kCols / kPer;
-  static constexpr size_t kSmem = kParts + kV + kSlabs * 16384 + 1024;
+struct ExpandShared {
+  uint64_t pfull[2], pempty[2], vfull[2], vempty[2], sfull[kMaxRing], sempty[kMaxRing], dfull[2], dempty[2];
+  uint32_t tmem;
+  volatile int abort;
 };
 
-template <int RPMAX, typename TO, bool VT>
-__global__ void __launch_bounds__(kLoaders) expand_tc_kernel(const ExpandTc p) {
-  using Z = ExpandSize<RPMAX, TO, VT>;
-  constexpr int VN = 16 / sizeof(TO);   // columns of a chunk
+template <typename TO, bool VT>
+__global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __grid_constant__ ExpandTc p) {
+  constexpr int VN = 16 / sizeof(TO), PER = 128 / sizeof(TO), SLABS = kCols / PER;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *vs = smem + Z::kParts, *slabs = vs + Z::kV;
-  __shared__ Shared st;
-  __shared__ int64_t tok[kTileRows];
+  uint8_t *vs = smem + p.n_p * p.p_bytes, *slabs = vs + p.n_v * p.v_bytes;
+  __shared__ ExpandShared st;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  setup(st, 0);
-  pdl_wait();
-  const int blocks = (p.d + kCols - 1) / kCols;   // the columns of a tile one after another
-  const int64_t ti = blockIdx.x / blocks;
-  if (ti >= p.plan.tiles()) return;
-  const int4 tile = p.plan.tile(ti);
-  const TO *base = static_cast<const TO *>(p.base);
-  TO *out = static_cast<TO *>(p.out);
-  if (tile.z <= 0 || (tile.x < 0 && base == out)) return;
-  tok[tid] = tid < tile.z ? p.plan.token(tile.y + tid) : -1;
-  if (warp == 0 && tile.x >= 0) tmem_alloc<kCols>(&st.tmem);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const int c0 = (int)(blockIdx.x % blocks) * kCols;
-
-  // parts and V, then the base rows: a warp copies what it alone reads and writes
-  if (tile.x >= 0) {
-    const int pc = p.rp / 4;   // chunks of a row of parts
-    const bf16 *parts = p.parts + (int64_t)tile.y * 2 * p.rp;
-    for (int i = tid; i < kTileRows * pc; i += kLoaders) {
-      const int row = i / pc, c = i % pc;
-      const bool in = row < tile.z;
-      copy16(smem_u32(smem) + (c >> 3) * 16384 + swz(row, c & 7), in ? parts + (int64_t)row * 2 * p.rp + c * 8 : parts, in);
+  if (tid == 0) {
+    st.abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&st.pfull[i]), 1);
+      mbar_init(smem_u32(&st.pempty[i]), 1);
+      mbar_init(smem_u32(&st.vfull[i]), 1);
+      mbar_init(smem_u32(&st.vempty[i]), 1);
+      mbar_init(smem_u32(&st.dfull[i]), 1);
+      mbar_init(smem_u32(&st.dempty[i]), 4);
     }
-    const bf16 *V = p.V + (int64_t)tile.x * p.rank * p.d;
-    if constexpr (!VT) {
-      const int vc = p.rp / 8;
-      for (int i = tid; i < kCols * vc; i += kLoaders) {
-        const int col = i / vc, c = i % vc;
-        const bool in = c * 8 < p.rank && c0 + col < p.d;
-        copy16(smem_u32(vs) + (c >> 3) * 16384 + swz(col, c & 7), in ? V + (int64_t)(c0 + col) * p.rank + c * 8 : V, in);
-      }
-    } else {
-      for (int i = tid; i < p.rp * 16; i += kLoaders) {
-        const int j = i >> 4, c = i & 15;
-        const bool in = j < p.rank && c0 + c * 8 < p.d;
-        copy16(smem_u32(vs) + (c >> 3) * (p.rp * 128) + swz(j, c & 7), in ? V + (int64_t)j * p.d + c0 + c * 8 : V, in);
-      }
+    for (int i = 0; i < 2 * p.n_slab; ++i) {
+      mbar_init(smem_u32(&st.sfull[i]), 1);
+      mbar_init(smem_u32(&st.sempty[i]), 4);
     }
-  }
-  copies_commit();
-  const int rq = lane >> 3, ch = lane & 7;   // four rows at once, eight chunks each
-  if (base != nullptr) {
-#pragma unroll
-    for (int s = 0; s < Z::kSlabs; ++s)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = warp * 32 + i * 4 + rq, col = c0 + s * Z::kPer + ch * VN;
-        const int64_t t = tok[row];
-        const bool in = t >= 0 && col < p.d;
-        copy16(smem_u32(slabs) + s * 16384 + swz(row, ch), in ? base + t * p.ld + col : base, in);
-      }
-  }
-  copies_commit();
-  bool good = true;
-  if (tile.x >= 0) {
-    copies_wait<1>();
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async();
-    __syncthreads();
-    if (tid == 0) {
-      const uint32_t idesc = instr_desc(128, kCols, 0, VT ? 1 : 0);
-      const uint32_t as = smem_u32(smem), bs = smem_u32(vs);
-      for (int ks = 0; ks < p.rp / 8; ++ks) {   // 2 rp / 16: hi, then lo, against the same V
-        const int kb = ks < p.rp / 16 ? ks : ks - p.rp / 16;
-        const uint64_t ad = smem_desc(as + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024);
-        const uint64_t bd = VT ? smem_desc(bs + kb * 2048, (uint32_t)p.rp * 128, 1024)
-                               : smem_desc(bs + (kb >> 2) * 16384 + (kb & 3) * 32, 16, 1024);
-        tc_mma(st.tmem, ad, bd, idesc, ks > 0 ? 1u : 0u);
-      }
-      tc_commit(smem_u32(&st.done));
-    }
-    copies_wait<0>();
-    wait(&st.abort, &st.done, 0, p.plan.status, kRoleExpand);
-    tc_fence_after();
-    __syncthreads();
-    good = st.abort == 0;
-  } else {
-    copies_wait<0>();
-    __syncwarp();
   }
-  if (good) {
-    const float f = p.factor * (tile.x >= 0 && p.scale != nullptr ? p.scale[tile.x] : 1.0f);
-    const Philox g(p.rng, p.threshold);
-    const int row = warp * 32 + lane;
-    const int64_t t = tok[row];
-#pragma unroll 1
-    for (int s = 0; s < Z::kSlabs; ++s) {
-      uint8_t *slab = slabs + s * 16384;
-#pragma unroll 1
-      for (int h = 0; h < Z::kPer / 32; ++h) {
-        const int col = c0 + s * Z::kPer + h * 32;
-        float v[32];
-        if (tile.x >= 0) tmem_ld32(st.tmem + ((uint32_t)(warp * 32) << 16) + s * Z::kPer + h * 32, v);
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          if (tile.x >= 0 && p.threshold != 0 && t >= 0 && col + e < p.d) {
-            const uint4 w = g.block((uint64_t)(t * p.d + col + e) >> 3);
-            if (!g.kept<0>(w)) v[e] = 0.0f;
-            if (!g.kept<1>(w)) v[e + 1] = 0.0f;
-            if (!g.kept<2>(w)) v[e + 2] = 0.0f;
-            if (!g.kept<3>(w)) v[e + 3] = 0.0f;
-            if (!g.kept<4>(w)) v[e + 4] = 0.0f;
-            if (!g.kept<5>(w)) v[e + 5] = 0.0f;
-            if (!g.kept<6>(w)) v[e + 6] = 0.0f;
-            if (!g.kept<7>(w)) v[e + 7] = 0.0f;
-          }
-#pragma unroll
-          for (int k = 0; k < 8; k += VN) {
-            TO *at = reinterpret_cast<TO *>(slab + swz(row, (h * 32 + e + k) / VN));
-            float b[VN];
-            if (base != nullptr) {
-              load16<TO>(at, b);
-            } else {
-#pragma unroll
-              for (int i = 0; i < VN; ++i) b[i] = 0.0f;
-            }
-            if (tile.x >= 0)
-#pragma unroll
-              for (int i = 0; i < VN; ++i) b[i] = fmaf(f, v[e + k + i], b[i]);
-            store16<TO>(at, b);
-          }
-        }
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = warp * 32 + i * 4 + rq, col = c0 + s * Z::kPer + ch * VN;
-        const int64_t tr = tok[r];
-        if (tr >= 0 && col < p.d)
-          *reinterpret_cast<uint4 *>(out + tr * p.ld + col) = *reinterpret_cast<const uint4 *>(slab + swz(r, ch));
-      }
-    }
-  }
-  if (tile.x >= 0) {
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 0) tmem_free<kCols>(st.tmem);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Weight gradients: a CTA takes 128 columns of a chunk and runs through its
-// tokens, 64 a step: both operands have the tokens (K) as rows.
-struct WgradTc {
-  Plan plan;
-  const bf16 *z, *parts;   // [.., d] by token, [T, 2 rp] by position
-  int64_t ld;
-  int d, rank, rp;
-  uint32_t threshold;
-  const uint64_t *rng;
-  const float *scale;
-  float factor;
-  float *out, *partial;    // [n, rank, d], or [n, d, rank] (GT); [slots, ..]
-};
-
-template <int RPMAX> struct WgradSize {
-  static constexpr int kStage = 16384 + 8192 * ((2 * RPMAX + 63) / 64);
-  static constexpr int kStages = RPMAX <= 32 ? 4 : RPMAX <= 64 ? 3 : 4;
-  static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
-};
-
-template <int RPMAX, bool GT>
-__global__ void __launch_bounds__(kPipeThreads) wgrad_tc_kernel(const WgradTc p) {
-  using Z = WgradSize<RPMAX>;
-  constexpr int NST = Z::kStages, COLS = 2 * RPMAX;
-  extern __shared__ uint8_t raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  __shared__ Shared st;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  setup(st, NST);
+  if (warp == 1) tmem_alloc(&st.tmem, 256);
   pdl_wait();
-  if (blockIdx.y >= p.plan.chunks()) return;
-  const int4 ch = p.plan.chunk(blockIdx.y);
-  if (ch.z <= 0) return;
-  if (warp == 4) tmem_alloc<COLS>(&st.tmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = st.tmem;
-  const int c0 = blockIdx.x * kCols, steps = (ch.z + 63) / 64;
+  const TO *base = static_cast<const TO *>(p.base);
+  TO *out = static_cast<TO *>(p.out);
+  const int blocks = (p.d + kCols - 1) / kCols, groups = (blocks + p.span - 1) / p.span;
+  const int64_t items = p.plan.tiles() * groups;
+  // The same walk for every role: items of tiles that have something to write.
+  auto item = [&](int64_t it, int4 &tile, int &b0, int &b1) {
+    tile = p.plan.tile(it / groups);
+    b0 = (int)(it % groups) * p.span;
+    b1 = min(blocks, b0 + p.span);
+    return tile.z > 0 && (tile.x >= 0 || base != out);
+  };
 
-  if (warp < 4) {
-    const int c = tid & 15, r0 = tid >> 4;   // chunk of 8 columns, rows 8 apart
-    const bool in_width = c0 + c * 8 < p.d;
-    const bf16 *z = p.z + c0 + c * 8;
-    const Mask mask(p.rng, p.threshold);
-    const bool drops = p.threshold != 0;
-    const int pc = p.rp / 4;
-    int64_t next[8];
-    auto tokens = [&](int step) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = step * 64 + r0 + 8 * i;
-        next[i] = row < ch.z ? p.plan.token(ch.y + row) : -1;
+  if (warp == 0) {
+    // ---- fetch
+    int pi = 0, vi = 0, block = 0, si[2] = {0, 0};   // parts, V, blocks, and each set's slabs so far
+    bool ok = true;
+    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      int4 tile;
+      int b0, b1;
+      if (!item(it, tile, b0, b1)) continue;
+      int t[4];
+      lane_tokens(p.plan, tile.y, 4 * lane, tile.z, t);
+      const int row0 = __shfl_sync(0xffffffffu, t[0], 0);
+      const int last = (int)p.plan.token(tile.y + tile.z - 1);
+      const bool run = last - row0 == tile.z - 1;
+      const bool live = tile.x >= 0;
+      if (live) {
+        const int b = pi % p.n_p;
+        if (pi >= p.n_p) ok = wait(&st.abort, &st.pempty[b], (uint32_t)((pi / p.n_p - 1) & 1), p.plan.status, kRoleEmpty);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (lane == 0) {
+          mbar_expect_tx(smem_u32(&st.pfull[b]), (uint32_t)p.p_bytes);
+          for (int k = 0; k * 16384 < p.p_bytes; ++k)
+            tma_load_2d(smem_u32(smem + b * p.p_bytes + k * 16384), &p.mp, smem_u32(&st.pfull[b]), k * 64, tile.y);
+        }
+        ++pi;
       }
-    };
-    tokens(0);
-    auto copy = [&](int step, int s) {
-      const uint32_t zs = smem_u32(smem + s * Z::kStage), ps = zs + 16384;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool in = next[i] >= 0 && in_width;
-        copy16(zs + (c >> 3) * 8192 + swz(r0 + 8 * i, c & 7), in ? z + next[i] * p.ld : p.z, in);
+      for (int blk = b0; blk < b1; ++blk, ++block) {
+        const int c0 = blk * kCols, set = block & 1;
+        if (live) {
+          const int b = vi % p.n_v;
+          if (vi >= p.n_v) ok = wait(&st.abort, &st.vempty[b], (uint32_t)((vi / p.n_v - 1) & 1), p.plan.status, kRoleEmpty);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (lane == 0) {
+            mbar_expect_tx(smem_u32(&st.vfull[b]), (uint32_t)p.v_bytes);
+            const uint32_t dst = smem_u32(vs + b * p.v_bytes);
+            if constexpr (VT) {
+              for (int k = 0; k < 2; ++k) tma_load_3d(dst + k * (p.v_bytes / 2), &p.mv, &st.vfull[b], c0 + 64 * k, 0, tile.x);
+            } else {
+              for (int k = 0; k * 16384 < p.v_bytes; ++k) tma_load_3d(dst + k * 16384, &p.mv, &st.vfull[b], k * 64, c0, tile.x);
+            }
+          }
+          ++vi;
+        }
+        for (int s = 0; s < SLABS; ++s) {
+          const int n = set ? si[1]++ : si[0]++, b = set * p.n_slab + n % p.n_slab;
+          if (n >= p.n_slab)
+            ok = wait(&st.abort, &st.sempty[b], (uint32_t)((n / p.n_slab - 1) & 1), p.plan.status, kRoleEmpty);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          const int c = c0 + s * PER;
+          if (base == nullptr || c >= p.d) {
+            if (lane == 0) mbar_arrive(smem_u32(&st.sfull[b]));
+          } else {
+            const uint32_t dst = smem_u32(slabs + b * 16384);
+            if (lane == 0) {
+              mbar_expect_tx(smem_u32(&st.sfull[b]), 16384);
+              if (run) tma_load_2d(dst, &p.mb, smem_u32(&st.sfull[b]), c, row0);
+            }
+            __syncwarp();
+            if (!run) tma_gather4(dst + lane * 512, &p.mb_row, &st.sfull[b], c, t);
+          }
+        }
+        if (!ok) break;
       }
-      const bf16 *parts = p.parts + (int64_t)(ch.y + step * 64) * 2 * p.rp;
-      const int rows = min(64, ch.z - step * 64);
-      for (int i = tid; i < 64 * pc; i += kLoaders) {
-        const int row = i / pc, k = i % pc;
-        const bool in = row < rows;
-        copy16(ps + (k >> 3) * 8192 + swz(row, k & 7), in ? parts + (int64_t)row * 2 * p.rp + k * 8 : p.parts, in);
+    }
+    if (lane == 0) {
+      for (int b = 0; b < p.n_p && b < pi; ++b) drain(&st.pfull[b], (uint32_t)(((pi - 1 - b) / p.n_p) & 1));
+      for (int b = 0; b < p.n_v && b < vi; ++b) drain(&st.vfull[b], (uint32_t)(((vi - 1 - b) / p.n_v) & 1));
+      for (int h = 0; h < 2; ++h)   // after a wait that gave up the last slab counted may not have been fetched
+        for (int b = 0, n = (h ? si[1] : si[0]) - (ok ? 0 : 1); b < p.n_slab && b < n; ++b)
+          drain(&st.sfull[h * p.n_slab + b], (uint32_t)(((n - 1 - b) / p.n_slab) & 1));
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- products
+    const uint32_t idesc = instr_desc(128, kCols, 0, VT ? 1 : 0);
+    int pi = 0, vi = 0, block = 0, used[2] = {0, 0}, last = -1;   // used: of each accumulator so far
+    bool ok = true;
+    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      int4 tile;
+      int b0, b1;
+      if (!item(it, tile, b0, b1)) continue;
+      if (tile.x < 0) {
+        block += b1 - b0;
+        continue;
       }
-      if (step + 1 < steps) tokens(step + 1);
-    };
-    auto own = [&](int step, int s) {
-      if (!drops || !in_width) return;
-      uint8_t *zs = smem + s * Z::kStage;
-#pragma unroll 2
-      for (int i = 0; i < 8; ++i) {
-        const int row = step * 64 + r0 + 8 * i;
-        if (row >= ch.z) continue;
-        uint4 *v = reinterpret_cast<uint4 *>(zs + (c >> 3) * 8192 + swz(r0 + 8 * i, c & 7));
-        uint4 w = *v;
-        mask.apply((uint64_t)(p.plan.token(ch.y + row) * p.d + c0 + c * 8) >> 3, w);
-        *v = w;
+      const int pb = pi % p.n_p;
+      ok = wait(&st.abort, &st.pfull[pb], (uint32_t)((pi / p.n_p) & 1), p.plan.status, kRoleFull);
+      for (int blk = b0; blk < b1; ++blk, ++vi, ++block) {
+        const int vb = vi % p.n_v, db = block & 1, n = db ? used[1]++ : used[0]++;
+        if (ok) ok = wait(&st.abort, &st.vfull[vb], (uint32_t)((vi / p.n_v) & 1), p.plan.status, kRoleFull);
+        if (ok && n > 0) ok = wait(&st.abort, &st.dempty[db], (uint32_t)((n - 1) & 1), p.plan.status, kRoleAcc);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t as = smem_u32(smem + pb * p.p_bytes), bs = smem_u32(vs + vb * p.v_bytes);
+          const int per = p.rp / 16;
+          int ks = 0;
+          for (int part = 0; part < p.nparts; ++part)
+            for (int kb = 0; kb < per; ++kb, ++ks) {
+              const uint64_t ad = smem_desc(as + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024);
+              const uint64_t bd = VT ? smem_desc(bs + kb * 2048, (uint32_t)(p.v_bytes / 2), 1024)
+                                     : smem_desc(bs + (kb >> 2) * 16384 + (kb & 3) * 32, 16, 1024);
+              tc_mma(tmem + db * kCols, ad, bd, idesc, ks > 0 ? 1u : 0u);
+            }
+          tc_commit(smem_u32(&st.vempty[vb]));
+          tc_commit(smem_u32(&st.dfull[db]));
+          if (blk + 1 == b1) tc_commit(smem_u32(&st.pempty[pb]));
+        }
+        last = n * 2 + db;
+        __syncwarp();
       }
-    };
-    load_loop<NST>(st, steps, p.plan.status, copy, own);
+      ++pi;
+    }
+    // the last products have ended before TMEM is freed
+    if (last >= 0 && lane == 0) drain(&st.dfull[last & 1], (uint32_t)((last >> 1) & 1));
+    __syncwarp();
   } else {
-    const uint32_t idesc = instr_desc(128, 2 * p.rp, 1, 1);
-    mma_loop<NST>(st, steps, lane, p.plan.status, [&](int step, int s) {
-      const uint32_t zs = smem_u32(smem + s * Z::kStage), ps = zs + 16384;
+    // ---- accumulators onto the base rows
+    const int set = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const int rq = lane >> 3, ch = lane & 7;   // four rows at once, eight chunks each
+    const Philox g(p.rng, p.threshold);
+    int block = 0, used = 0, sn = 0, pending = -1;   // used, sn: this set's accumulator and slabs so far
+    bool ok = true;
+    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      int4 tile;
+      int b0, b1;
+      if (!item(it, tile, b0, b1)) continue;
+      const bool live = tile.x >= 0;
+      const int64_t t = row < tile.z ? p.plan.token(tile.y + row) : -1;
+      const int64_t first = p.plan.token(tile.y);
+      const bool run = p.plan.token(tile.y + tile.z - 1) - first == tile.z - 1;
+      const bool whole = run && quarter * 32 + 32 <= tile.z;   // this warp's 32 rows leave at once
+      const float f = p.factor * (live && p.scale != nullptr ? p.scale[tile.x] : 1.0f);
+      for (int blk = b0; blk < b1; ++blk, ++block) {
+        if ((block & 1) != set) continue;
+        if (live) {
+          ok = __all_sync(0xffffffffu, wait(&st.abort, &st.dfull[set], (uint32_t)(used & 1), p.plan.status, kRoleDone));
+          if (!ok) break;
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int s = 0; s < SLABS; ++s, ++sn) {
+          const int b = set * p.n_slab + sn % p.n_slab, c0 = blk * kCols + s * PER;
+          ok = __all_sync(0xffffffffu, wait(&st.abort, &st.sfull[b], (uint32_t)((sn / p.n_slab) & 1), p.plan.status, kRoleSlab));
+          if (!ok) break;
+          uint8_t *slab = slabs + b * 16384;
+#pragma unroll 1
+          for (int h = 0; h < PER / 32; ++h) {
+            const int col = c0 + h * 32;
+            float v[32];
+            if (live) tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + set * kCols + s * PER + h * 32, v);
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        tc_mma(tmem, smem_desc(zs + ks * 2048, 8192, 1024), smem_desc(ps + ks * 2048, 8192, 1024), idesc,
-               (step > 0 || ks > 0) ? 1u : 0u);
-    });
+            for (int e = 0; e < 32; e += 8) {
+              if (live && p.threshold != 0) {
+                const uint4 w = g.block((uint64_t)(t * p.d + col + e) >> 3);
+                if (!g.kept<0>(w)) v[e] = 0.0f;
+                if (!g.kept<1>(w)) v[e + 1] = 0.0f;
+                if (!g.kept<2>(w)) v[e + 2] = 0.0f;
+                if (!g.kept<3>(w)) v[e + 3] = 0.0f;
+                if (!g.kept<4>(w)) v[e + 4] = 0.0f;
+                if (!g.kept<5>(w)) v[e + 5] = 0.0f;
+                if (!g.kept<6>(w)) v[e + 6] = 0.0f;
+                if (!g.kept<7>(w)) v[e + 7] = 0.0f;
+              }
+#pragma unroll
+              for (int k = 0; k < 8; k += VN) {
+                TO *at = reinterpret_cast<TO *>(slab + swz(row, (h * 32 + e + k) / VN));
+                float o[VN] = {};
+                if (base != nullptr) load16<TO>(at, o);
+                if (live)
+#pragma unroll
+                  for (int i = 0; i < VN; ++i) o[i] = fmaf(f, v[e + k + i], o[i]);
+                store16<TO>(at, o);
+              }
+            }
+          }
+          if (whole && c0 < p.d) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                               reinterpret_cast<uint64_t>(&p.mo)),
+                           "r"(smem_u32(slab) + quarter * 4096), "r"(c0), "r"((int)first + quarter * 32)
+                           : "memory");
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              if (pending >= 0) {   // the slab before this one has been read
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                mbar_arrive(smem_u32(&st.sempty[pending]));
+              }
+            }
+            pending = b;
+          } else {
+            __syncwarp();
+            const int cc = c0 + ch * VN;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = i * 4 + rq;
+              const int64_t tr = __shfl_sync(0xffffffffu, t, r);
+              if (tr >= 0 && cc < p.d)
+                *reinterpret_cast<uint4 *>(out + tr * p.ld + cc) = *reinterpret_cast<const uint4 *>(slab + swz(quarter * 32 + r, ch));
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&st.sempty[b]));
+          }
+        }
+        if (!ok) break;
+        if (live) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&st.dempty[set]));
+          ++used;
+        }
+        if (pending >= 0 && lane == 0) {
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          mbar_arrive(smem_u32(&st.sempty[pending]));
+        }
+        pending = -1;
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
-  wait(&st.abort, &st.done, 0, p.plan.status, kRoleDone);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_free(tmem, 256);
+}
+
+// ---------------------------------------------------------------------------
+// Weight gradients: a CTA takes 128 columns of a chunk and runs through its
+// tokens, 64 a step: both operands have the tokens (K) as rows. The two
+// gradients of a backward are two jobs of one launch, block by block in turn.
+struct WgradJob {
+  CUtensorMap mz, mz_row, mp, mp_row;   // [.., d] by token and parts by position: 64 rows, one row
+  int d, transposed;                    // out [n, d, rank] instead of [n, rank, d]
+  uint32_t threshold;
+  const float *scale;
+  float factor;
+  float *out, *partial;                 // [n, rank d], [slots, rank d]
+};
+struct WgradTc {
+  WgradJob job[2];
+  Plan plan;
+  int rank, rp, blocks[2];
+  const uint64_t *rng;
+};
+
+// ATOMS: 64-column boxes of the parts, three parts of up to ATOMS * 64 / 3 columns
+template <int ATOMS> struct WgradSize {
+  static constexpr int kStage = 16384 + 8192 * ATOMS;
+  static constexpr int kStages = ATOMS == 1 ? 4 : ATOMS == 2 ? 3 : ATOMS == 3 ? 5 : 3;   // two CTAs an SM, or one
+  static constexpr int kAccCols = ATOMS == 1 ? 64 : ATOMS == 2 ? 128 : ATOMS == 3 ? 256 : 512;
+  static constexpr int kAcc = ATOMS == 1 ? 4 : ATOMS <= 3 ? 2 : 1;
+  static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+};
+struct WgradShared {
+  uint64_t full[kMaxRing], ready[kMaxRing], empty[kMaxRing], done;
+  uint32_t tmem;
+  volatile int abort;
+  int tok[kMaxRing][64];
+};
+
+template <int ATOMS, bool DROP>
+__global__ void __launch_bounds__(DROP ? 320 : 192) wgrad_tc_kernel(const __grid_constant__ WgradTc p) {
+  using Z = WgradSize<ATOMS>;
+  constexpr int NST = Z::kStages, WORK = DROP ? 256 : 128;
+  extern __shared__ uint8_t raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  __shared__ WgradShared st;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    st.abort = 0;
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(smem_u32(&st.full[s]), 1);
+      mbar_init(smem_u32(&st.ready[s]), WORK / 32);
+      mbar_init(smem_u32(&st.empty[s]), 1);
+    }
+    mbar_init(smem_u32(&st.done), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async();
+  }
+  pdl_wait();
+  if (blockIdx.y >= p.plan.chunks()) return;
+  const int4 ch = p.plan.chunk(blockIdx.y);
+  if (ch.z <= 0) return;
+  // block by block in turn while both jobs have some
+  const int both = min(p.blocks[0], p.blocks[1]), bx = (int)blockIdx.x;
+  const int j = bx < 2 * both ? bx & 1 : (p.blocks[1] > p.blocks[0] ? 1 : 0);
+  const WgradJob &job = p.job[j];
+  const int c0 = (bx < 2 * both ? bx >> 1 : bx - both) * kCols;
+  const bool drops = DROP && job.threshold != 0;
+  if (warp == 1) tmem_alloc(&st.tmem, Z::kAcc * Z::kAccCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = st.tmem;
+  const int steps = (ch.z + 63) / 64;
+
+  if (warp == 0) {
+    const uint32_t bytes = 16384 + 8192 * ATOMS;
+    int t[4], pos[4];
+    lane_tokens(p.plan, ch.y, 4 * lane, lane < 16 ? ch.z : 0, t);
+    int i = 0;
+    for (; i < steps; ++i) {
+      const int s = i % NST, r0 = i * 64;
+      const bool full = r0 + 64 <= ch.z;
+      const int first = __shfl_sync(0xffffffffu, t[0], 0), last = __shfl_sync(0xffffffffu, t[3], 15);
+      const bool run = full && last - first == 63;
+      bool ok = true;
+      if (i >= NST) ok = wait(&st.abort, &st.empty[s], (uint32_t)((i / NST - 1) & 1), p.plan.status, kRoleEmpty);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (drops && lane < 16)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st.tok[s][4 * lane + k] = t[k];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pos[k] = r0 + 4 * lane + k < ch.z ? ch.y + r0 + 4 * lane + k : -1;
+      __syncwarp();
+      const uint32_t zs = smem_u32(smem + s * Z::kStage), ps = zs + 16384;
+      if (lane == 0) {
+        mbar_expect_tx(smem_u32(&st.full[s]), bytes);
+        if (run) {
+          tma_load_2d(zs, &job.mz, smem_u32(&st.full[s]), c0, first);
+          tma_load_2d(zs + 8192, &job.mz, smem_u32(&st.full[s]), c0 + 64, first);
+        }
+        if (full)
+#pragma unroll
+          for (int b = 0; b < ATOMS; ++b) tma_load_2d(ps + b * 8192, &job.mp, smem_u32(&st.full[s]), b * 64, ch.y + r0);
+      }
+      __syncwarp();
+      if (lane < 16) {
+        if (!run) {
+          tma_gather4(zs + lane * 512, &job.mz_row, &st.full[s], c0, t);
+          tma_gather4(zs + 8192 + lane * 512, &job.mz_row, &st.full[s], c0 + 64, t);
+        }
+        if (!full)
+#pragma unroll
+          for (int b = 0; b < ATOMS; ++b) tma_gather4(ps + b * 8192 + lane * 512, &job.mp_row, &st.full[s], b * 64, pos);
+      }
+      if (i + 1 < steps) lane_tokens(p.plan, ch.y, r0 + 64 + 4 * lane, lane < 16 ? ch.z : 0, t);
+    }
+    if (lane == 0)
+      for (int s = 0; s < NST && s < i; ++s) drain(&st.full[s], (uint32_t)(((i - 1 - s) / NST) & 1));
+    __syncwarp();
+  } else if (warp == 1) {
+    // three parts beside one another; beyond 256 columns the third on its own
+    const int n1 = 3 * p.rp <= 256 ? 3 * p.rp : 2 * p.rp;
+    const uint32_t id1 = instr_desc(128, n1, 1, 1), id2 = instr_desc(128, p.rp, 1, 1);
+    for (int i = 0; i < steps; ++i) {
+      const int s = i % NST;
+      if (!__all_sync(0xffffffffu, wait(&st.abort, drops ? &st.ready[s] : &st.full[s], (uint32_t)((i / NST) & 1),
+                                        p.plan.status, kRoleFull)))
+        break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t zs = smem_u32(smem + s * Z::kStage), ps = zs + 16384;
+        const uint32_t acc = tmem + (uint32_t)(i % Z::kAcc) * Z::kAccCols, more = i >= Z::kAcc;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint64_t ad = smem_desc(zs + ks * 2048, 8192, 1024);
+          tc_mma(acc, ad, smem_desc(ps + ks * 2048, 8192, 1024), id1, more || ks > 0);
+          if (n1 < 3 * p.rp)
+            tc_mma(acc + n1, ad, smem_desc(ps + (n1 / 64) * 8192 + ks * 2048, 8192, 1024), id2, more || ks > 0);
+        }
+        tc_commit(smem_u32(&st.empty[s]));
+      }
+      __syncwarp();
+    }
+    if (lane == 0) tc_commit(smem_u32(&st.done));
+    __syncwarp();
+  } else if (drops) {
+    const int id = tid - 64, c = id & 15, r0 = id >> 4;
+    const Mask mask(p.rng, job.threshold);
+    for (int i = 0; i < steps; ++i) {
+      const int s = i % NST;
+      if (!__all_sync(0xffffffffu, wait(&st.abort, &st.full[s], (uint32_t)((i / NST) & 1), p.plan.status, kRoleReady)))
+        break;
+      uint8_t *zs = smem + s * Z::kStage + (c >> 3) * 8192;
+      if (c0 + c * 8 < job.d)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int64_t t = st.tok[s][r0 + 16 * h];   // -1: a row of zeros, which stays one
+          uint4 *at = reinterpret_cast<uint4 *>(zs + swz(r0 + 16 * h, c & 7));
+          uint4 w = *at;
+          mask.apply((uint64_t)(t * job.d + c0 + c * 8) >> 3, w);
+          *at = w;
+        }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&st.ready[s]));
+    }
+  }
+  if (!wait(&st.abort, &st.done, 0, p.plan.status, kRoleDone)) st.abort = 1;
   tc_fence_after();
   __syncthreads();
-  if (warp < 4 && st.abort == 0) {
-    const float f = p.factor * (p.scale != nullptr ? p.scale[ch.x] : 1.0f);
-    float *out = ch.w < 0 ? p.out + (int64_t)ch.x * p.rank * p.d : p.partial + (int64_t)ch.w * p.rank * p.d;
-    const int col = c0 + tid;
-    const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16);
-    for (int j = 0; j < p.rp; j += 16) {
-      float hi[16], lo[16];
-      tmem_ld16(at + j, hi);
-      tmem_ld16(at + p.rp + j, lo);
+  if (warp >= 2 && warp < 6 && st.abort == 0) {
+    const float f = job.factor * (job.scale != nullptr ? job.scale[ch.x] : 1.0f);
+    float *out = ch.w < 0 ? job.out + (int64_t)ch.x * p.rank * job.d : job.partial + (int64_t)ch.w * p.rank * job.d;
+    const int quarter = warp & 3, col = c0 + quarter * 32 + lane, accs = min(steps, Z::kAcc);
+    for (int r = 0; r < p.rp; r += 16) {
+      float v[16] = {};
+      for (int a = 0; a < accs; ++a)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) hi[i] = f * (hi[i] + lo[i]);
-      if (col < p.d) {
-        if constexpr (GT) {   // a thread's values lie side by side
+        for (int part = 2; part >= 0; --part) {
+          float w[16];
+          tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + a * Z::kAccCols + part * p.rp + r, w);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += w[i];
+        }
+      if (col < job.d) {
+        if (job.transposed) {   // a thread's values lie side by side
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
-            if (j + i < p.rank)
-              *reinterpret_cast<float4 *>(out + (int64_t)col * p.rank + j + i) =
-                  make_float4(hi[i], hi[i + 1], hi[i + 2], hi[i + 3]);
+            if (r + i < p.rank)
+              *reinterpret_cast<float4 *>(out + (int64_t)col * p.rank + r + i) =
+                  make_float4(f * v[i], f * v[i + 1], f * v[i + 2], f * v[i + 3]);
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (j + i < p.rank) out[(int64_t)(j + i) * p.d + col] = hi[i];
+            if (r + i < p.rank) out[(int64_t)(r + i) * job.d + col] = f * v[i];
         }
       }
     }
@@ -685,104 +868,180 @@ __global__ void __launch_bounds__(kPipeThreads) wgrad_tc_kernel(const WgradTc p)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 4) tmem_free<COLS>(tmem);
+  if (warp == 1) tmem_free(tmem, Z::kAcc * Z::kAccCols);
 }
 
 // ---------------------------------------------------------------------------
+// Tensor maps: 128-byte swizzle, zeros outside.
+cudaError_t map2(CUtensorMap *m, const void *base, int esize, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * esize};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / esize), (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return fn(m, esize == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base),
+            dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess : cudaErrorInvalidValue;
+}
+// [n, rows, cols] bf16, boxes of 64 columns and box_rows rows of one matrix
+cudaError_t map3(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t n, int box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)(cols * rows) * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <typename K> cudaError_t allow(K kernel, size_t smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
-// CTAs a tile: until two a SM have work, as far as four steps are left to each
+// CTAs a tile: several waves of two an SM, as long as each has eight steps, so
+// that the last wave weighs little; where tiles are few, down to four steps.
 void set_split(const AdapterArgs &a, ShrinkTc &p) {
-  const int64_t tiles = host_tiles(a), all = (p.d + 63) / 64;
+  const int64_t tiles = host_tiles(a), all = (p.d + 63) / 64, sms = sm_count();
   p.split = 1;
-  while (p.split < 8 && tiles * p.split < 2 * sm_count() && all / (p.split * 2) >= 4) p.split *= 2;
+  while (p.split < 8 && ((tiles * p.split < 6 * sms && all / (p.split * 2) >= 8) ||
+                         (tiles * p.split < sms && all / (p.split * 2) >= 4)))
+    p.split *= 2;
   p.per = (int)((all + p.split - 1) / p.split);
 }
 
-template <int RPMAX, bool WT> cudaError_t shrink(const AdapterArgs &a, const ShrinkTc &p, cudaStream_t s) {
+template <int RPMAX, bool WT, bool DROP> cudaError_t shrink(const AdapterArgs &a, const ShrinkTc &p, cudaStream_t s) {
   constexpr size_t smem = ShrinkSize<RPMAX, WT>::kSmem;
-  cudaError_t e = allow(shrink_tc_kernel<RPMAX, WT>, smem);
+  cudaError_t e = allow(shrink_tc_kernel<RPMAX, WT, DROP>, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl_clusters(shrink_tc_kernel<RPMAX, WT>, dim3((unsigned)(host_tiles(a) * p.split)), dim3(kPipeThreads),
-                             p.split, smem, s, p);
+  return launch_pdl_clusters(shrink_tc_kernel<RPMAX, WT, DROP>, dim3((unsigned)(host_tiles(a) * p.split)),
+                             dim3(DROP ? 320 : 192), p.split, smem, s, p);
 }
-template <int RPMAX, typename TO, bool VT>
-cudaError_t expand(const AdapterArgs &a, const ExpandTc &p, cudaStream_t s) {
-  constexpr size_t smem = ExpandSize<RPMAX, TO, VT>::kSmem;
-  cudaError_t e = allow(expand_tc_kernel<RPMAX, TO, VT>, smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(expand_tc_kernel<RPMAX, TO, VT>, dim3((unsigned)((p.d + kCols - 1) / kCols * host_tiles(a))),
-                    dim3(kLoaders), smem, s, p);
+template <bool WT, bool DROP> cudaError_t shrink(const AdapterArgs &a, const ShrinkTc &p, cudaStream_t s) {
+  return p.rp <= 32 ? shrink<32, WT, DROP>(a, p, s) : p.rp <= 64 ? shrink<64, WT, DROP>(a, p, s)
+                                                                  : shrink<128, WT, DROP>(a, p, s);
 }
-template <int RPMAX, bool GT> cudaError_t wgrad(const AdapterArgs &a, const WgradTc &p, cudaStream_t s) {
-  constexpr size_t smem = WgradSize<RPMAX>::kSmem;
-  cudaError_t e = allow(wgrad_tc_kernel<RPMAX, GT>, smem);
+// x [T, d] rows ld apart; W [n, rank, d], or [n, d, rank] (WT)
+template <bool WT>
+cudaError_t shrink(const AdapterArgs &a, ShrinkTc &p, const void *x, int64_t ld, const void *W, cudaStream_t s) {
+  p.plan = plan_of(a);
+  p.rank = a.rank;
+  p.rp = padded_rank(a.rank);
+  set_split(a, p);
+  cudaError_t e = map2(&p.mx, x, 2, p.d, a.T, ld, kTileRows);
+  if (e == cudaSuccess) e = map2(&p.mx_row, x, 2, p.d, a.T, ld, 1);
+  if (e == cudaSuccess) e = WT ? map3(&p.mw, W, p.rank, p.d, a.n, 64) : map3(&p.mw, W, p.d, p.rank, a.n, p.rp);
   if (e != cudaSuccess) return e;
-  return launch_pdl(wgrad_tc_kernel<RPMAX, GT>, dim3((unsigned)((p.d + kCols - 1) / kCols), (unsigned)host_chunks(a)),
-                    dim3(kPipeThreads), smem, s, p);
-}
-
-template <int RPMAX> cudaError_t forward(const AdapterArgs &a, int rp, cudaStream_t s) {
-  const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
-  bf16 *parts = reinterpret_cast<bf16 *>(a.ws + sc.u);
-  ShrinkTc sh{};
-  sh.plan = plan_of(a);
-  sh.x = static_cast<const bf16 *>(a.x); sh.W = static_cast<const bf16 *>(a.A); sh.ld = a.ld_in; sh.d = a.d_in;
-  sh.rank = a.rank; sh.rp = rp; sh.threshold = a.threshold; sh.rng = a.rng; sh.factor = drop_scale(a.threshold);
-  sh.parts = parts; sh.by_token = a.u;
-  set_split(a, sh);
-  cudaError_t e = shrink<RPMAX, false>(a, sh, s);
-  if (e != cudaSuccess) return e;
-  ExpandTc ex{};
-  ex.plan = sh.plan; ex.parts = parts; ex.V = static_cast<const bf16 *>(a.B); ex.base = a.base; ex.out = a.y;
-  ex.ld = a.ld_out; ex.d = a.d_out; ex.rank = a.rank; ex.rp = rp; ex.scale = a.scale; ex.factor = 1.0f;
-  return expand<RPMAX, bf16, false>(a, ex, s);
+  return p.threshold != 0 ? shrink<WT, true>(a, p, s) : shrink<WT, false>(a, p, s);
 }
 
-template <int RPMAX> cudaError_t backward(const AdapterArgs &a, int rp, cudaStream_t s) {
+constexpr int kExpandSmem = 222 * 1024;
+// out [T, d] rows ld apart; V [n, d, rank], or [n, rank, d] (VT)
+template <typename TO, bool VT>
+cudaError_t expand(const AdapterArgs &a, ExpandTc &p, const bf16 *parts, const void *V, cudaStream_t s) {
+  constexpr int esize = sizeof(TO);
+  p.plan = plan_of(a);
+  p.rank = a.rank;
+  p.rp = padded_rank(a.rank);
+  p.nparts = esize == 4 ? 3 : 2;
+  p.p_bytes = (p.nparts * p.rp + 63) / 64 * 16384;
+  p.v_bytes = VT ? p.rp * 256 : (p.rp + 63) / 64 * 16384;
+  p.n_p = p.p_bytes <= 32768 ? 2 : 1;
+  p.n_v = p.n_p * p.p_bytes + 2 * p.v_bytes + 4 * 16384 <= kExpandSmem ? 2 : 1;
+  p.n_slab = (kExpandSmem - p.n_p * p.p_bytes - p.n_v * p.v_bytes) / 32768;   // two at least: a slab is
+  if (p.n_slab > kMaxRing / 2) p.n_slab = kMaxRing / 2;                       // released by the next one's store
+  // columns of an item: enough items for every SM to have several
+  const int64_t tiles = host_tiles(a), blocks = (p.d + kCols - 1) / kCols, sms = sm_count();
+  int64_t span = tiles * blocks / (8 * sms);
+  p.span = (int)(span < 1 ? 1 : span > 16 ? 16 : span);
+  const int64_t items = tiles * ((blocks + p.span - 1) / p.span);
+  cudaError_t e = map2(&p.mp, parts, 2, 3 * p.rp, a.T, 3 * p.rp, kTileRows);
+  if (e == cudaSuccess) e = VT ? map3(&p.mv, V, p.d, p.rank, a.n, p.rp) : map3(&p.mv, V, p.rank, p.d, a.n, kCols);
+  if (e == cudaSuccess && p.base != nullptr) e = map2(&p.mb, p.base, esize, p.d, a.T, p.ld, kTileRows);
+  if (e == cudaSuccess && p.base != nullptr) e = map2(&p.mb_row, p.base, esize, p.d, a.T, p.ld, 1);
+  if (e == cudaSuccess) e = map2(&p.mo, p.out, esize, p.d, a.T, p.ld, 32);
+  if (e == cudaSuccess) e = allow(expand_tc_kernel<TO, VT>, kExpandSmem + 1024);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(expand_tc_kernel<TO, VT>, dim3((unsigned)(items < sms ? items : sms)), dim3(kExpandThreads),
+                    (size_t)kExpandSmem + 1024, s, p);
+}
+
+template <int ATOMS, bool DROP> cudaError_t wgrad(const AdapterArgs &a, const WgradTc &p, cudaStream_t s) {
+  constexpr size_t smem = WgradSize<ATOMS>::kSmem;
+  cudaError_t e = allow(wgrad_tc_kernel<ATOMS, DROP>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(wgrad_tc_kernel<ATOMS, DROP>, dim3((unsigned)(p.blocks[0] + p.blocks[1]), (unsigned)host_chunks(a)),
+                    dim3(DROP ? 320 : 192), smem, s, p);
+}
+cudaError_t wgrad(const AdapterArgs &a, const bf16 *u, const bf16 *du, cudaStream_t s) {
   const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
-  bf16 *u = reinterpret_cast<bf16 *>(a.ws + sc.u), *du = reinterpret_cast<bf16 *>(a.ws + sc.du);
-  const float keep = drop_scale(a.threshold);
-  ShrinkTc sh{};
-  sh.plan = plan_of(a);
-  sh.x = static_cast<const bf16 *>(a.dy); sh.W = static_cast<const bf16 *>(a.B); sh.ld = a.ld_out; sh.d = a.d_out;
-  sh.rank = a.rank; sh.rp = rp; sh.scale = a.scale; sh.factor = 1.0f; sh.parts = du;
-  if (a.dA != nullptr) { sh.u_in = a.u_in; sh.parts_in = u; }
-  set_split(a, sh);
-  cudaError_t e = shrink<RPMAX, true>(a, sh, s);
-  if (e == cudaSuccess && a.dA != nullptr) {
-    WgradTc w{};
-    w.plan = sh.plan; w.rank = a.rank; w.rp = rp;
-    w.z = static_cast<const bf16 *>(a.dy); w.parts = u; w.ld = a.ld_out; w.d = a.d_out; w.scale = a.scale; w.factor = 1.0f;
-    w.out = a.dB; w.partial = reinterpret_cast<float *>(a.ws + sc.dB);
-    e = wgrad<RPMAX, true>(a, w, s);
-    w.z = static_cast<const bf16 *>(a.x); w.parts = du; w.ld = a.ld_in; w.d = a.d_in; w.scale = nullptr; w.factor = keep;
-    w.threshold = a.threshold; w.rng = a.rng; w.out = a.dA; w.partial = reinterpret_cast<float *>(a.ws + sc.dA);
-    if (e == cudaSuccess) e = wgrad<RPMAX, false>(a, w, s);
-    if (e == cudaSuccess) e = launch_adapter_join(a, s);
-  }
-  if (e == cudaSuccess && a.dx != nullptr) {
-    ExpandTc ex{};
-    ex.plan = sh.plan; ex.parts = du; ex.V = static_cast<const bf16 *>(a.A); ex.base = a.dx_in; ex.out = a.dx;
-    ex.ld = a.d_in; ex.d = a.d_in; ex.rank = a.rank; ex.rp = rp; ex.threshold = a.threshold; ex.rng = a.rng;
-    ex.factor = keep;
-    e = a.dx_dtype == MOE_F32 ? expand<RPMAX, float, true>(a, ex, s) : expand<RPMAX, bf16, true>(a, ex, s);
-  }
-  return e;
+  WgradTc p{};
+  p.plan = plan_of(a);
+  p.rank = a.rank;
+  p.rp = padded_rank(a.rank);
+  p.rng = a.rng;
+  auto fill = [&](int j, const void *z, int64_t ld, int d, const bf16 *parts, float *out, size_t partial) {
+    WgradJob &w = p.job[j];
+    p.blocks[j] = (d + kCols - 1) / kCols;
+    w.d = d;
+    w.out = out;
+    w.partial = reinterpret_cast<float *>(a.ws + partial);
+    cudaError_t e = map2(&w.mz, z, 2, d, a.T, ld, 64);
+    if (e == cudaSuccess) e = map2(&w.mz_row, z, 2, d, a.T, ld, 1);
+    if (e == cudaSuccess) e = map2(&w.mp, parts, 2, 3 * p.rp, a.T, 3 * p.rp, 64);
+    if (e == cudaSuccess) e = map2(&w.mp_row, parts, 2, 3 * p.rp, a.T, 3 * p.rp, 1);
+    return e;
+  };
+  cudaError_t e = fill(0, a.x, a.ld_in, a.d_in, du, a.dA, sc.dA);
+  if (e == cudaSuccess) e = fill(1, a.dy, a.ld_out, a.d_out, u, a.dB, sc.dB);
+  if (e != cudaSuccess) return e;
+  p.job[0].threshold = a.threshold;
+  p.job[0].factor = drop_scale(a.threshold);
+  p.job[1].transposed = 1;
+  p.job[1].scale = a.scale;
+  p.job[1].factor = 1.0f;
+  const int atoms = (3 * p.rp + 63) / 64;
+  if (a.threshold != 0)
+    return atoms == 1 ? wgrad<1, true>(a, p, s) : atoms == 2 ? wgrad<2, true>(a, p, s)
+           : atoms == 3 ? wgrad<3, true>(a, p, s) : wgrad<6, true>(a, p, s);
+  return atoms == 1 ? wgrad<1, false>(a, p, s) : atoms == 2 ? wgrad<2, false>(a, p, s)
+         : atoms == 3 ? wgrad<3, false>(a, p, s) : wgrad<6, false>(a, p, s);
 }
 
 }  // namespace
 
-// Shared memory and TMEM are taken for ranks up to 32, 64 or 128.
 cudaError_t launch_adapter_tc(const AdapterArgs &a, cudaStream_t s) {
-  const int rp = (a.rank + 15) / 16 * 16;
-  return rp <= 32 ? forward<32>(a, rp, s) : rp <= 64 ? forward<64>(a, rp, s) : forward<128>(a, rp, s);
+  const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
+  bf16 *parts = reinterpret_cast<bf16 *>(a.ws + sc.u);
+  ShrinkTc sh{};
+  sh.d = a.d_in; sh.threshold = a.threshold; sh.rng = a.rng; sh.factor = drop_scale(a.threshold);
+  sh.parts = parts; sh.by_token = a.u;
+  cudaError_t e = shrink<false>(a, sh, a.x, a.ld_in, a.A, s);
+  if (e != cudaSuccess) return e;
+  ExpandTc ex{};
+  ex.base = a.base; ex.out = a.y; ex.ld = a.ld_out; ex.d = a.d_out; ex.scale = a.scale; ex.factor = 1.0f;
+  return expand<bf16, false>(a, ex, parts, a.B, s);
 }
+
 cudaError_t launch_adapter_bwd_tc(const AdapterArgs &a, cudaStream_t s) {
-  const int rp = (a.rank + 15) / 16 * 16;
-  return rp <= 32 ? backward<32>(a, rp, s) : rp <= 64 ? backward<64>(a, rp, s) : backward<128>(a, rp, s);
+  const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
+  bf16 *u = reinterpret_cast<bf16 *>(a.ws + sc.u), *du = reinterpret_cast<bf16 *>(a.ws + sc.du);
+  ShrinkTc sh{};
+  sh.d = a.d_out; sh.scale = a.scale; sh.factor = 1.0f; sh.parts = du;
+  if (a.dA != nullptr) { sh.u_in = a.u_in; sh.parts_in = u; }
+  cudaError_t e = shrink<true>(a, sh, a.dy, a.ld_out, a.B, s);
+  if (e == cudaSuccess && a.dA != nullptr) {
+    e = wgrad(a, u, du, s);
+    if (e == cudaSuccess) e = launch_adapter_join(a, s);
+  }
+  if (e == cudaSuccess && a.dx != nullptr) {
+    ExpandTc ex{};
+    ex.base = a.dx_in; ex.out = a.dx; ex.ld = a.d_in; ex.d = a.d_in; ex.threshold = a.threshold; ex.rng = a.rng;
+    ex.factor = drop_scale(a.threshold);
+    e = a.dx_dtype == MOE_F32 ? expand<float, true>(a, ex, du, a.A, s) : expand<bf16, true>(a, ex, du, a.A, s);
+  }
+  return e;
 }
 
 }  // namespace moe

@@ -58,11 +58,9 @@
 // returns, so the GPU context stays usable.
 #include <cstdlib>
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "softmax.cuh"
 #include "tc.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 namespace {
@@ -1372,19 +1370,6 @@ __global__ void group_maps_kernel(const __grid_constant__ CUtensorMap tA,
 
 // ---------------------------------------------------------------------------
 // host side
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (fn == nullptr) {
-    cudaDriverEntryPointQueryResult q;
-    void *ptr = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
 
 // 2D bf16 tensor [outer, inner] row-major (inner contiguous), box
 // {64 inner, box_outer}, 128-byte swizzle, zero fill out of bounds.
