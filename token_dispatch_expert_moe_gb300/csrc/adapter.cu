@@ -298,9 +298,7 @@ __global__ void __launch_bounds__(kSimtThreads) shrink_kernel(const Shrink p) {
   __shared__ __align__(16) float xs[kSimtRows * kPad];
   __shared__ __align__(16) float ws[128 * kPad];
   __shared__ int64_t tok[kSimtRows];
-  const int64_t ti = blockIdx.x / 4;
-  if (ti >= p.plan.tiles()) return;
-  const int4 tile = p.plan.tile(ti);
+  const int4 tile = p.plan.tile_of(blockIdx.x / 4);
   const int r0 = (int)(blockIdx.x % 4) * kSimtRows, rows = min(kSimtRows, tile.z - r0), tid = threadIdx.x;
   if (rows <= 0) return;
   if (tid < kSimtRows) tok[tid] = tid < rows ? p.plan.token(tile.y + r0 + tid) : -1;
@@ -397,9 +395,7 @@ __global__ void __launch_bounds__(kSimtThreads) expand_kernel(const Expand p) {
   __shared__ __align__(16) float us[kSimtRows][36];
   __shared__ __align__(16) float wt[32][kExpandCols + 4];
   __shared__ int64_t tok[kSimtRows];
-  const int64_t ti = blockIdx.x / 4;
-  if (ti >= p.plan.tiles()) return;
-  const int4 tile = p.plan.tile(ti);
+  const int4 tile = p.plan.tile_of(blockIdx.x / 4);
   const int r0 = (int)(blockIdx.x % 4) * kSimtRows, rows = min(kSimtRows, tile.z - r0), tid = threadIdx.x;
   if (rows <= 0) return;
   const TO *base = static_cast<const TO *>(p.base);
@@ -487,8 +483,7 @@ __global__ void __launch_bounds__(kSimtThreads) wgrad_kernel(const Wgrad p) {
   float (*zs)[kGradCols + 4] = reinterpret_cast<float(*)[kGradCols + 4]>(buf);
   float (*vs)[128] = reinterpret_cast<float(*)[128]>(buf + 32 * (kGradCols + 4));
   __shared__ int64_t tok[32];
-  if (blockIdx.x >= p.plan.chunks()) return;
-  const int4 ch = p.plan.chunk(blockIdx.x);
+  const int4 ch = p.plan.chunk_of(blockIdx.x);
   if (ch.z <= 0) return;
   const int r = p.rank, r8 = (r + 7) / 8, c0 = blockIdx.y * kGradCols, tid = threadIdx.x;
   const int set = r8 * 16, sets = kSimtThreads / set, mine = tid / set, at = tid % set;
@@ -549,7 +544,7 @@ __global__ void __launch_bounds__(kSimtThreads) wgrad_kernel(const Wgrad p) {
 
 // The second pass: zeros for adapters without tokens, the chunks' sums in order
 // for those of several; nothing to do for one chunk.
-constexpr int kJoinThreads = 256, kJoinEach = 4;
+constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(Plan plan, int64_t na, int64_t nb, float *dA, float *dB,
                                                             const float *pa, const float *pb) {
@@ -558,20 +553,20 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Plan plan, int64_t n
   const int a = blockIdx.y;
   const int2 g = plan.group(a);
   if (g.y == 1) return;
-  const int64_t step = (int64_t)gridDim.x * kJoinThreads * 4;
-  for (int64_t i = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 4; i < na + nb; i += step) {
-    const bool second = i >= na;   // na and nb are multiples of 4
-    const int64_t n = second ? nb : na, k = second ? i - na : i;
-    const float *p = second ? pb : pa;
-    float v[4] = {};
-    for (int c = 0; c < g.y; ++c) {
-      float w[4];
-      load4(p + (g.x + c) * n + k, w);
+  const int64_t i = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 4;
+  if (i >= na + nb) return;
+  const bool second = i >= na;   // na and nb are multiples of 4
+  const int64_t n = second ? nb : na, k = second ? i - na : i;
+  const float *p = (second ? pb : pa) + g.x * n + k;
+  float v[4] = {};
+#pragma unroll 8
+  for (int c = 0; c < g.y; ++c) {
+    float w[4];
+    load4(p + c * n, w);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += w[j];
-    }
-    store4((second ? dB : dA) + a * n + k, v);
+    for (int j = 0; j < 4; ++j) v[j] += w[j];
   }
+  store4((second ? dB : dA) + a * n + k, v);
 }
 
 template <typename T, bool WT>
@@ -630,7 +625,7 @@ template <typename T> cudaError_t backward(const AdapterArgs &a, cudaStream_t s)
 cudaError_t launch_adapter_join(const AdapterArgs &a, cudaStream_t s) {
   const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
   const int64_t na = (int64_t)a.rank * a.d_in, nb = (int64_t)a.rank * a.d_out;
-  const int64_t each = kJoinThreads * 4 * kJoinEach, ctas = (na + nb + each - 1) / each;
+  const int64_t each = kJoinThreads * 4, ctas = (na + nb + each - 1) / each;   // four sums a thread
   return launch_pdl(join_kernel, dim3((unsigned)ctas, (unsigned)a.n), dim3(kJoinThreads), 0, s, plan_of(a), na, nb, a.dA,
                     a.dB, reinterpret_cast<const float *>(a.ws + sc.dA), reinterpret_cast<const float *>(a.ws + sc.dB));
 }

@@ -10,15 +10,15 @@ namespace moe {
 constexpr int kTileRows = 128;   // tokens of a tile, all of one adapter
 
 // Tokens of a chunk: the weight gradients are summed over a chunk's tokens in
-// one CTA, and over an adapter's chunks in a second pass. An eighth of the
+// one CTA, and over an adapter's chunks in a second pass. A sixteenth of the
 // batch gives that pass few partial sums and the first enough CTAs.
 __host__ __device__ constexpr int64_t chunk_rows(int64_t T) {
-  const int64_t e = (T / 8 + kTileRows - 1) / kTileRows * kTileRows;
-  return e < 512 ? 512 : e;
+  const int64_t e = (T / 16 + kTileRows - 1) / kTileRows * kTileRows;
+  return e < kTileRows ? kTileRows : e;
 }
 // An adapter of several chunks has more than one chunk's tokens, so at most
 // twice as many chunks as full ones.
-constexpr int kMaxSlots = 16;
+constexpr int kMaxSlots = 32;
 
 // The map, in 32-bit words: a header, order [T] (the tokens by adapter, in
 // their order inside one; those without an adapter last), and, 16-byte aligned,
@@ -55,10 +55,31 @@ struct Plan {
   uint32_t *status;
 
   __device__ __forceinline__ bool of_this_batch() const {
-    if (map == nullptr) return true;
-    if (map[kMapT] == (int32_t)T && map[kMapN] == n) return true;
+    return map == nullptr || this_batch(*reinterpret_cast<const int4 *>(map));
+  }
+  // Tile i of a grid of at most max_tiles: -1 and no rows beyond the batch's. The
+  // header and the tile are read at once.
+  __device__ __forceinline__ int4 tile_of(int64_t i) const {
+    if (map == nullptr) return i < tiles() ? tile(i) : make_int4(-1, 0, 0, 0);
+    const int4 head = *reinterpret_cast<const int4 *>(map);
+    const int4 t = reinterpret_cast<const int4 *>(map + map_layout(T, n).tiles)[i];
+    return this_batch(head) && i < head.z ? checked(t, kTileRows) : make_int4(-1, 0, 0, 0);
+  }
+  __device__ __forceinline__ int4 chunk_of(int64_t i) const {
+    if (map == nullptr) return i < chunks() ? chunk(i) : make_int4(-1, 0, 0, -1);
+    const int4 head = *reinterpret_cast<const int4 *>(map);
+    const int4 c = reinterpret_cast<const int4 *>(map + map_layout(T, n).chunks)[i];
+    return this_batch(head) && i < head.w ? checked_chunk(c) : make_int4(-1, 0, 0, -1);
+  }
+  __device__ __forceinline__ bool this_batch(const int4 &head) const {
+    if (head.x == (int32_t)T && head.y == n) return true;
     report(status, MOE_ERR_DEVICE, kInfoAdapterMap);
     return false;
+  }
+  __device__ __forceinline__ int4 checked_chunk(int4 c) const {
+    c = checked(c, chunk_rows(T));
+    if (c.x < 0 || c.w >= kMaxSlots) c.z = 0;
+    return c;
   }
   __device__ __forceinline__ int64_t tiles() const {
     if (map == nullptr) return (T + kTileRows - 1) / kTileRows;
@@ -92,9 +113,7 @@ struct Plan {
       const int64_t left = T - i * C;
       return make_int4(0, (int)(i * C), (int)(left < C ? left : C), T > C ? (int)i : -1);
     }
-    int4 c = checked(reinterpret_cast<const int4 *>(map + map_layout(T, n).chunks)[i], C);
-    if (c.x < 0 || c.w >= kMaxSlots) c.z = 0;
-    return c;
+    return checked_chunk(reinterpret_cast<const int4 *>(map + map_layout(T, n).chunks)[i]);
   }
   __device__ __forceinline__ int2 group(int a) const {
     if (map == nullptr) {

@@ -112,12 +112,13 @@ struct Mask {
     asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(m) : "r"((u & w) | ((u | w) & maj)));
     return m;
   }
-  __device__ __forceinline__ void apply(uint64_t block, uint4 &v) const {
+  __device__ __forceinline__ uint4 words(uint64_t block) const {
     const uint4 w = g.block(block);
-    v.x &= word(w.x);
-    v.y &= word(w.y);
-    v.z &= word(w.z);
-    v.w &= word(w.w);
+    return make_uint4(word(w.x), word(w.y), word(w.z), word(w.w));
+  }
+  static __device__ __forceinline__ void apply(uint4 *at, const uint4 &m) {
+    const uint4 v = *at;
+    *at = make_uint4(v.x & m.x, v.y & m.y, v.z & m.z, v.w & m.w);
   }
 };
 
@@ -167,11 +168,15 @@ struct ShrinkTc {
   bf16 *parts_in;
 };
 
-template <int RPMAX, bool WT> struct ShrinkSize {
+template <int RPMAX, bool WT, bool DROP> struct ShrinkSize {
   static constexpr int kW = WT ? 8192 * ((RPMAX + 63) / 64) : RPMAX * 128;
   static constexpr int kStage = 16384 + kW;
-  static constexpr int kStages = (100 * 1024) / kStage;   // two CTAs an SM
-  static constexpr int kAcc = RPMAX <= 64 ? 4 : 2;
+  // Many CTAs an SM with short rings: one's start and end (7 us of loads that
+  // wait for one another, and the sums' way out) hide behind the others. With
+  // dropout three, for the registers.
+  static constexpr int kCtas = RPMAX > 64 ? 2 : DROP ? 3 : 4;
+  static constexpr int kStages = kCtas == 4 ? 2 : 3;
+  static constexpr int kAcc = RPMAX <= 32 ? 4 : 2;
   static constexpr int kTmem = kAcc * RPMAX;
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
 };
@@ -184,8 +189,8 @@ struct Shared {
 };
 
 template <int RPMAX, bool WT, bool DROP>
-__global__ void __launch_bounds__(DROP ? 320 : 192) shrink_tc_kernel(const __grid_constant__ ShrinkTc p) {
-  using Z = ShrinkSize<RPMAX, WT>;
+__global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP>::kCtas) shrink_tc_kernel(const __grid_constant__ ShrinkTc p) {
+  using Z = ShrinkSize<RPMAX, WT, DROP>;
   constexpr int NST = Z::kStages, WORK = DROP ? 256 : 128, THREADS = WORK + 64;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -205,8 +210,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192) shrink_tc_kernel(const __gri
   pdl_wait();
   const int64_t ti = blockIdx.x / p.split;
   const int q = (int)(blockIdx.x % p.split);   // the CTA's rank in its cluster
-  const bool on = ti < p.plan.tiles();
-  const int4 tile = on ? p.plan.tile(ti) : make_int4(-1, 0, 0, 0);
+  const int4 tile = p.plan.tile_of(ti);
   if (tile.x < 0) {   // the whole cluster
     if (p.by_token != nullptr && q == 0)
       for (int i = tid; i < tile.z * p.rank; i += THREADS)
@@ -281,20 +285,22 @@ __global__ void __launch_bounds__(DROP ? 320 : 192) shrink_tc_kernel(const __gri
   } else if constexpr (DROP) {
     const int id = tid - 64, c = id & 7, r0 = id >> 3;
     const Mask mask(p.rng, p.threshold);
+    uint64_t block[4];   // of the generator: rows past the end count for nothing
+#pragma unroll
+    for (int h = 0; h < 4; ++h) block[h] = (uint64_t)((int64_t)st.tok[r0 + 32 * h] * (p.d >> 3) + k0 * 8 + c);
     for (int i = 0; i < steps; ++i) {
-      const int s = i % NST, k = (k0 + i) * 64 + c * 8;
+      const int s = i % NST;
+      uint4 m[4];   // while the stage is on its way
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        m[h] = mask.words(block[h]);
+        block[h] += 8;
+      }
       if (!__all_sync(0xffffffffu, wait(&st.abort, &st.full[s], (uint32_t)((i / NST) & 1), p.plan.status, kRoleReady)))
         break;
       uint8_t *xs = smem + s * Z::kStage;
-      if (k < p.d)
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int64_t t = st.tok[r0 + 32 * h];
-          uint4 *at = reinterpret_cast<uint4 *>(xs + swz(r0 + 32 * h, c));
-          uint4 w = *at;
-          mask.apply((uint64_t)(t * p.d + k) >> 3, w);   // rows past the end count for nothing
-          *at = w;
-        }
+      for (int h = 0; h < 4; ++h) Mask::apply(reinterpret_cast<uint4 *>(xs + swz(r0 + 32 * h, c)), m[h]);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&st.ready[s]));
@@ -373,11 +379,13 @@ __global__ void __launch_bounds__(DROP ? 320 : 192) shrink_tc_kernel(const __gri
 // ---------------------------------------------------------------------------
 // Expand. One CTA an SM runs through items: a tile and up to `span` blocks of
 // 128 columns. Base rows come by TMA into slabs of 128 rows x 128 bytes, the
-// product of a block into one of two accumulators; two sets of four warps take
-// the blocks in turn: a thread adds its row of the accumulator to its row of
-// the slab, and the slab leaves by TMA, or row by row where the tile's rows do
-// not follow one another. Each set has an accumulator and a ring of slabs of its
-// own, so that it sees every phase of the barriers it waits on.
+// product of a block into the accumulator of one of two sets of four warps,
+// which take the blocks in turn: a thread adds its row of the accumulator to its
+// row of the slab, and the slab leaves by TMA, or row by row where the tile's
+// rows do not follow one another. Each set has a ring of slabs of its own, so
+// that it sees every phase of the barriers it waits on. With dropout eight more
+// warps make the masks ahead, a bit an element: made by the sets themselves
+// they kept the slabs waiting (32768 x 8192, rank 16: 355 us).
 struct ExpandTc {
   CUtensorMap mp, mv, mb, mb_row, mo;   // parts, V [n, d, rank] or [n, rank, d], base (128 rows; one), out (32 rows)
   Plan plan;
@@ -385,37 +393,45 @@ struct ExpandTc {
   void *out;
   int64_t ld;
   int d, rank, rp, nparts, span;
-  int p_bytes, v_bytes, n_p, n_v, n_slab;   // shared memory: parts, V, how many of each, and slabs of a set
+  int p_bytes, v_bytes, n_v, n_slab;    // shared memory: parts, V and how many of them, slabs of a set
   uint32_t threshold;
   const uint64_t *rng;
   const float *scale;
   float factor;
 };
-constexpr int kExpandThreads = 64 + 256;
+
+// Warps 0: base, 1: products, 2: parts and V, 3: none, 4-11: the sets, 12-19: masks
+template <bool DROP> constexpr int expand_threads() { return DROP ? 640 : 384; }
 
 struct ExpandShared {
-  uint64_t pfull[2], pempty[2], vfull[2], vempty[2], sfull[kMaxRing], sempty[kMaxRing], dfull[2], dempty[2];
+  uint64_t pfull, pempty, vfull[2], vempty[2], sfull[kMaxRing], sempty[kMaxRing], dfull[2], dempty[2];
+  uint64_t mfull[4], mempty[4];     // masks: two buffers of each set
   uint32_t tmem;
   volatile int abort;
+  uint4 masks[4][kTileRows];        // a bit a column
 };
 
-template <typename TO, bool VT>
-__global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __grid_constant__ ExpandTc p) {
+template <typename TO, bool VT, bool DROP>
+__global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(const __grid_constant__ ExpandTc p) {
   constexpr int VN = 16 / sizeof(TO), PER = 128 / sizeof(TO), SLABS = kCols / PER;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *vs = smem + p.n_p * p.p_bytes, *slabs = vs + p.n_v * p.v_bytes;
+  uint8_t *vs = smem + p.p_bytes, *slabs = vs + p.n_v * p.v_bytes;
   __shared__ ExpandShared st;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     st.abort = 0;
+    mbar_init(smem_u32(&st.pfull), 1);
+    mbar_init(smem_u32(&st.pempty), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&st.pfull[i]), 1);
-      mbar_init(smem_u32(&st.pempty[i]), 1);
       mbar_init(smem_u32(&st.vfull[i]), 1);
       mbar_init(smem_u32(&st.vempty[i]), 1);
       mbar_init(smem_u32(&st.dfull[i]), 1);
       mbar_init(smem_u32(&st.dempty[i]), 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&st.mfull[i]), 8);
+      mbar_init(smem_u32(&st.mempty[i]), 4);
     }
     for (int i = 0; i < 2 * p.n_slab; ++i) {
       mbar_init(smem_u32(&st.sfull[i]), 1);
@@ -424,7 +440,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __gr
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async();
   }
-  if (warp == 1) tmem_alloc(&st.tmem, 256);
+  if (warp == 1) tmem_alloc(&st.tmem, 2 * kCols);
   pdl_wait();
   tc_fence_before();
   __syncthreads();
@@ -441,11 +457,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __gr
     b1 = min(blocks, b0 + p.span);
     return tile.z > 0 && (tile.x >= 0 || base != out);
   };
+  bool ok = true;
+  int block = 0;   // blocks so far: block b is set b % 2's (b / 2)-th
 
   if (warp == 0) {
-    // ---- fetch
-    int pi = 0, vi = 0, block = 0, si[2] = {0, 0};   // parts, V, blocks, and each set's slabs so far
-    bool ok = true;
+    // ---- base rows
+    int fetched[2] = {};   // slabs of each set
     for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
       int4 tile;
       int b0, b1;
@@ -453,43 +470,14 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __gr
       int t[4];
       lane_tokens(p.plan, tile.y, 4 * lane, tile.z, t);
       const int row0 = __shfl_sync(0xffffffffu, t[0], 0);
-      const int last = (int)p.plan.token(tile.y + tile.z - 1);
-      const bool run = last - row0 == tile.z - 1;
-      const bool live = tile.x >= 0;
-      if (live) {
-        const int b = pi % p.n_p;
-        if (pi >= p.n_p) ok = wait(&st.abort, &st.pempty[b], (uint32_t)((pi / p.n_p - 1) & 1), p.plan.status, kRoleEmpty);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        if (lane == 0) {
-          mbar_expect_tx(smem_u32(&st.pfull[b]), (uint32_t)p.p_bytes);
-          for (int k = 0; k * 16384 < p.p_bytes; ++k)
-            tma_load_2d(smem_u32(smem + b * p.p_bytes + k * 16384), &p.mp, smem_u32(&st.pfull[b]), k * 64, tile.y);
-        }
-        ++pi;
-      }
-      for (int blk = b0; blk < b1; ++blk, ++block) {
-        const int c0 = blk * kCols, set = block & 1;
-        if (live) {
-          const int b = vi % p.n_v;
-          if (vi >= p.n_v) ok = wait(&st.abort, &st.vempty[b], (uint32_t)((vi / p.n_v - 1) & 1), p.plan.status, kRoleEmpty);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          if (lane == 0) {
-            mbar_expect_tx(smem_u32(&st.vfull[b]), (uint32_t)p.v_bytes);
-            const uint32_t dst = smem_u32(vs + b * p.v_bytes);
-            if constexpr (VT) {
-              for (int k = 0; k < 2; ++k) tma_load_3d(dst + k * (p.v_bytes / 2), &p.mv, &st.vfull[b], c0 + 64 * k, 0, tile.x);
-            } else {
-              for (int k = 0; k * 16384 < p.v_bytes; ++k) tma_load_3d(dst + k * 16384, &p.mv, &st.vfull[b], k * 64, c0, tile.x);
-            }
-          }
-          ++vi;
-        }
+      const bool run = (int)p.plan.token(tile.y + tile.z - 1) - row0 == tile.z - 1;
+      for (int blk = b0; blk < b1 && ok; ++blk, ++block) {
+        const int set = block & 1;
         for (int s = 0; s < SLABS; ++s) {
-          const int n = set ? si[1]++ : si[0]++, b = set * p.n_slab + n % p.n_slab;
+          const int n = (block >> 1) * SLABS + s, b = set * p.n_slab + n % p.n_slab, c = blk * kCols + s * PER;
           if (n >= p.n_slab)
             ok = wait(&st.abort, &st.sempty[b], (uint32_t)((n / p.n_slab - 1) & 1), p.plan.status, kRoleEmpty);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          const int c = c0 + s * PER;
           if (base == nullptr || c >= p.d) {
             if (lane == 0) mbar_arrive(smem_u32(&st.sfull[b]));
           } else {
@@ -501,23 +489,59 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __gr
             __syncwarp();
             if (!run) tma_gather4(dst + lane * 512, &p.mb_row, &st.sfull[b], c, t);
           }
+          if (set) fetched[1] = n + 1;
+          else fetched[0] = n + 1;
         }
-        if (!ok) break;
       }
     }
+    __syncwarp();
+    if (lane == 0)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        for (int b = 0; b < p.n_slab && b < fetched[h]; ++b)
+          drain(&st.sfull[h * p.n_slab + b], (uint32_t)(((fetched[h] - 1 - b) / p.n_slab) & 1));
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---- parts and V
+    int pi = 0, vi = 0;
+    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      int4 tile;
+      int b0, b1;
+      if (!item(it, tile, b0, b1) || tile.x < 0) continue;
+      if (pi > 0) ok = wait(&st.abort, &st.pempty, (uint32_t)((pi - 1) & 1), p.plan.status, kRoleEmpty);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (lane == 0) {
+        mbar_expect_tx(smem_u32(&st.pfull), (uint32_t)p.p_bytes);
+        for (int k = 0; k * 16384 < p.p_bytes; ++k)
+          tma_load_2d(smem_u32(smem + k * 16384), &p.mp, smem_u32(&st.pfull), k * 64, tile.y);
+      }
+      ++pi;
+      for (int blk = b0; blk < b1; ++blk) {
+        const int b = vi % p.n_v, c0 = blk * kCols;
+        if (vi >= p.n_v) ok = wait(&st.abort, &st.vempty[b], (uint32_t)((vi / p.n_v - 1) & 1), p.plan.status, kRoleEmpty);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (lane == 0) {
+          mbar_expect_tx(smem_u32(&st.vfull[b]), (uint32_t)p.v_bytes);
+          const uint32_t dst = smem_u32(vs + b * p.v_bytes);
+          if constexpr (VT) {
+            for (int k = 0; k < 2; ++k) tma_load_3d(dst + k * (p.v_bytes / 2), &p.mv, &st.vfull[b], c0 + 64 * k, 0, tile.x);
+          } else {
+            for (int k = 0; k * 16384 < p.v_bytes; ++k) tma_load_3d(dst + k * 16384, &p.mv, &st.vfull[b], k * 64, c0, tile.x);
+          }
+        }
+        ++vi;
+      }
+    }
+    __syncwarp();
     if (lane == 0) {
-      for (int b = 0; b < p.n_p && b < pi; ++b) drain(&st.pfull[b], (uint32_t)(((pi - 1 - b) / p.n_p) & 1));
+      if (pi > 0) drain(&st.pfull, (uint32_t)((pi - 1) & 1));
       for (int b = 0; b < p.n_v && b < vi; ++b) drain(&st.vfull[b], (uint32_t)(((vi - 1 - b) / p.n_v) & 1));
-      for (int h = 0; h < 2; ++h)   // after a wait that gave up the last slab counted may not have been fetched
-        for (int b = 0, n = (h ? si[1] : si[0]) - (ok ? 0 : 1); b < p.n_slab && b < n; ++b)
-          drain(&st.sfull[h * p.n_slab + b], (uint32_t)(((n - 1 - b) / p.n_slab) & 1));
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---- products
     const uint32_t idesc = instr_desc(128, kCols, 0, VT ? 1 : 0);
-    int pi = 0, vi = 0, block = 0, used[2] = {0, 0}, last = -1;   // used: of each accumulator so far
-    bool ok = true;
+    int pi = 0, vi = 0, last_set = -1, last_use = 0, used[2] = {};   // used: uses of each accumulator so far
     for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
       int4 tile;
       int b0, b1;
@@ -526,8 +550,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __gr
         block += b1 - b0;
         continue;
       }
-      const int pb = pi % p.n_p;
-      ok = wait(&st.abort, &st.pfull[pb], (uint32_t)((pi / p.n_p) & 1), p.plan.status, kRoleFull);
+      ok = wait(&st.abort, &st.pfull, (uint32_t)(pi & 1), p.plan.status, kRoleFull);
       for (int blk = b0; blk < b1; ++blk, ++vi, ++block) {
         const int vb = vi % p.n_v, db = block & 1, n = db ? used[1]++ : used[0]++;
         if (ok) ok = wait(&st.abort, &st.vfull[vb], (uint32_t)((vi / p.n_v) & 1), p.plan.status, kRoleFull);
@@ -535,7 +558,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __gr
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         if (lane == 0) {
-          const uint32_t as = smem_u32(smem + pb * p.p_bytes), bs = smem_u32(vs + vb * p.v_bytes);
+          const uint32_t as = smem_u32(smem), bs = smem_u32(vs + vb * p.v_bytes);
           const int per = p.rp / 16;
           int ks = 0;
           for (int part = 0; part < p.nparts; ++part)
@@ -547,23 +570,54 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __gr
             }
           tc_commit(smem_u32(&st.vempty[vb]));
           tc_commit(smem_u32(&st.dfull[db]));
-          if (blk + 1 == b1) tc_commit(smem_u32(&st.pempty[pb]));
+          if (blk + 1 == b1) tc_commit(smem_u32(&st.pempty));
         }
-        last = n * 2 + db;
+        last_set = db;
+        last_use = n;
         __syncwarp();
       }
       ++pi;
     }
     // the last products have ended before TMEM is freed
-    if (last >= 0 && lane == 0) drain(&st.dfull[last & 1], (uint32_t)((last >> 1) & 1));
+    if (last_set >= 0 && lane == 0) drain(&st.dfull[last_set], (uint32_t)(last_use & 1));
     __syncwarp();
-  } else {
+  } else if (DROP && warp >= 12) {
+    // ---- masks, 16 bytes a row and block: thread i takes half a row
+    const Mask mask(p.rng, p.threshold);
+    const int id = tid - 384, row = id >> 1, half = id & 1;
+    int used[2] = {};
+    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      int4 tile;
+      int b0, b1;
+      if (!item(it, tile, b0, b1)) continue;
+      if (tile.x < 0) {
+        block += b1 - b0;
+        continue;
+      }
+      const int64_t t = row < tile.z ? p.plan.token(tile.y + row) : 0;
+      const uint64_t first = (uint64_t)(t * (p.d >> 3)) + half * 8;
+      for (int blk = b0; blk < b1; ++blk, ++block) {
+        const int set = block & 1, n = set ? used[1]++ : used[0]++, buf = set * 2 + (n & 1);
+        uint32_t bits[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 w = mask.words(first + blk * 16 + i);
+          const uint32_t v = (w.x & 0x00020001u) | (w.y & 0x00080004u) | (w.z & 0x00200010u) | (w.w & 0x00800040u);
+          bits[i >> 2] |= ((v | v >> 16) & 0xFFu) << (8 * (i & 3));
+        }
+        if (n >= 2) ok = wait(&st.abort, &st.mempty[buf], (uint32_t)((n / 2 - 1) & 1), p.plan.status, kRoleEmpty);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        reinterpret_cast<uint2 *>(st.masks[buf])[id] = make_uint2(bits[0], bits[1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&st.mfull[buf]));
+      }
+    }
+  } else if (warp >= 4) {
     // ---- accumulators onto the base rows
-    const int set = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const int set = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const int rq = lane >> 3, ch = lane & 7;   // four rows at once, eight chunks each
-    const Philox g(p.rng, p.threshold);
-    int block = 0, used = 0, sn = 0, pending = -1;   // used, sn: this set's accumulator and slabs so far
-    bool ok = true;
+    const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + set * kCols;
+    int used = 0, sn = 0, pending = -1;        // used, sn: this set's accumulator and slabs so far
     for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
       int4 tile;
       int b0, b1;
@@ -576,45 +630,46 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __gr
       const float f = p.factor * (live && p.scale != nullptr ? p.scale[tile.x] : 1.0f);
       for (int blk = b0; blk < b1; ++blk, ++block) {
         if ((block & 1) != set) continue;
+        uint4 bits = make_uint4(0, 0, 0, 0);
         if (live) {
           ok = __all_sync(0xffffffffu, wait(&st.abort, &st.dfull[set], (uint32_t)(used & 1), p.plan.status, kRoleDone));
           if (!ok) break;
+          if constexpr (DROP) {
+            const int buf = set * 2 + (used & 1);
+            ok = __all_sync(0xffffffffu, wait(&st.abort, &st.mfull[buf], (uint32_t)((used / 2) & 1), p.plan.status, kRoleReady));
+            if (!ok) break;
+            bits = st.masks[buf][row];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&st.mempty[buf]));
+          }
           tc_fence_after();
         }
 #pragma unroll 1
         for (int s = 0; s < SLABS; ++s, ++sn) {
           const int b = set * p.n_slab + sn % p.n_slab, c0 = blk * kCols + s * PER;
+          uint8_t *slab = slabs + b * 16384;
           ok = __all_sync(0xffffffffu, wait(&st.abort, &st.sfull[b], (uint32_t)((sn / p.n_slab) & 1), p.plan.status, kRoleSlab));
           if (!ok) break;
-          uint8_t *slab = slabs + b * 16384;
 #pragma unroll 1
           for (int h = 0; h < PER / 32; ++h) {
-            const int col = c0 + h * 32;
             float v[32];
-            if (live) tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + set * kCols + s * PER + h * 32, v);
+            if (live) tmem_ld32(acc + s * PER + h * 32, v);
+            if constexpr (DROP) {
+              const uint32_t m = bits.x;   // of these 32 columns
+              bits = make_uint4(bits.y, bits.z, bits.w, 0);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              if (live && p.threshold != 0) {
-                const uint4 w = g.block((uint64_t)(t * p.d + col + e) >> 3);
-                if (!g.kept<0>(w)) v[e] = 0.0f;
-                if (!g.kept<1>(w)) v[e + 1] = 0.0f;
-                if (!g.kept<2>(w)) v[e + 2] = 0.0f;
-                if (!g.kept<3>(w)) v[e + 3] = 0.0f;
-                if (!g.kept<4>(w)) v[e + 4] = 0.0f;
-                if (!g.kept<5>(w)) v[e + 5] = 0.0f;
-                if (!g.kept<6>(w)) v[e + 6] = 0.0f;
-                if (!g.kept<7>(w)) v[e + 7] = 0.0f;
-              }
+              for (int e = 0; e < 32; ++e)
+                if (!(m >> e & 1)) v[e] = 0.0f;
+            }
 #pragma unroll
-              for (int k = 0; k < 8; k += VN) {
-                TO *at = reinterpret_cast<TO *>(slab + swz(row, (h * 32 + e + k) / VN));
-                float o[VN] = {};
-                if (base != nullptr) load16<TO>(at, o);
-                if (live)
+            for (int e = 0; e < 32; e += VN) {
+              TO *at = reinterpret_cast<TO *>(slab + swz(row, (h * 32 + e) / VN));
+              float o[VN] = {};
+              if (base != nullptr) load16<TO>(at, o);
+              if (live)
 #pragma unroll
-                  for (int i = 0; i < VN; ++i) o[i] = fmaf(f, v[e + k + i], o[i]);
-                store16<TO>(at, o);
-              }
+                for (int i = 0; i < VN; ++i) o[i] = fmaf(f, v[e + i], o[i]);
+              store16<TO>(at, o);
             }
           }
           if (whole && c0 < p.d) {
@@ -633,6 +688,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __gr
             }
             pending = b;
           } else {
+            if (pending >= 0 && lane == 0) {
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              mbar_arrive(smem_u32(&st.sempty[pending]));
+            }
+            pending = -1;
             __syncwarp();
             const int cc = c0 + ch * VN;
 #pragma unroll
@@ -654,11 +714,6 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __gr
           if (lane == 0) mbar_arrive(smem_u32(&st.dempty[set]));
           ++used;
         }
-        if (pending >= 0 && lane == 0) {
-          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          mbar_arrive(smem_u32(&st.sempty[pending]));
-        }
-        pending = -1;
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -667,7 +722,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tc_kernel(const __gr
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_free(tmem, 256);
+  if (warp == 1) tmem_free(tmem, 2 * kCols);
 }
 
 // ---------------------------------------------------------------------------
@@ -690,11 +745,12 @@ struct WgradTc {
 };
 
 // ATOMS: 64-column boxes of the parts, three parts of up to ATOMS * 64 / 3 columns
-template <int ATOMS> struct WgradSize {
+template <int ATOMS, bool DROP> struct WgradSize {
   static constexpr int kStage = 16384 + 8192 * ATOMS;
-  static constexpr int kStages = ATOMS == 1 ? 4 : ATOMS == 2 ? 3 : ATOMS == 3 ? 5 : 3;   // two CTAs an SM, or one
+  static constexpr int kCtas = ATOMS == 1 ? (DROP ? 3 : 4) : ATOMS == 2 ? 3 : ATOMS == 3 ? 2 : 1;
+  static constexpr int kStages = ATOMS == 6 || (ATOMS == 1 && DROP) ? 3 : 2;
   static constexpr int kAccCols = ATOMS == 1 ? 64 : ATOMS == 2 ? 128 : ATOMS == 3 ? 256 : 512;
-  static constexpr int kAcc = ATOMS == 1 ? 4 : ATOMS <= 3 ? 2 : 1;
+  static constexpr int kAcc = ATOMS == 1 ? 2 : 1;
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
 };
 struct WgradShared {
@@ -705,8 +761,8 @@ struct WgradShared {
 };
 
 template <int ATOMS, bool DROP>
-__global__ void __launch_bounds__(DROP ? 320 : 192) wgrad_tc_kernel(const __grid_constant__ WgradTc p) {
-  using Z = WgradSize<ATOMS>;
+__global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCtas) wgrad_tc_kernel(const __grid_constant__ WgradTc p) {
+  using Z = WgradSize<ATOMS, DROP>;
   constexpr int NST = Z::kStages, WORK = DROP ? 256 : 128;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -724,8 +780,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192) wgrad_tc_kernel(const __grid
     fence_proxy_async();
   }
   pdl_wait();
-  if (blockIdx.y >= p.plan.chunks()) return;
-  const int4 ch = p.plan.chunk(blockIdx.y);
+  const int4 ch = p.plan.chunk_of(blockIdx.y);
   if (ch.z <= 0) return;
   // block by block in turn while both jobs have some
   const int both = min(p.blocks[0], p.blocks[1]), bx = (int)blockIdx.x;
@@ -819,15 +874,13 @@ __global__ void __launch_bounds__(DROP ? 320 : 192) wgrad_tc_kernel(const __grid
       if (!__all_sync(0xffffffffu, wait(&st.abort, &st.full[s], (uint32_t)((i / NST) & 1), p.plan.status, kRoleReady)))
         break;
       uint8_t *zs = smem + s * Z::kStage + (c >> 3) * 8192;
-      if (c0 + c * 8 < job.d)
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int64_t t = st.tok[s][r0 + 16 * h];   // -1: a row of zeros, which stays one
-          uint4 *at = reinterpret_cast<uint4 *>(zs + swz(r0 + 16 * h, c & 7));
-          uint4 w = *at;
-          mask.apply((uint64_t)(t * job.d + c0 + c * 8) >> 3, w);
-          *at = w;
-        }
+      for (int h = 0; h < 4; ++h) {
+        const int row = r0 + 16 * h;
+        const int64_t t = st.tok[s][row];   // -1: a row of zeros, which stays one
+        Mask::apply(reinterpret_cast<uint4 *>(zs + swz(row, c & 7)),
+                    mask.words((uint64_t)(t * (job.d >> 3) + (c0 >> 3) + c)));
+      }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&st.ready[s]));
@@ -912,7 +965,7 @@ void set_split(const AdapterArgs &a, ShrinkTc &p) {
 }
 
 template <int RPMAX, bool WT, bool DROP> cudaError_t shrink(const AdapterArgs &a, const ShrinkTc &p, cudaStream_t s) {
-  constexpr size_t smem = ShrinkSize<RPMAX, WT>::kSmem;
+  constexpr size_t smem = ShrinkSize<RPMAX, WT, DROP>::kSmem;
   cudaError_t e = allow(shrink_tc_kernel<RPMAX, WT, DROP>, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl_clusters(shrink_tc_kernel<RPMAX, WT, DROP>, dim3((unsigned)(host_tiles(a) * p.split)),
@@ -936,7 +989,7 @@ cudaError_t shrink(const AdapterArgs &a, ShrinkTc &p, const void *x, int64_t ld,
   return p.threshold != 0 ? shrink<WT, true>(a, p, s) : shrink<WT, false>(a, p, s);
 }
 
-constexpr int kExpandSmem = 222 * 1024;
+constexpr int kExpandSmem = 216 * 1024;
 // out [T, d] rows ld apart; V [n, d, rank], or [n, rank, d] (VT)
 template <typename TO, bool VT>
 cudaError_t expand(const AdapterArgs &a, ExpandTc &p, const bf16 *parts, const void *V, cudaStream_t s) {
@@ -947,10 +1000,10 @@ cudaError_t expand(const AdapterArgs &a, ExpandTc &p, const bf16 *parts, const v
   p.nparts = esize == 4 ? 3 : 2;
   p.p_bytes = (p.nparts * p.rp + 63) / 64 * 16384;
   p.v_bytes = VT ? p.rp * 256 : (p.rp + 63) / 64 * 16384;
-  p.n_p = p.p_bytes <= 32768 ? 2 : 1;
-  p.n_v = p.n_p * p.p_bytes + 2 * p.v_bytes + 4 * 16384 <= kExpandSmem ? 2 : 1;
-  p.n_slab = (kExpandSmem - p.n_p * p.p_bytes - p.n_v * p.v_bytes) / 32768;   // two at least: a slab is
-  if (p.n_slab > kMaxRing / 2) p.n_slab = kMaxRing / 2;                       // released by the next one's store
+  // two slabs a set at least: one is released by the next one's store
+  p.n_v = p.p_bytes + 2 * p.v_bytes + 4 * 16384 <= kExpandSmem ? 2 : 1;
+  const int slabs = (kExpandSmem - p.p_bytes - p.n_v * p.v_bytes) / 16384;
+  p.n_slab = (slabs < kMaxRing ? slabs : kMaxRing) / 2;
   // columns of an item: enough items for every SM to have several
   const int64_t tiles = host_tiles(a), blocks = (p.d + kCols - 1) / kCols, sms = sm_count();
   int64_t span = tiles * blocks / (8 * sms);
@@ -961,14 +1014,20 @@ cudaError_t expand(const AdapterArgs &a, ExpandTc &p, const bf16 *parts, const v
   if (e == cudaSuccess && p.base != nullptr) e = map2(&p.mb, p.base, esize, p.d, a.T, p.ld, kTileRows);
   if (e == cudaSuccess && p.base != nullptr) e = map2(&p.mb_row, p.base, esize, p.d, a.T, p.ld, 1);
   if (e == cudaSuccess) e = map2(&p.mo, p.out, esize, p.d, a.T, p.ld, 32);
-  if (e == cudaSuccess) e = allow(expand_tc_kernel<TO, VT>, kExpandSmem + 1024);
   if (e != cudaSuccess) return e;
-  return launch_pdl(expand_tc_kernel<TO, VT>, dim3((unsigned)(items < sms ? items : sms)), dim3(kExpandThreads),
-                    (size_t)kExpandSmem + 1024, s, p);
+  auto run = [&](auto kernel, int threads) {
+    const cudaError_t err = allow(kernel, kExpandSmem + 1024);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(kernel, dim3((unsigned)(items < sms ? items : sms)), dim3((unsigned)threads),
+                      (size_t)kExpandSmem + 1024, s, p);
+  };
+  if constexpr (VT)   // only the gradient passes a mask
+    if (p.threshold != 0) return run(expand_tc_kernel<TO, VT, true>, expand_threads<true>());
+  return run(expand_tc_kernel<TO, VT, false>, expand_threads<false>());
 }
 
 template <int ATOMS, bool DROP> cudaError_t wgrad(const AdapterArgs &a, const WgradTc &p, cudaStream_t s) {
-  constexpr size_t smem = WgradSize<ATOMS>::kSmem;
+  constexpr size_t smem = WgradSize<ATOMS, DROP>::kSmem;
   cudaError_t e = allow(wgrad_tc_kernel<ATOMS, DROP>, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(wgrad_tc_kernel<ATOMS, DROP>, dim3((unsigned)(p.blocks[0] + p.blocks[1]), (unsigned)host_chunks(a)),
