@@ -14,10 +14,10 @@
 // the product next to 2^-8 of the result). The products stay below the memory
 // time (rank 128: 1536 of 2700 clocks a 128 x 128 block).
 //
-// Rows of one tile may lie anywhere in the batch. Where they follow one another
-// (packed requests, one adapter) a TMA box fetches them at once, elsewhere
-// tile::gather4 four rows at a time; rows past the tile's end are row -1, which
-// the copy fills with zeros.
+// Rows of one tile may lie anywhere in the batch. Where 32 of them follow one
+// another (packed requests, one adapter) a TMA box fetches them at once,
+// elsewhere tile::gather4 four rows at a time, at half the rate (16384 x 6144 of
+// 32 adapters of rank 64: 131 us in boxes, 220 us with tokens in any order).
 #include "adapter.cuh"
 #include "tmap.cuh"
 
@@ -145,6 +145,31 @@ __device__ __forceinline__ void lane_tokens(const Plan &plan, int start, int fir
   for (int i = 0; i < 4; ++i) t[i] = first + i < rows ? (int)plan.token(start + first + i) : -1;
 }
 
+// How a warp fetches the rows of its lanes' tokens (four a lane): eight lanes,
+// 32 rows, by one box where they follow one another, else four rows a lane. Rows
+// past the end are not fetched, or (`zeros`) filled with zeros.
+struct RowCopy {
+  int issue;        // of this lane: 0 nothing, 1 a box, 2 its four rows
+  uint32_t bytes;   // of the warp
+};
+__device__ __forceinline__ RowCopy row_copy(const int (&t)[4], int lane, bool zeros, bool on) {
+  const int first = __shfl_sync(0xffffffffu, t[0], lane & 24), at = first + 4 * (lane & 7);
+  bool follows = first >= 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) follows = follows && (t[i] == at + i || (t[i] < 0 && !zeros));
+  const bool box = (__ballot_sync(0xffffffffu, follows) >> (lane & 24) & 0xffu) == 0xffu;
+  RowCopy r;
+  r.issue = !on ? 0 : box ? ((lane & 7) == 0 ? 1 : 0) : (zeros || t[0] >= 0) ? 2 : 0;
+  r.bytes = __reduce_add_sync(0xffffffffu, r.issue == 1 ? 4096u : r.issue == 2 ? 512u : 0u);
+  return r;
+}
+// rows of 128 bytes from dst on
+__device__ __forceinline__ void copy_rows(const RowCopy &r, uint32_t dst, const CUtensorMap *box, const CUtensorMap *row,
+                                          uint64_t *bar, int col, const int (&t)[4], int lane) {
+  if (r.issue == 1) tma_load_2d(dst + (lane >> 3) * 4096, box, smem_u32(bar), col, t[0]);
+  else if (r.issue == 2) tma_gather4(dst + lane * 512, row, bar, col, t);
+}
+
 // ---------------------------------------------------------------------------
 // Shrink. A cluster of `split` CTAs takes a tile; each runs through a part of
 // the width, the fp32 sums meet in shared memory and every CTA finishes a part
@@ -154,7 +179,7 @@ __device__ __forceinline__ void lane_tokens(const Plan &plan, int start, int fir
 // The steps of K take turns over several accumulators, which are added at the
 // end: the tensor core truncates each addition, and a short chain loses less.
 struct ShrinkTc {
-  CUtensorMap mx, mx_row, mw;   // x in boxes of 128 rows and of one; W [n, rank, d] or [n, d, rank]
+  CUtensorMap mx, mx_row, mw;   // x in boxes of 32 rows and of one; W [n, rank, d] or [n, d, rank]
   Plan plan;
   int d, rank, rp;              // rp: padded_rank
   int split, per;               // CTAs a tile, 64-column steps a CTA
@@ -226,13 +251,11 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP>:
   const int k0 = q * p.per, all = (p.d + 63) / 64, steps = max(0, min(p.per, all - k0));
 
   if (warp == 0) {
-    const int row0 = st.tok[0];
-    // ascending inside an adapter, so the ends tell
-    const bool run = tile.z > 0 && st.tok[tile.z - 1] - row0 == tile.z - 1;
     int t[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) t[i] = st.tok[4 * lane + i];
-    const uint32_t bytes = 16384 + (WT ? 8192 * ((p.rp + 63) / 64) : p.rp * 128);
+    const RowCopy rows = row_copy(t, lane, false, true);
+    const uint32_t bytes = rows.bytes + (WT ? 8192 * ((p.rp + 63) / 64) : p.rp * 128);
     int i = 0;
     for (; i < steps; ++i) {
       const int s = i % NST;
@@ -243,7 +266,6 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP>:
       const int k = (k0 + i) * 64;
       if (lane == 0) {
         mbar_expect_tx(smem_u32(&st.full[s]), bytes);
-        if (run) tma_load_2d(xs, &p.mx, smem_u32(&st.full[s]), k, row0);
         if constexpr (WT) {
           for (int b = 0; b * 64 < p.rp; ++b) tma_load_3d(ws + b * 8192, &p.mw, &st.full[s], b * 64, k, tile.x);
         } else {
@@ -251,7 +273,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP>:
         }
       }
       __syncwarp();
-      if (!run) tma_gather4(xs + lane * 512, &p.mx_row, &st.full[s], k, t);
+      copy_rows(rows, xs, &p.mx, &p.mx_row, &st.full[s], k, t, lane);
     }
     if (lane == 0)
       for (int s = 0; s < NST && s < i; ++s) drain(&st.full[s], (uint32_t)(((i - 1 - s) / NST) & 1));
@@ -377,22 +399,22 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP>:
 }
 
 // ---------------------------------------------------------------------------
-// Expand. One CTA an SM runs through items: a tile and up to `span` blocks of
-// 128 columns. Base rows come by TMA into slabs of 128 rows x 128 bytes, the
-// product of a block into the accumulator of one of two sets of four warps,
-// which take the blocks in turn: a thread adds its row of the accumulator to its
-// row of the slab, and the slab leaves by TMA, or row by row where the tile's
-// rows do not follow one another. Each set has a ring of slabs of its own, so
-// that it sees every phase of the barriers it waits on. With dropout eight more
+// Expand. One CTA an SM runs through an equal share of all tiles' blocks of 128
+// columns, tile after tile. Base rows come by TMA into slabs of 128 rows x 128
+// bytes, the product of a block into one of two accumulators of one of two sets
+// of four warps, which take the blocks in turn: a thread adds its row of the
+// accumulator to its row of the slab, and the slab leaves by TMA, or row by row
+// where the tile's rows do not follow one another. Each set has a ring of slabs
+// of its own, so that it sees every phase of the barriers it waits on. With dropout eight more
 // warps make the masks ahead, a bit an element: made by the sets themselves
 // they kept the slabs waiting (32768 x 8192, rank 16: 355 us).
 struct ExpandTc {
-  CUtensorMap mp, mv, mb, mb_row, mo;   // parts, V [n, d, rank] or [n, rank, d], base (128 rows; one), out (32 rows)
+  CUtensorMap mp, mv, mb, mb_row, mo;   // parts, V [n, d, rank] or [n, rank, d], base (32 rows; one), out (32 rows)
   Plan plan;
   const void *base;
   void *out;
   int64_t ld;
-  int d, rank, rp, nparts, span;
+  int d, rank, rp, nparts;
   int p_bytes, v_bytes, n_v, n_slab;    // shared memory: parts, V and how many of them, slabs of a set
   uint32_t threshold;
   const uint64_t *rng;
@@ -404,7 +426,7 @@ struct ExpandTc {
 template <bool DROP> constexpr int expand_threads() { return DROP ? 640 : 384; }
 
 struct ExpandShared {
-  uint64_t pfull, pempty, vfull[2], vempty[2], sfull[kMaxRing], sempty[kMaxRing], dfull[2], dempty[2];
+  uint64_t pfull, pempty, vfull[2], vempty[2], sfull[kMaxRing], sempty[kMaxRing], dfull[4], dempty[4];
   uint64_t mfull[4], mempty[4];     // masks: two buffers of each set
   uint32_t tmem;
   volatile int abort;
@@ -426,10 +448,10 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&st.vfull[i]), 1);
       mbar_init(smem_u32(&st.vempty[i]), 1);
-      mbar_init(smem_u32(&st.dfull[i]), 1);
-      mbar_init(smem_u32(&st.dempty[i]), 4);
     }
     for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&st.dfull[i]), 1);
+      mbar_init(smem_u32(&st.dempty[i]), 4);
       mbar_init(smem_u32(&st.mfull[i]), 8);
       mbar_init(smem_u32(&st.mempty[i]), 4);
     }
@@ -440,7 +462,7 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async();
   }
-  if (warp == 1) tmem_alloc(&st.tmem, 2 * kCols);
+  if (warp == 1) tmem_alloc(&st.tmem, 4 * kCols);
   pdl_wait();
   tc_fence_before();
   __syncthreads();
@@ -448,13 +470,16 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
   const uint32_t tmem = st.tmem;
   const TO *base = static_cast<const TO *>(p.base);
   TO *out = static_cast<TO *>(p.out);
-  const int blocks = (p.d + kCols - 1) / kCols, groups = (blocks + p.span - 1) / p.span;
-  const int64_t items = p.plan.tiles() * groups;
-  // The same walk for every role: items of tiles that have something to write.
-  auto item = [&](int64_t it, int4 &tile, int &b0, int &b1) {
-    tile = p.plan.tile(it / groups);
-    b0 = (int)(it % groups) * p.span;
-    b1 = min(blocks, b0 + p.span);
+  const int blocks = (p.d + kCols - 1) / kCols;
+  const int64_t all = p.plan.tiles() * blocks, end = all * (blockIdx.x + 1) / gridDim.x;
+  // The same walk for every role: from block `at` of all on, the tile and its
+  // blocks b0 .. b1 of this CTA; false for a tile with nothing to write.
+  const int64_t begin = all * blockIdx.x / gridDim.x;
+  auto item = [&](int64_t &at, int4 &tile, int &b0, int &b1) {
+    tile = p.plan.tile(at / blocks);
+    b0 = (int)(at % blocks);
+    b1 = (int)(end - at < blocks - b0 ? b0 + (end - at) : blocks);
+    at += b1 - b0;
     return tile.z > 0 && (tile.x >= 0 || base != out);
   };
   bool ok = true;
@@ -463,14 +488,13 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
   if (warp == 0) {
     // ---- base rows
     int fetched[2] = {};   // slabs of each set
-    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+    for (int64_t at = begin; at < end && ok;) {
       int4 tile;
       int b0, b1;
-      if (!item(it, tile, b0, b1)) continue;
+      if (!item(at, tile, b0, b1)) continue;
       int t[4];
       lane_tokens(p.plan, tile.y, 4 * lane, tile.z, t);
-      const int row0 = __shfl_sync(0xffffffffu, t[0], 0);
-      const bool run = (int)p.plan.token(tile.y + tile.z - 1) - row0 == tile.z - 1;
+      const RowCopy rows = row_copy(t, lane, false, true);
       for (int blk = b0; blk < b1 && ok; ++blk, ++block) {
         const int set = block & 1;
         for (int s = 0; s < SLABS; ++s) {
@@ -482,12 +506,9 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
             if (lane == 0) mbar_arrive(smem_u32(&st.sfull[b]));
           } else {
             const uint32_t dst = smem_u32(slabs + b * 16384);
-            if (lane == 0) {
-              mbar_expect_tx(smem_u32(&st.sfull[b]), 16384);
-              if (run) tma_load_2d(dst, &p.mb, smem_u32(&st.sfull[b]), c, row0);
-            }
+            if (lane == 0) mbar_expect_tx(smem_u32(&st.sfull[b]), rows.bytes);
             __syncwarp();
-            if (!run) tma_gather4(dst + lane * 512, &p.mb_row, &st.sfull[b], c, t);
+            copy_rows(rows, dst, &p.mb, &p.mb_row, &st.sfull[b], c, t, lane);
           }
           if (set) fetched[1] = n + 1;
           else fetched[0] = n + 1;
@@ -504,10 +525,10 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
   } else if (warp == 2) {
     // ---- parts and V
     int pi = 0, vi = 0;
-    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+    for (int64_t at = begin; at < end && ok;) {
       int4 tile;
       int b0, b1;
-      if (!item(it, tile, b0, b1) || tile.x < 0) continue;
+      if (!item(at, tile, b0, b1) || tile.x < 0) continue;
       if (pi > 0) ok = wait(&st.abort, &st.pempty, (uint32_t)((pi - 1) & 1), p.plan.status, kRoleEmpty);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       if (lane == 0) {
@@ -541,18 +562,19 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
   } else if (warp == 1) {
     // ---- products
     const uint32_t idesc = instr_desc(128, kCols, 0, VT ? 1 : 0);
-    int pi = 0, vi = 0, last_set = -1, last_use = 0, used[2] = {};   // used: uses of each accumulator so far
-    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+    int pi = 0, vi = 0, last_acc = -1, last_use = 0, used[2] = {};   // used: products of each set so far
+    for (int64_t at = begin; at < end && ok;) {
       int4 tile;
       int b0, b1;
-      if (!item(it, tile, b0, b1)) continue;
+      if (!item(at, tile, b0, b1)) continue;
       if (tile.x < 0) {
         block += b1 - b0;
         continue;
       }
       ok = wait(&st.abort, &st.pfull, (uint32_t)(pi & 1), p.plan.status, kRoleFull);
       for (int blk = b0; blk < b1; ++blk, ++vi, ++block) {
-        const int vb = vi % p.n_v, db = block & 1, n = db ? used[1]++ : used[0]++;
+        // a set's products take turns over its two accumulators
+        const int vb = vi % p.n_v, set = block & 1, m = set ? used[1]++ : used[0]++, db = set * 2 + (m & 1), n = m >> 1;
         if (ok) ok = wait(&st.abort, &st.vfull[vb], (uint32_t)((vi / p.n_v) & 1), p.plan.status, kRoleFull);
         if (ok && n > 0) ok = wait(&st.abort, &st.dempty[db], (uint32_t)((n - 1) & 1), p.plan.status, kRoleAcc);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -572,24 +594,24 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
           tc_commit(smem_u32(&st.dfull[db]));
           if (blk + 1 == b1) tc_commit(smem_u32(&st.pempty));
         }
-        last_set = db;
+        last_acc = db;
         last_use = n;
         __syncwarp();
       }
       ++pi;
     }
     // the last products have ended before TMEM is freed
-    if (last_set >= 0 && lane == 0) drain(&st.dfull[last_set], (uint32_t)(last_use & 1));
+    if (last_acc >= 0 && lane == 0) drain(&st.dfull[last_acc], (uint32_t)(last_use & 1));
     __syncwarp();
   } else if (DROP && warp >= 12) {
     // ---- masks, 16 bytes a row and block: thread i takes half a row
     const Mask mask(p.rng, p.threshold);
     const int id = tid - 384, row = id >> 1, half = id & 1;
     int used[2] = {};
-    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+    for (int64_t at = begin; at < end && ok;) {
       int4 tile;
       int b0, b1;
-      if (!item(it, tile, b0, b1)) continue;
+      if (!item(at, tile, b0, b1)) continue;
       if (tile.x < 0) {
         block += b1 - b0;
         continue;
@@ -616,23 +638,23 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
     // ---- accumulators onto the base rows
     const int set = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const int rq = lane >> 3, ch = lane & 7;   // four rows at once, eight chunks each
-    const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + set * kCols;
     int used = 0, sn = 0, pending = -1;        // used, sn: this set's accumulator and slabs so far
-    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+    for (int64_t at = begin; at < end && ok;) {
       int4 tile;
       int b0, b1;
-      if (!item(it, tile, b0, b1)) continue;
+      if (!item(at, tile, b0, b1)) continue;
       const bool live = tile.x >= 0;
       const int64_t t = row < tile.z ? p.plan.token(tile.y + row) : -1;
-      const int64_t first = p.plan.token(tile.y);
-      const bool run = p.plan.token(tile.y + tile.z - 1) - first == tile.z - 1;
-      const bool whole = run && quarter * 32 + 32 <= tile.z;   // this warp's 32 rows leave at once
+      const int first = __shfl_sync(0xffffffffu, (int)t, 0);
+      const bool whole = __all_sync(0xffffffffu, t >= 0 && t == first + lane);   // this warp's 32 rows leave at once
       const float f = p.factor * (live && p.scale != nullptr ? p.scale[tile.x] : 1.0f);
       for (int blk = b0; blk < b1; ++blk, ++block) {
         if ((block & 1) != set) continue;
         uint4 bits = make_uint4(0, 0, 0, 0);
+        const int db = set * 2 + (used & 1);
+        const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + db * kCols;
         if (live) {
-          ok = __all_sync(0xffffffffu, wait(&st.abort, &st.dfull[set], (uint32_t)(used & 1), p.plan.status, kRoleDone));
+          ok = __all_sync(0xffffffffu, wait(&st.abort, &st.dfull[db], (uint32_t)((used >> 1) & 1), p.plan.status, kRoleDone));
           if (!ok) break;
           if constexpr (DROP) {
             const int buf = set * 2 + (used & 1);
@@ -678,7 +700,7 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
             if (lane == 0) {
               asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                                reinterpret_cast<uint64_t>(&p.mo)),
-                           "r"(smem_u32(slab) + quarter * 4096), "r"(c0), "r"((int)first + quarter * 32)
+                           "r"(smem_u32(slab) + quarter * 4096), "r"(c0), "r"(first)
                            : "memory");
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
               if (pending >= 0) {   // the slab before this one has been read
@@ -711,7 +733,7 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
         if (live) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&st.dempty[set]));
+          if (lane == 0) mbar_arrive(smem_u32(&st.dempty[db]));
           ++used;
         }
       }
@@ -722,7 +744,7 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_free(tmem, 2 * kCols);
+  if (warp == 1) tmem_free(tmem, 4 * kCols);
 }
 
 // ---------------------------------------------------------------------------
@@ -730,7 +752,7 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
 // tokens, 64 a step: both operands have the tokens (K) as rows. The two
 // gradients of a backward are two jobs of one launch, block by block in turn.
 struct WgradJob {
-  CUtensorMap mz, mz_row, mp, mp_row;   // [.., d] by token and parts by position: 64 rows, one row
+  CUtensorMap mz, mz_row, mp, mp_row;   // [.., d] by token (32 rows; one), parts by position (64 rows; one)
   int d, transposed;                    // out [n, d, rank] instead of [n, rank, d]
   uint32_t threshold;
   const float *scale;
@@ -754,7 +776,7 @@ template <int ATOMS, bool DROP> struct WgradSize {
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
 };
 struct WgradShared {
-  uint64_t full[kMaxRing], ready[kMaxRing], empty[kMaxRing], done;
+  uint64_t full[kMaxRing], ready[kMaxRing], empty[kMaxRing], known[kMaxRing], done;   // known: a stage's tokens
   uint32_t tmem;
   volatile int abort;
   int tok[kMaxRing][64];
@@ -774,6 +796,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
       mbar_init(smem_u32(&st.full[s]), 1);
       mbar_init(smem_u32(&st.ready[s]), WORK / 32);
       mbar_init(smem_u32(&st.empty[s]), 1);
+      mbar_init(smem_u32(&st.known[s]), 1);
     }
     mbar_init(smem_u32(&st.done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -796,15 +819,13 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
   const int steps = (ch.z + 63) / 64;
 
   if (warp == 0) {
-    const uint32_t bytes = 16384 + 8192 * ATOMS;
     int t[4], pos[4];
     lane_tokens(p.plan, ch.y, 4 * lane, lane < 16 ? ch.z : 0, t);
     int i = 0;
     for (; i < steps; ++i) {
       const int s = i % NST, r0 = i * 64;
       const bool full = r0 + 64 <= ch.z;
-      const int first = __shfl_sync(0xffffffffu, t[0], 0), last = __shfl_sync(0xffffffffu, t[3], 15);
-      const bool run = full && last - first == 63;
+      const RowCopy rows = row_copy(t, lane, true, lane < 16);   // rows past the chunk's end count as zeros
       bool ok = true;
       if (i >= NST) ok = wait(&st.abort, &st.empty[s], (uint32_t)((i / NST - 1) & 1), p.plan.status, kRoleEmpty);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -816,25 +837,18 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
       __syncwarp();
       const uint32_t zs = smem_u32(smem + s * Z::kStage), ps = zs + 16384;
       if (lane == 0) {
-        mbar_expect_tx(smem_u32(&st.full[s]), bytes);
-        if (run) {
-          tma_load_2d(zs, &job.mz, smem_u32(&st.full[s]), c0, first);
-          tma_load_2d(zs + 8192, &job.mz, smem_u32(&st.full[s]), c0 + 64, first);
-        }
+        if (drops) mbar_arrive(smem_u32(&st.known[s]));
+        mbar_expect_tx(smem_u32(&st.full[s]), 2 * rows.bytes + 8192 * ATOMS);
         if (full)
 #pragma unroll
           for (int b = 0; b < ATOMS; ++b) tma_load_2d(ps + b * 8192, &job.mp, smem_u32(&st.full[s]), b * 64, ch.y + r0);
       }
       __syncwarp();
-      if (lane < 16) {
-        if (!run) {
-          tma_gather4(zs + lane * 512, &job.mz_row, &st.full[s], c0, t);
-          tma_gather4(zs + 8192 + lane * 512, &job.mz_row, &st.full[s], c0 + 64, t);
-        }
-        if (!full)
+      copy_rows(rows, zs, &job.mz, &job.mz_row, &st.full[s], c0, t, lane);
+      copy_rows(rows, zs + 8192, &job.mz, &job.mz_row, &st.full[s], c0 + 64, t, lane);
+      if (lane < 16 && !full)
 #pragma unroll
-          for (int b = 0; b < ATOMS; ++b) tma_gather4(ps + b * 8192 + lane * 512, &job.mp_row, &st.full[s], b * 64, pos);
-      }
+        for (int b = 0; b < ATOMS; ++b) tma_gather4(ps + b * 8192 + lane * 512, &job.mp_row, &st.full[s], b * 64, pos);
       if (i + 1 < steps) lane_tokens(p.plan, ch.y, r0 + 64 + 4 * lane, lane < 16 ? ch.z : 0, t);
     }
     if (lane == 0)
@@ -871,16 +885,18 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
     const Mask mask(p.rng, job.threshold);
     for (int i = 0; i < steps; ++i) {
       const int s = i % NST;
-      if (!__all_sync(0xffffffffu, wait(&st.abort, &st.full[s], (uint32_t)((i / NST) & 1), p.plan.status, kRoleReady)))
-        break;
-      uint8_t *zs = smem + s * Z::kStage + (c >> 3) * 8192;
+      const uint32_t phase = (uint32_t)((i / NST) & 1);
+      if (!__all_sync(0xffffffffu, wait(&st.abort, &st.known[s], phase, p.plan.status, kRoleReady))) break;
+      uint4 m[4];   // while the stage is on its way
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        const int row = r0 + 16 * h;
-        const int64_t t = st.tok[s][row];   // -1: a row of zeros, which stays one
-        Mask::apply(reinterpret_cast<uint4 *>(zs + swz(row, c & 7)),
-                    mask.words((uint64_t)(t * (job.d >> 3) + (c0 >> 3) + c)));
+        const int64_t t = st.tok[s][r0 + 16 * h];   // -1: a row of zeros, which stays one
+        m[h] = mask.words((uint64_t)(t * (job.d >> 3) + (c0 >> 3) + c));
       }
+      if (!__all_sync(0xffffffffu, wait(&st.abort, &st.full[s], phase, p.plan.status, kRoleReady))) break;
+      uint8_t *zs = smem + s * Z::kStage + (c >> 3) * 8192;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) Mask::apply(reinterpret_cast<uint4 *>(zs + swz(r0 + 16 * h, c & 7)), m[h]);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&st.ready[s]));
@@ -982,7 +998,7 @@ cudaError_t shrink(const AdapterArgs &a, ShrinkTc &p, const void *x, int64_t ld,
   p.rank = a.rank;
   p.rp = padded_rank(a.rank);
   set_split(a, p);
-  cudaError_t e = map2(&p.mx, x, 2, p.d, a.T, ld, kTileRows);
+  cudaError_t e = map2(&p.mx, x, 2, p.d, a.T, ld, 32);
   if (e == cudaSuccess) e = map2(&p.mx_row, x, 2, p.d, a.T, ld, 1);
   if (e == cudaSuccess) e = WT ? map3(&p.mw, W, p.rank, p.d, a.n, 64) : map3(&p.mw, W, p.d, p.rank, a.n, p.rp);
   if (e != cudaSuccess) return e;
@@ -1004,21 +1020,17 @@ cudaError_t expand(const AdapterArgs &a, ExpandTc &p, const bf16 *parts, const v
   p.n_v = p.p_bytes + 2 * p.v_bytes + 4 * 16384 <= kExpandSmem ? 2 : 1;
   const int slabs = (kExpandSmem - p.p_bytes - p.n_v * p.v_bytes) / 16384;
   p.n_slab = (slabs < kMaxRing ? slabs : kMaxRing) / 2;
-  // columns of an item: enough items for every SM to have several
-  const int64_t tiles = host_tiles(a), blocks = (p.d + kCols - 1) / kCols, sms = sm_count();
-  int64_t span = tiles * blocks / (8 * sms);
-  p.span = (int)(span < 1 ? 1 : span > 16 ? 16 : span);
-  const int64_t items = tiles * ((blocks + p.span - 1) / p.span);
+  const int64_t all = host_tiles(a) * ((p.d + kCols - 1) / kCols), sms = sm_count();
   cudaError_t e = map2(&p.mp, parts, 2, 3 * p.rp, a.T, 3 * p.rp, kTileRows);
   if (e == cudaSuccess) e = VT ? map3(&p.mv, V, p.d, p.rank, a.n, p.rp) : map3(&p.mv, V, p.rank, p.d, a.n, kCols);
-  if (e == cudaSuccess && p.base != nullptr) e = map2(&p.mb, p.base, esize, p.d, a.T, p.ld, kTileRows);
+  if (e == cudaSuccess && p.base != nullptr) e = map2(&p.mb, p.base, esize, p.d, a.T, p.ld, 32);
   if (e == cudaSuccess && p.base != nullptr) e = map2(&p.mb_row, p.base, esize, p.d, a.T, p.ld, 1);
   if (e == cudaSuccess) e = map2(&p.mo, p.out, esize, p.d, a.T, p.ld, 32);
   if (e != cudaSuccess) return e;
   auto run = [&](auto kernel, int threads) {
     const cudaError_t err = allow(kernel, kExpandSmem + 1024);
     if (err != cudaSuccess) return err;
-    return launch_pdl(kernel, dim3((unsigned)(items < sms ? items : sms)), dim3((unsigned)threads),
+    return launch_pdl(kernel, dim3((unsigned)(all < sms ? all : sms)), dim3((unsigned)threads),
                       (size_t)kExpandSmem + 1024, s, p);
   };
   if constexpr (VT)   // only the gradient passes a mask
@@ -1046,7 +1058,7 @@ cudaError_t wgrad(const AdapterArgs &a, const bf16 *u, const bf16 *du, cudaStrea
     w.d = d;
     w.out = out;
     w.partial = reinterpret_cast<float *>(a.ws + partial);
-    cudaError_t e = map2(&w.mz, z, 2, d, a.T, ld, 64);
+    cudaError_t e = map2(&w.mz, z, 2, d, a.T, ld, 32);
     if (e == cudaSuccess) e = map2(&w.mz_row, z, 2, d, a.T, ld, 1);
     if (e == cudaSuccess) e = map2(&w.mp, parts, 2, 3 * p.rp, a.T, 3 * p.rp, 64);
     if (e == cudaSuccess) e = map2(&w.mp_row, parts, 2, 3 * p.rp, a.T, 3 * p.rp, 1);
