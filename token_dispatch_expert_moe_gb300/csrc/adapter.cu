@@ -16,19 +16,30 @@ size_t adapter_scratch_bytes(int64_t T, int d_in, int d_out, int rank) {
 }
 size_t adapter_map_bytes(int64_t T, int n) { return (size_t)map_layout(T, n).words * 4; }
 
-// Row by row every token reads its adapter (rank * (d_in + d_out) elements)
-// from L2; by tiles one reading serves up to 128 tokens, after a map.
-bool adapter_rowwise(int64_t T, int, int, int, int) { return T <= 64; }
+// Row by row every token reads its adapter (rank (d_in + d_out) elements) from
+// L2, at 6.5 MB/us measured; by tiles there are a map and two more kernels (17 us
+// for the smallest batch) and half a microsecond a tile, of up to 128 tokens of
+// one adapter each: measured at 6144 and rank 16, 256 tokens of 64 adapters 19
+// us by rows and 53 us by tiles, 1021 x 3584 to 5120 of 12 adapters of rank 24
+// 54 us by rows and 30 us by tiles.
+bool adapter_rowwise(int64_t T, int d_in, int d_out, int n, int rank, int dtype) {
+  const double bytes = (double)T * rank * ((double)d_in + d_out) * (dtype == MOE_BF16 ? 2 : 4);
+  const double tiles = (double)(T / kTileRows) + (double)(n < T ? n : T);
+  return bytes / 6.5e6 < 17.0 + 0.5 * tiles;
+}
 
 namespace {
 
 // ---------------------------------------------------------------------------
 // The map: a stable counting sort by adapter in one launch. A cluster of CTAs
 // cuts the tokens into one run per warp; every warp counts its run, the counts
-// are added up over warps and CTAs, and every warp places its run.
+// are added up over warps and CTAs, and every warp places its run. Bound by the
+// latency of its steps: the tokens of a run stay in registers, one CTA without a
+// cluster serves up to 4096 of them.
 constexpr int kMapThreads = 1024;
 constexpr int kMapCtas = 8;
 constexpr size_t kMapSmem = 220 * 1024;
+constexpr int kMapKept = 4;   // indices a lane keeps
 
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
@@ -48,13 +59,13 @@ __device__ __forceinline__ int find_bin(const int *first, int bins, int i) {
 
 __global__ void __launch_bounds__(kMapThreads) map_kernel(int64_t T, int n, int runs, const int32_t *adapter_of,
                                                           int32_t *map, uint32_t *status) {
-  pdl_wait();
   extern __shared__ int sm[];
   const int bins = n + 1;   // the last: no adapter
   int *hist = sm;                    // [runs][bins]
   int *total = hist + runs * bins;   // of this CTA
   int *all = total + bins;
-  int *off = all + bins;
+  int *prior = all + bins;           // of the CTAs before this one
+  int *off = prior + bins;
   int *tile0 = off + bins, *chunk0 = tile0 + bins, *slot0 = chunk0 + bins;
   __shared__ int4 warp_sums[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -64,34 +75,51 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(int64_t T, int n, int 
   const int64_t C = chunk_rows(T);
 
   for (int i = tid; i < runs * bins; i += kMapThreads) hist[i] = 0;
+  pdl_wait();
+  // the bin of token t; -1 past the run
+  auto bin = [&](int64_t t) {
+    if (t >= hi) return -1;
+    int e = adapter_of[t];
+    if (e < -1 || e >= n) report(status, MOE_ERR_DEVICE, kInfoAdapterRange);
+    return e < 0 || e >= n ? n : e;
+  };
+  const bool kept = len <= 32 * kMapKept;
+  int mine[kMapKept];
+#pragma unroll
+  for (int k = 0; k < kMapKept; ++k) mine[k] = warp < runs && kept ? bin(lo + 32 * k + lane) : -1;
   __syncthreads();
-  if (warp < runs)
-    for (int64_t t = lo + lane; t < hi; t += 32) {
-      int e = adapter_of[t];
-      if (e < -1 || e >= n) report(status, MOE_ERR_DEVICE, kInfoAdapterRange);
-      if (e < 0 || e >= n) e = n;
-      atomicAdd(&hist[warp * bins + e], 1);
+  if (warp < runs) {
+    if (kept) {
+#pragma unroll
+      for (int k = 0; k < kMapKept; ++k)
+        if (mine[k] >= 0) atomicAdd(&hist[warp * bins + mine[k]], 1);
+    } else {
+      for (int64_t t = lo + lane; t < hi; t += 32) atomicAdd(&hist[warp * bins + bin(t)], 1);
     }
-  __syncthreads();
-  for (int e = tid; e < bins; e += kMapThreads) {
-    int sum = 0;
-    for (int w = 0; w < runs; ++w) {
-      const int c = hist[w * bins + e];
-      hist[w * bins + e] = sum;
-      sum += c;
-    }
-    total[e] = sum;
   }
-  cluster_sync();
+  __syncthreads();
+  for (int e = warp; e < bins; e += kMapThreads / 32) {   // a bin a warp, a run a lane
+    const int c = lane < runs ? hist[lane * bins + e] : 0;
+    int sum = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane < runs) hist[lane * bins + e] = sum - c;
+    if (lane == 31) total[e] = sum;
+  }
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
   for (int e = tid; e < bins; e += kMapThreads) {
     int before = 0, sum = 0;
     for (int r = 0; r < ctas; ++r) {
-      const int c = remote_int(&total[e], (uint32_t)r);
+      const int c = ctas > 1 ? remote_int(&total[e], (uint32_t)r) : total[e];
       if (r < me) before += c;
       sum += c;
     }
     all[e] = sum;
-    for (int w = 0; w < runs; ++w) hist[w * bins + e] += before;
+    prior[e] = before;
   }
   __syncthreads();
   // exclusive sums over the bins of tokens, tiles, chunks and slots
@@ -102,12 +130,12 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(int64_t T, int n, int 
     const int k = e < n ? (int)((c + C - 1) / C) : 0;
     return make_int4(c, (c + kTileRows - 1) / kTileRows, k, k > 1 ? k : 0);
   };
-  int4 mine = make_int4(0, 0, 0, 0);
+  int4 own = make_int4(0, 0, 0, 0);
   for (int e = e0; e < e1; ++e) {
     const int4 c = counts(e);
-    mine.x += c.x; mine.y += c.y; mine.z += c.z; mine.w += c.w;
+    own.x += c.x; own.y += c.y; own.z += c.z; own.w += c.w;
   }
-  int4 inc = mine;
+  int4 inc = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
@@ -116,9 +144,9 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(int64_t T, int n, int 
   }
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  int4 run = make_int4(inc.x - mine.x, inc.y - mine.y, inc.z - mine.z, inc.w - mine.w);
+  int4 run = make_int4(inc.x - own.x, inc.y - own.y, inc.z - own.z, inc.w - own.w);
   int4 sums = make_int4(0, 0, 0, 0);
-  for (int w = 0; w < 32; ++w) {
+  for (int w = 0; w < (bins + 32 * per - 1) / (32 * per); ++w) {   // the warps with bins
     const int4 v = warp_sums[w];
     if (w < warp) { run.x += v.x; run.y += v.y; run.z += v.z; run.w += v.w; }
     sums.y += v.y;
@@ -131,22 +159,27 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(int64_t T, int n, int 
   }
   __syncthreads();
 
-  if (warp < runs)
-    for (int64_t t0 = lo; t0 < hi; t0 += 32) {
-      const int64_t t = t0 + lane;
-      int e = t < hi ? adapter_of[t] : -2;
-      if (t < hi && (e < 0 || e >= n)) e = n;
+  if (warp < runs) {
+    auto place = [&](int64_t t, int e) {
       const uint32_t same = __match_any_sync(0xffffffffu, e);
       const int rank = __popc(same & ((1u << lane) - 1u));
       int at = 0;
-      if (t < hi) {
+      if (e >= 0) {
         at = hist[warp * bins + e];
-        map[kMapHeader + off[e] + at + rank] = (int32_t)t;
+        map[kMapHeader + off[e] + prior[e] + at + rank] = (int32_t)t;
       }
       __syncwarp();
-      if (t < hi && rank == 0) hist[warp * bins + e] = at + __popc(same);
+      if (e >= 0 && rank == 0) hist[warp * bins + e] = at + __popc(same);
       __syncwarp();
+    };
+    if (kept) {
+#pragma unroll
+      for (int k = 0; k < kMapKept; ++k)
+        if (lo + 32 * k < hi) place(lo + 32 * k + lane, mine[k]);
+    } else {
+      for (int64_t t0 = lo; t0 < hi; t0 += 32) place(t0 + lane, bin(t0 + lane));
     }
+  }
   const MapLayout m = map_layout(T, n);
   int4 *tiles = reinterpret_cast<int4 *>(map + m.tiles), *chunks = reinterpret_cast<int4 *>(map + m.chunks);
   int2 *groups = reinterpret_cast<int2 *>(map + m.groups);
@@ -167,7 +200,7 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(int64_t T, int n, int 
     map[kMapTiles] = sums.y;
     map[kMapChunks] = sums.z;
   }
-  cluster_sync();   // no CTA leaves while another reads its counts
+  if (ctas > 1) cluster_sync();   // no CTA leaves while another reads its counts
 }
 
 // ---------------------------------------------------------------------------
@@ -205,11 +238,13 @@ __device__ __forceinline__ void mask4(const Philox &g, int64_t i, float (&v)[4])
 
 // ---------------------------------------------------------------------------
 // Row by row: a cluster of 8 CTAs a token. Every CTA takes a part of d_in for u,
-// the parts meet in shared memory, and every CTA takes a part of d_out for y.
+// the parts meet in shared memory, and every CTA takes a part of d_out for y. Bound by
+// latency for few tokens, by L2 from some hundreds on (0.4 MB a token at 6144 and
+// rank 16: 4 TB/s).
 constexpr int kRowCtas = 8, kRowThreads = 256;
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) row_kernel(const AdapterArgs a, float keep_scale) {
+template <typename T, bool DROP>
+__global__ void __launch_bounds__(kRowThreads, DROP ? 2 : 5) row_kernel(const AdapterArgs a, float keep_scale) {
   pdl_wait();
   __shared__ float part[128], us[128];
   const int64_t t = blockIdx.x / kRowCtas;
@@ -233,44 +268,94 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const AdapterArgs a, f
       for (int j = tid; j < r; j += kRowThreads) a.u[t * r + j] = 0.0f;
     return;
   }
+  constexpr int VN = Vec<T>::N, JS = 2, PC = 3, PB = 2;
   const T *x = static_cast<const T *>(a.x) + t * a.ld_in;
   const T *A = static_cast<const T *>(a.A) + (int64_t)ad * r * a.d_in;
   const T *B = static_cast<const T *>(a.B) + (int64_t)ad * a.d_out * r;
-  const Philox g(a.rng, a.threshold);
-  const int k0 = (int)((int64_t)(a.d_in / 4) * q / kRowCtas), k1 = (int)((int64_t)(a.d_in / 4) * (q + 1) / kRowCtas);
-  for (int j = warp; j < r; j += kRowThreads / 32) {
-    float sum = 0.0f;
-    for (int k = k0 + lane; k < k1; k += 32) {
-      float v[4], w[4];
-      load4(x + 4 * k, v);
-      if (a.threshold != 0) mask4(g, t * a.d_in + 4 * k, v);
-      load4(A + (int64_t)j * a.d_in + 4 * k, w);
+  const Philox g(DROP ? a.rng : nullptr, a.threshold);
+  const int k0 = (int)((int64_t)(a.d_in / VN) * q / kRowCtas), k1 = (int)((int64_t)(a.d_in / VN) * (q + 1) / kRowCtas);
+  // B and base of this thread's first columns are on their way while u is summed
+  uint4 early[PC][PB];
+  float add[PC];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum = fmaf(v[i], w[i], sum);
+  for (int i = 0; i < PC; ++i) {
+    const int c = c0 + tid + i * kRowThreads;
+    add[i] = base != nullptr && c < c1 ? to_f32(base[c]) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < PB; ++j)
+      early[i][j] = c < c1 && j * VN < r ? *reinterpret_cast<const uint4 *>(B + (int64_t)c * r + j * VN) : make_uint4(0, 0, 0, 0);
+  }
+  for (int j0 = warp; j0 < r; j0 += JS * kRowThreads / 32) {
+    float sum[JS] = {};
+#pragma unroll 2
+    for (int k = k0 + lane; k < k1; k += 32) {
+      float v[VN], w[JS][VN];
+      load16<T>(x + (int64_t)k * VN, v);
+#pragma unroll
+      for (int i = 0; i < JS; ++i) {
+        const int j = j0 + i * (kRowThreads / 32);
+        if (j < r) load16<T>(A + (int64_t)j * a.d_in + (int64_t)k * VN, w[i]);
+      }
+      if constexpr (DROP)
+#pragma unroll
+        for (int h = 0; h < VN; h += 4) {
+          float m[4] = {v[h], v[h + 1], v[h + 2], v[h + 3]};
+          mask4(g, t * a.d_in + (int64_t)k * VN + h, m);
+          v[h] = m[0]; v[h + 1] = m[1]; v[h + 2] = m[2]; v[h + 3] = m[3];
+        }
+#pragma unroll
+      for (int i = 0; i < JS; ++i)
+        if (j0 + i * (kRowThreads / 32) < r)
+#pragma unroll
+          for (int h = 0; h < VN; ++h) sum[i] = fmaf(v[h], w[i][h], sum[i]);
     }
-    sum = warp_sum(sum);
-    if (lane == 0) part[j] = sum;
+#pragma unroll
+    for (int i = 0; i < JS; ++i) {
+      const int j = j0 + i * (kRowThreads / 32);
+      if (j < r) {
+        sum[i] = warp_sum(sum[i]);
+        if (lane == 0) part[j] = sum[i];
+      }
+    }
   }
   cluster_sync();
   const float s = a.scale != nullptr ? a.scale[ad] : 1.0f;
   for (int j = tid; j < r; j += kRowThreads) {
     float v = 0.0f;
+#pragma unroll
     for (int c = 0; c < kRowCtas; ++c) v += remote_float(&part[j], (uint32_t)c);
     v *= keep_scale;
     if (a.u != nullptr && q == 0) a.u[t * r + j] = v;
     us[j] = v;
   }
-  cluster_sync();   // us is whole, and no CTA leaves while another reads its part
-  for (int c = c0 + tid; c < c1; c += kRowThreads) {
-    float sum = 0.0f;
-    for (int j = 0; j < r; j += 4) {
-      float w[4];
-      load4(B + (int64_t)c * r + j, w);
+  __syncthreads();
+  // this CTA has read the others' parts; before it leaves they have read its own
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  auto dot = [&](const uint4 &u, int j, float sum) {
+    float w[VN];
+    unpack16<T>(u, w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum = fmaf(us[j + i], w[i], sum);
+    for (int i = 0; i < VN; ++i) sum = fmaf(us[j + i], w[i], sum);
+    return sum;
+  };
+  auto column = [&](int c, float sum, int j, float b) {
+#pragma unroll 4
+    for (; j < r; j += VN) sum = dot(*reinterpret_cast<const uint4 *>(B + (int64_t)c * r + j), j, sum);
+    y[c] = from_f32<T>(fmaf(s, sum, b));
+  };
+#pragma unroll
+  for (int i = 0; i < PC; ++i) {
+    const int c = c0 + tid + i * kRowThreads;
+    if (c < c1) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < PB; ++j)
+        if (j * VN < r) sum = dot(early[i][j], j * VN, sum);
+      column(c, sum, PB * VN, add[i]);
     }
-    y[c] = from_f32<T>(fmaf(s, sum, base != nullptr ? to_f32(base[c]) : 0.0f));
   }
+  for (int c = c0 + tid + PC * kRowThreads; c < c1; c += kRowThreads) column(c, 0.0f, 0, base != nullptr ? to_f32(base[c]) : 0.0f);
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -633,22 +718,24 @@ cudaError_t launch_adapter_join(const AdapterArgs &a, cudaStream_t s) {
 cudaError_t launch_adapter_map(int64_t T, int n, const int32_t *adapter_of, int32_t *map, uint32_t *status,
                                cudaStream_t s) {
   const int bins = n + 1;
-  int runs = (int)(kMapSmem / 4 / bins) - 6;
+  int runs = (int)(kMapSmem / 4 / bins) - 7;
   if (runs > 32) runs = 32;
-  const size_t smem = (size_t)(runs + 6) * bins * 4;
+  const size_t smem = (size_t)(runs + 7) * bins * 4;
   cudaError_t e = cudaFuncSetAttribute(map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMapSmem);
   if (e != cudaSuccess) return e;
-  const int ctas = T <= 4096 ? 1 : kMapCtas;   // a run of up to 128 tokens a warp
+  const int ctas = T <= runs * 32 * kMapKept ? 1 : kMapCtas;
   return launch_pdl_clusters(map_kernel, dim3((unsigned)ctas), dim3(kMapThreads), ctas, smem, s, T, n, runs, adapter_of,
                              map, status);
 }
 
 cudaError_t launch_adapter(const AdapterArgs &a, cudaStream_t s) {
-  if (a.map == nullptr && (a.adapter_of != nullptr || adapter_rowwise(a.T, a.d_in, a.d_out, a.n, a.rank))) {
+  if (a.map == nullptr && (a.adapter_of != nullptr || adapter_rowwise(a.T, a.d_in, a.d_out, 1, a.rank, a.dtype))) {
     const float keep = drop_scale(a.threshold);
-    const dim3 grid((unsigned)(a.T * kRowCtas));
-    if (a.dtype == MOE_F32) return launch_pdl_clusters(row_kernel<float>, grid, dim3(kRowThreads), kRowCtas, 0, s, a, keep);
-    return launch_pdl_clusters(row_kernel<__nv_bfloat16>, grid, dim3(kRowThreads), kRowCtas, 0, s, a, keep);
+    auto run = [&](auto kernel) {
+      return launch_pdl_clusters(kernel, dim3((unsigned)(a.T * kRowCtas)), dim3(kRowThreads), kRowCtas, 0, s, a, keep);
+    };
+    if (a.dtype == MOE_F32) return a.threshold != 0 ? run(row_kernel<float, true>) : run(row_kernel<float, false>);
+    return a.threshold != 0 ? run(row_kernel<__nv_bfloat16, true>) : run(row_kernel<__nv_bfloat16, false>);
   }
   return a.dtype == MOE_F32 ? forward<float>(a, s) : launch_adapter_tc(a, s);
 }
