@@ -17,15 +17,15 @@ size_t adapter_scratch_bytes(int64_t T, int d_in, int d_out, int rank) {
 size_t adapter_map_bytes(int64_t T, int n) { return (size_t)map_layout(T, n).words * 4; }
 
 // Row by row every token reads its adapter (rank (d_in + d_out) elements) from
-// L2, at 6.5 MB/us measured; by tiles there are a map and two more kernels (17 us
+// L2, at 4 MB/us measured; by tiles there are a map and two more kernels (17 us
 // for the smallest batch) and half a microsecond a tile, of up to 128 tokens of
-// one adapter each: measured at 6144 and rank 16, 256 tokens of 64 adapters 19
+// one adapter each: measured at 6144 and rank 16, 256 tokens of 64 adapters 28
 // us by rows and 53 us by tiles, 1021 x 3584 to 5120 of 12 adapters of rank 24
-// 54 us by rows and 30 us by tiles.
+// 81 us by rows and 30 us by tiles.
 bool adapter_rowwise(int64_t T, int d_in, int d_out, int n, int rank, int dtype) {
   const double bytes = (double)T * rank * ((double)d_in + d_out) * (dtype == MOE_BF16 ? 2 : 4);
   const double tiles = (double)(T / kTileRows) + (double)(n < T ? n : T);
-  return bytes / 6.5e6 < 17.0 + 0.5 * tiles;
+  return bytes / 4.0e6 < 17.0 + 0.5 * tiles;
 }
 
 namespace {
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(int64_t T, int n, int 
     if (lane < runs) hist[lane * bins + e] = sum - c;
     if (lane == 31) total[e] = sum;
   }
-  if (ctas > 1) cluster_sync();
+  if (ctas > 1) cluster_meet();
   else __syncthreads();
   for (int e = tid; e < bins; e += kMapThreads) {
     int before = 0, sum = 0;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(int64_t T, int n, int 
     map[kMapTiles] = sums.y;
     map[kMapChunks] = sums.z;
   }
-  if (ctas > 1) cluster_sync();   // no CTA leaves while another reads its counts
+  if (ctas > 1) cluster_meet();   // no CTA leaves while another reads its counts
 }
 
 // ---------------------------------------------------------------------------
@@ -238,13 +238,15 @@ __device__ __forceinline__ void mask4(const Philox &g, int64_t i, float (&v)[4])
 
 // ---------------------------------------------------------------------------
 // Row by row: a cluster of 8 CTAs a token. Every CTA takes a part of d_in for u,
-// the parts meet in shared memory, and every CTA takes a part of d_out for y. Bound by
-// latency for few tokens, by L2 from some hundreds on (0.4 MB a token at 6144 and
-// rank 16: 4 TB/s).
+// the parts meet in shared memory, and every CTA takes a part of d_out for y, of
+// which the first factors are fetched before u is known. Bound by latency for few
+// tokens (6144, rank 16: one token 4.8 us, 64 tokens 8.3 us in a graph, of which
+// the launch is 2), by L2 from some hundreds on. 64 registers, four CTAs an SM:
+// more values in flight a thread and fewer CTAs took 11 us for the 64 tokens.
 constexpr int kRowCtas = 8, kRowThreads = 256;
 
 template <typename T, bool DROP>
-__global__ void __launch_bounds__(kRowThreads, DROP ? 2 : 5) row_kernel(const AdapterArgs a, float keep_scale) {
+__global__ void __launch_bounds__(kRowThreads, DROP ? 2 : 4) row_kernel(const AdapterArgs a, float keep_scale) {
   pdl_wait();
   __shared__ float part[128], us[128];
   const int64_t t = blockIdx.x / kRowCtas;
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kRowThreads, DROP ? 2 : 5) row_kernel(const Ad
       for (int j = tid; j < r; j += kRowThreads) a.u[t * r + j] = 0.0f;
     return;
   }
-  constexpr int VN = Vec<T>::N, JS = 2, PC = 3, PB = 2;
+  constexpr int VN = Vec<T>::N, PC = 3, PB = 2;
   const T *x = static_cast<const T *>(a.x) + t * a.ld_in;
   const T *A = static_cast<const T *>(a.A) + (int64_t)ad * r * a.d_in;
   const T *B = static_cast<const T *>(a.B) + (int64_t)ad * a.d_out * r;
@@ -285,40 +287,28 @@ __global__ void __launch_bounds__(kRowThreads, DROP ? 2 : 5) row_kernel(const Ad
     for (int j = 0; j < PB; ++j)
       early[i][j] = c < c1 && j * VN < r ? *reinterpret_cast<const uint4 *>(B + (int64_t)c * r + j * VN) : make_uint4(0, 0, 0, 0);
   }
-  for (int j0 = warp; j0 < r; j0 += JS * kRowThreads / 32) {
-    float sum[JS] = {};
+  for (int j = warp; j < r; j += kRowThreads / 32) {
+    float sum = 0.0f;
 #pragma unroll 2
     for (int k = k0 + lane; k < k1; k += 32) {
-      float v[VN], w[JS][VN];
+      float v[VN], w[VN];
       load16<T>(x + (int64_t)k * VN, v);
-#pragma unroll
-      for (int i = 0; i < JS; ++i) {
-        const int j = j0 + i * (kRowThreads / 32);
-        if (j < r) load16<T>(A + (int64_t)j * a.d_in + (int64_t)k * VN, w[i]);
-      }
-      if constexpr (DROP)
+      load16<T>(A + (int64_t)j * a.d_in + (int64_t)k * VN, w);
+      if constexpr (DROP) {
 #pragma unroll
         for (int h = 0; h < VN; h += 4) {
           float m[4] = {v[h], v[h + 1], v[h + 2], v[h + 3]};
           mask4(g, t * a.d_in + (int64_t)k * VN + h, m);
           v[h] = m[0]; v[h + 1] = m[1]; v[h + 2] = m[2]; v[h + 3] = m[3];
         }
-#pragma unroll
-      for (int i = 0; i < JS; ++i)
-        if (j0 + i * (kRowThreads / 32) < r)
-#pragma unroll
-          for (int h = 0; h < VN; ++h) sum[i] = fmaf(v[h], w[i][h], sum[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < JS; ++i) {
-      const int j = j0 + i * (kRowThreads / 32);
-      if (j < r) {
-        sum[i] = warp_sum(sum[i]);
-        if (lane == 0) part[j] = sum[i];
       }
+#pragma unroll
+      for (int h = 0; h < VN; ++h) sum = fmaf(v[h], w[h], sum);
     }
+    sum = warp_sum(sum);
+    if (lane == 0) part[j] = sum;
   }
-  cluster_sync();
+  cluster_meet();
   const float s = a.scale != nullptr ? a.scale[ad] : 1.0f;
   for (int j = tid; j < r; j += kRowThreads) {
     float v = 0.0f;
@@ -330,7 +320,7 @@ __global__ void __launch_bounds__(kRowThreads, DROP ? 2 : 5) row_kernel(const Ad
   }
   __syncthreads();
   // this CTA has read the others' parts; before it leaves they have read its own
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  cluster_arrive();
   auto dot = [&](const uint4 &u, int j, float sum) {
     float w[VN];
     unpack16<T>(u, w);
@@ -355,7 +345,7 @@ __global__ void __launch_bounds__(kRowThreads, DROP ? 2 : 5) row_kernel(const Ad
     }
   }
   for (int c = c0 + tid + PC * kRowThreads; c < c1; c += kRowThreads) column(c, 0.0f, 0, base != nullptr ? to_f32(base[c]) : 0.0f);
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_wait();
 }
 
 // ---------------------------------------------------------------------------

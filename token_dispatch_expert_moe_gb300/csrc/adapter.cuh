@@ -133,6 +133,15 @@ struct Plan {
   }
 };
 
+// The cluster's barrier, thread by thread: the warps come to it out of loops and
+// branches that lanes leave at different times, and the .aligned forms (of
+// cluster_sync) want whole warps.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void cluster_meet() {
+  cluster_arrive();
+  cluster_wait();
+}
 // a word of another CTA's shared memory
 __device__ __forceinline__ int remote_int(const void *p, uint32_t rank) {
   int v;

@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP>:
     }
   }
   tc_fence_before();
-  if (p.split > 1) cluster_sync();
+  if (p.split > 1) cluster_meet();
   else __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_free(tmem, Z::kTmem);
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP>:
         store_parts(p.parts_in + pos, p.rp, w);
       }
     }
-  if (p.split > 1) cluster_sync();   // no CTA leaves while another reads its sums
+  if (p.split > 1) cluster_meet();   // no CTA leaves while another reads its sums
 }
 
 // ---------------------------------------------------------------------------
