@@ -19,6 +19,7 @@ __host__ __device__ constexpr int64_t chunk_rows(int64_t T) {
 // An adapter of several chunks has more than one chunk's tokens, so at most
 // twice as many chunks as full ones.
 constexpr int kMaxSlots = 32;
+__host__ __device__ constexpr int slots_of(int64_t T) { return T > chunk_rows(T) ? kMaxSlots : 0; }
 
 // The map, in 32-bit words: a header, order [T] (the tokens by adapter, in
 // their order inside one; those without an adapter last), and, 16-byte aligned,
@@ -78,7 +79,8 @@ struct Plan {
   }
   __device__ __forceinline__ int4 checked_chunk(int4 c) const {
     c = checked(c, chunk_rows(T));
-    if (c.x < 0 || c.w >= kMaxSlots) c.z = 0;
+    if (c.x >= 0 && c.w >= slots_of(T)) report(status, MOE_ERR_DEVICE, kInfoAdapterMap);
+    if (c.x < 0 || c.w >= slots_of(T)) c.z = 0;
     return c;
   }
   __device__ __forceinline__ int64_t tiles() const {
@@ -121,7 +123,11 @@ struct Plan {
       return a == 0 ? make_int2(0, (int)k) : make_int2(0, 0);
     }
     int2 g = reinterpret_cast<const int2 *>(map + map_layout(T, n).groups)[a];
-    if (g.y > 1 && (g.x < 0 || g.x + g.y > kMaxSlots)) g = make_int2(0, 0);
+    // compared without a sum, which words that make no sense would overflow
+    if (g.y < 0 || (g.y > 1 && (g.y > slots_of(T) || g.x < 0 || g.x > slots_of(T) - g.y))) {
+      report(status, MOE_ERR_DEVICE, kInfoAdapterMap);
+      g = make_int2(0, 0);
+    }
     return g;
   }
   __device__ __forceinline__ int64_t token(int64_t pos) const {
@@ -177,7 +183,7 @@ __host__ inline Scratch scratch_of(int64_t T, int d_in, int d_out, int rank) {
   Scratch s;
   // fp32 [T, rank], or bf16 [T, 3 padded_rank]: the three parts of u
   const size_t each = up((size_t)T * padded_rank(rank) * 6);
-  const size_t slots = T > chunk_rows(T) ? kMaxSlots : 0;
+  const size_t slots = (size_t)slots_of(T);
   s.u = 0;
   s.du = each;
   s.dA = 2 * each;
