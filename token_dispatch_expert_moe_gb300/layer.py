@@ -1,11 +1,13 @@
 """MoELayer: the whole layer through the C ABI, buffers held in torch tensors.
 
-Forward: [moe_rmsnorm ->] moe_route [-> moe_balance_loss] -> moe_permute or
-moe_permute_e4m3 -> moe_expert_ffn (routed experts)
-[-> moe_expert_ffn (shared expert: one group, offsets {0, T})] -> moe_unpermute.
+Forward: [moe_dropout ->] [moe_rmsnorm ->] moe_route [-> moe_balance_loss] ->
+moe_permute or moe_permute_e4m3 -> moe_expert_ffn (routed experts)
+[-> moe_expert_ffn (shared expert: one group, offsets {0, T})] -> moe_unpermute
+[-> moe_adapter_map -> moe_adapter].
 Backward: moe_unpermute_bwd -> moe_expert_ffn_bwd (routed [, shared])
-[-> moe_balance_loss_bwd] -> moe_route_bwd -> moe_permute_bwd
-[-> moe_rmsnorm_bwd]; clip_grads: moe_grad_norm -> moe_grad_clip.
+[-> moe_adapter_bwd] [-> moe_balance_loss_bwd] -> moe_route_bwd -> moe_permute_bwd
+[-> moe_rmsnorm_bwd] [-> moe_dropout_bwd]; clip_grads: moe_grad_norm ->
+moe_grad_clip.
 torch only allocates device memory and supplies the stream; every step runs
 in libmoe.so.
 """
@@ -69,13 +71,33 @@ class MoELayer:
     padding) takes tokens out of it; backward adds its gradient, times dloss
     ([1] on the device) if given, to the router's.
 
+    dropout > 0 (with gamma) drops out of x in front of the residual's addition:
+    h = residual + drop(x). backward's "dx" is then the gradient of h and of the
+    residual, and "dx_drop", of the same dtype, that of x.
+
+    With weights "lora_A" [n, rank, d] and "lora_B" [n, d, rank] (in the layer's
+    dtype; "lora_scale" [n] fp32, else 1) low-rank adapters stand beside the
+    layer, as a scaled parallel adapter does beside a block's FFN: forward's
+    adapter ([T] int32: the adapter of each token, -1 for none; None: adapter 0
+    for all) picks them, and the output gains lora_scale[a] lora_B[a] (lora_A[a]
+    drop(m)), m the MoE layer's input (the norm's output), dropped out of with
+    adapter_dropout. backward adds their part to dx and gives "dlora_A" and
+    "dlora_B" (fp32). An index outside [-1, n) counts as none and is reported by
+    moe_get_status(adapter_ws).
+
+    forward's rng ([2, 2] int64 on the device: seed and offset of the residual's
+    dropout, then of the adapters') says which masks: the caller counts an offset
+    up from step to step, in a captured step on the device. Both are kept as they
+    are until backward has run. rng None: nothing is dropped (evaluation).
+
     x, residual, dout and dh are [T, d] (or [..., d]) in the layer's dtype,
     dense, on the layer's device; a tensor of another kind is refused with a
     ValueError before anything is launched."""
 
     def __init__(self, cfg, weights: dict, device="cuda", backward=None, etp: int = 1,
                  layout: str = "compact", gather: bool = False, norm_eps: float = 1e-6,
-                 dispatch: str = "act", balance: float = 0.0, dx_dtype: str = "f32"):
+                 dispatch: str = "act", balance: float = 0.0, dx_dtype: str = "f32",
+                 dropout: float = 0.0, adapter_dropout: float = 0.0):
         self.cfg = cfg
         self.etp = etp
         self.layout = layout
@@ -108,6 +130,14 @@ class MoELayer:
         if dx_dtype == "act" and not self.norm:
             raise ValueError('dx_dtype="act" needs gamma')
         self.e4m3 = dispatch == "e4m3"
+        self.dropout, self.adapter_dropout = dropout, adapter_dropout
+        self.adapters = "lora_A" in weights
+        if not 0.0 <= dropout < 1.0 or not 0.0 <= adapter_dropout < 1.0:
+            raise ValueError(f"dropout {dropout} or adapter_dropout {adapter_dropout} is not in [0, 1)")
+        if dropout and not self.norm:
+            raise ValueError("dropout needs gamma")
+        if self.adapters != ("lora_B" in weights) or (not self.adapters and (adapter_dropout or "lora_scale" in weights)):
+            raise ValueError("adapters need lora_A and lora_B")
         z = lambda *s, dtype=dt: torch.empty(*s, dtype=dtype, device=device)  # noqa: E731
         self.ws = torch.zeros(L.moe_workspace_size(self.shape), dtype=torch.uint8, device=device)
         if self.norm:
@@ -119,6 +149,17 @@ class MoELayer:
             if self.e4m3:
                 self.q = z(T, d, dtype=torch.float8_e4m3fn)
                 self.q_scale = z(T, -(-d // E4M3_GROUP), dtype=torch.float32)
+        if self.adapters:
+            n, rank = (weights["lora_A"].shape + (0, 0))[:2]
+            self._take("lora_A", weights["lora_A"], (dt,), n * rank * d, last=d)
+            self._take("lora_B", weights["lora_B"], (dt,), n * rank * d, last=rank)
+            self._take("lora_scale", weights.get("lora_scale"), (torch.float32,), n)
+            self.adapter_shape = L.MoEAdapterShape(T=T, d_in=d, d_out=d, n=n, rank=rank, dtype=self.dtype_code)
+            if L.moe_adapter_workspace_size(self.adapter_shape) == 0:
+                raise ValueError(f"no adapters of shape {tuple(weights['lora_A'].shape)} and {tuple(weights['lora_B'].shape)}")
+            self.adapter_ws = torch.zeros(L.moe_adapter_workspace_size(self.adapter_shape), dtype=torch.uint8, device=device)
+            self.adapter_map = z(L.moe_adapter_map_size(self.adapter_shape), dtype=torch.uint8)
+            self.u = z(T, rank, dtype=torch.float32) if self.backward_enabled else None
         if balance:
             n_sub = -(-T // cfg.subseq)
             self.loss = z(1, dtype=torch.float32)
@@ -188,6 +229,11 @@ class MoELayer:
                 # None: dx itself, in place
                 self.dx_h = z(T, d) if dx_dtype == "act" and dt != torch.float32 else None
                 self.norm_ws = z(L.moe_rmsnorm_bwd_workspace_size(T, d), dtype=torch.uint8)
+                self.dx_drop = z(T, d, dtype=dt if dx_dtype == "act" else torch.float32) if dropout else None
+            if self.adapters:
+                self.dlora_A = z(n, rank, d, dtype=torch.float32)
+                self.dlora_B = z(n, d, rank, dtype=torch.float32)
+                self.dx_adapter = None if cfg.Fs else z(T, d, dtype=torch.float32)   # else onto the shared expert's
             self.grad_ws = z(L.MOE_GRAD_NORM_WORKSPACE_BYTES, dtype=torch.uint8)
             self.grad_norm = z(1, dtype=torch.float32)
             if self.shared:
@@ -217,7 +263,8 @@ class MoELayer:
         if t.device != self.ws.device:
             raise ValueError(f"{name} is on {t.device}, the layer on {self.ws.device}")
 
-    def forward(self, x: torch.Tensor, stream=None, residual=None, mask=None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, stream=None, residual=None, mask=None, adapter=None,
+                rng=None) -> torch.Tensor:
         c, s, w = self.cfg, self.shape, self.w
         if residual is not None and not self.norm:
             raise ValueError("a residual needs the norm (weight gamma)")
@@ -226,6 +273,14 @@ class MoELayer:
         self._take("x", x, (self.dt,), c.T * c.d, more=True)
         self._take("residual", residual, (self.dt,), c.T * c.d, last=c.d)
         self._take("mask", mask, (torch.uint8, torch.bool, torch.int8), c.T)
+        if adapter is not None and not self.adapters:
+            raise ValueError("an adapter needs the weights lora_A and lora_B")
+        self._take("adapter", adapter, (torch.int32,), c.T)
+        self._take("rng", rng, (torch.int64, torch.uint64), 4)
+        self.rng = rng if rng is None else rng.view(-1)
+        if self.dropout and rng is not None:   # the sum is formed here, the norm finds it done
+            L.moe_dropout(self.dtype_code, c.T * c.d, x, residual, self.dropout, self.rng[:2], self.h_own, stream)
+            x, residual = self.h_own, None
         if self.norm:
             self.h = x if residual is None else self.h_own
             L.moe_rmsnorm(self.dtype_code, c.T, c.d, x, residual, w["gamma"], self.norm_eps,
@@ -252,6 +307,16 @@ class MoELayer:
                              w["Ws_down"], self.As, self.Hs, self.Ys, self.ws, stream)
         L.moe_unpermute(s, self.Yp, self.row_of, self.topk_w, self.Ys, self.gate_logit, self.out,
                         stream)
+        if self.adapters:
+            a = self.adapter_shape
+            a.dropout = self.adapter_dropout if rng is not None else 0.0
+            by_rows = adapter is None or (L.moe_adapter_rowwise(a) and not self.backward_enabled)
+            self.adapter_groups = None if adapter is None else self.adapter_map
+            if adapter is not None and not by_rows:
+                L.moe_adapter_map(a, adapter, self.adapter_map, self.adapter_ws, stream)
+            L.moe_adapter(a, x, w["lora_A"], w["lora_B"], w.get("lora_scale"), adapter,
+                          None if by_rows else self.adapter_map, None if rng is None else self.rng[2:], self.out, self.out,
+                          self.u, self.adapter_ws, stream)
         return self.out
 
     def routed_ffn(self, stream=None):
@@ -288,9 +353,9 @@ class MoELayer:
     def backward(self, dout: torch.Tensor, stream=None, marks=None, dh=None, dloss=None) -> dict:
         """marks: optional dict of (start, end) CUDA event pairs, keyed by
         "unpermute_bwd", "ffn_bwd" (routed experts), "shared_ffn_bwd",
-        "route_bwd" (the balance loss's gradient included), "permute_bwd" and
-        "norm_bwd"; each present pair is recorded on the current stream around
-        that call."""
+        "adapter_bwd", "route_bwd" (the balance loss's gradient included),
+        "permute_bwd" and "norm_bwd"; each present pair is recorded on the
+        current stream around that call."""
         c, s, w = self.cfg, self.shape, self.w
         marks = marks or {}
         if dh is not None and not self.norm:
@@ -322,6 +387,14 @@ class MoELayer:
                                  self.dWs_gu, self.dWs_down, self.ws, stream)
             mark("shared_ffn_bwd", 1)
             dx_in = self.dXs
+        if self.adapters:
+            mark("adapter_bwd", 0)
+            dx = self.dXs if self.shared else self.dx_adapter
+            L.moe_adapter_bwd(self.adapter_shape, L.MOE_F32, dout, self.x, w["lora_A"], w["lora_B"], w.get("lora_scale"),
+                              self.adapter_groups, None if self.rng is None else self.rng[2:], self.u, dx_in, dx,
+                              self.dlora_A, self.dlora_B, self.adapter_ws, stream)
+            mark("adapter_bwd", 1)
+            dx_in = dx
         mark("route_bwd", 0)
         args = [s, self.x, w["W_r"], w.get("w_sg"), self.logits, self.topk_idx, self.topk_prob,
                 self.topk_w, self.dw, self.dz if self.shared else None]
@@ -347,9 +420,20 @@ class MoELayer:
                               c.T, c.d, self.dx, self.h, w["gamma"], self.rstd, dh, dx, self.dgamma,
                               self.norm_ws, stream)
             mark("norm_bwd", 1)
+        if self.dropout:
+            if self.rng is None:
+                dropped = dx
+            else:
+                dropped = self.dx_drop
+                code = L.MOE_F32 if dx.dtype == torch.float32 else L.MOE_BF16
+                L.moe_dropout_bwd(code, code, c.T * c.d, dx, self.dropout, self.rng[:2], dropped, stream)
         g = {"dx": dx, "dW_r": self.dW_r, "dW_gu": self.dW_gu, "dW_down": self.dW_down}
         if self.norm:
             g["dgamma"] = self.dgamma
+        if self.dropout:
+            g["dx_drop"] = dropped
+        if self.adapters:
+            g.update(dlora_A=self.dlora_A, dlora_B=self.dlora_B)
         if "b_r" in w:
             g["db_r"] = self.db_r
         if self.shared:
@@ -368,6 +452,8 @@ class MoELayer:
             g += [self.dWs_gu, self.dWs_down, self.dw_sg]
         if self.norm:
             g.append(self.dgamma)
+        if self.adapters:
+            g += [self.dlora_A, self.dlora_B]
         return g
 
     def clip_grads(self, max_norm: float, stream=None) -> torch.Tensor:
