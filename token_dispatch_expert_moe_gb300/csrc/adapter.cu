@@ -536,39 +536,45 @@ __global__ void __launch_bounds__(kSimtThreads) expand_kernel(const Expand p) {
   }
 }
 
-struct Wgrad {   // G_a = factor sum_t v_t z_t^T over a chunk: [rank, d], or [d, rank] (GT)
-  Plan plan;
+struct WgradJob {   // G_a = factor sum_t v_t z_t^T over a chunk: [rank, d], or `transposed` [d, rank]
   const void *z;
   const float *v;
-  int v_by_token;
+  int v_by_token, transposed;
   int64_t ld;
-  int d, rank;
+  int d;
   uint32_t threshold;
-  const uint64_t *rng;
   const float *scale;
   float factor;
   float *out, *partial;   // [n, rank d], [slots, rank d]
 };
+struct Wgrad {   // both gradients of a backward in one launch
+  WgradJob job[2];
+  Plan plan;
+  int rank;
+  const uint64_t *rng;
+};
 constexpr int kGradCols = 64;
 
-template <typename T, bool GT>
-__global__ void __launch_bounds__(kSimtThreads) wgrad_kernel(const Wgrad p) {
+template <typename T>
+__global__ void __launch_bounds__(kSimtThreads) wgrad_kernel(const Wgrad all) {
   pdl_wait();
+  const WgradJob &p = all.job[blockIdx.z];
+  if ((int)blockIdx.y * kGradCols >= p.d) return;
   __shared__ __align__(16) float buf[256 / 2 * 64];   // 32 KB: 32 rows of z and of v, then the sets' sums
   float (*zs)[kGradCols + 4] = reinterpret_cast<float(*)[kGradCols + 4]>(buf);
   float (*vs)[128] = reinterpret_cast<float(*)[128]>(buf + 32 * (kGradCols + 4));
   __shared__ int64_t tok[32];
-  const int4 ch = p.plan.chunk_of(blockIdx.x);
+  const int4 ch = all.plan.chunk_of(blockIdx.x);
   if (ch.z <= 0) return;
-  const int r = p.rank, r8 = (r + 7) / 8, c0 = blockIdx.y * kGradCols, tid = threadIdx.x;
+  const int r = all.rank, r8 = (r + 7) / 8, c0 = blockIdx.y * kGradCols, tid = threadIdx.x;
   const int set = r8 * 16, sets = kSimtThreads / set, mine = tid / set, at = tid % set;
   const int jj = (at / 16) * 8, cc = (at % 16) * 4;
   const T *z = static_cast<const T *>(p.z);
-  const Philox g(p.rng, p.threshold);
+  const Philox g(all.rng, p.threshold);
   float acc[8][4] = {};
   for (int i0 = 0; i0 < ch.z; i0 += 32) {
     const int rows = min(32, ch.z - i0);
-    if (tid < 32) tok[tid] = tid < rows ? p.plan.token(ch.y + i0 + tid) : -1;
+    if (tid < 32) tok[tid] = tid < rows ? all.plan.token(ch.y + i0 + tid) : -1;
     __syncthreads();
     for (int i = tid; i < 32 * (kGradCols / 4); i += kSimtThreads) {
       const int row = i / (kGradCols / 4), c = (i % (kGradCols / 4)) * 4;
@@ -609,11 +615,11 @@ __global__ void __launch_bounds__(kSimtThreads) wgrad_kernel(const Wgrad p) {
   const float f = p.factor * (p.scale != nullptr ? p.scale[ch.x] : 1.0f);
   float *out = ch.w < 0 ? p.out + (int64_t)ch.x * r * p.d : p.partial + (int64_t)ch.w * r * p.d;
   for (int i = tid; i < r * kGradCols; i += kSimtThreads) {
-    const int j = GT ? i % r : i / kGradCols, c = GT ? i / r : i % kGradCols;
+    const int j = p.transposed ? i % r : i / kGradCols, c = p.transposed ? i / r : i % kGradCols;
     if (c0 + c >= p.d) continue;
     float v = 0.0f;
     for (int k = 0; k < sets; ++k) v += buf[(k * r8 * 8 + j) * kGradCols + c];
-    out[GT ? (int64_t)(c0 + c) * r + j : (int64_t)j * p.d + c0 + c] = f * v;
+    out[p.transposed ? (int64_t)(c0 + c) * r + j : (int64_t)j * p.d + c0 + c] = f * v;
   }
 }
 
@@ -654,13 +660,6 @@ cudaError_t expand(const AdapterArgs &a, const Expand &p, cudaStream_t s) {
                     dim3((unsigned)(host_tiles(a) * 4), (unsigned)((p.d + kExpandCols - 1) / kExpandCols)),
                     dim3(kSimtThreads), 0, s, p);
 }
-template <typename T, bool GT>
-cudaError_t wgrad(const AdapterArgs &a, const Wgrad &p, cudaStream_t s) {
-  return launch_pdl(wgrad_kernel<T, GT>,
-                    dim3((unsigned)host_chunks(a), (unsigned)((p.d + kGradCols - 1) / kGradCols)),
-                    dim3(kSimtThreads), 0, s, p);
-}
-
 template <typename T> cudaError_t forward(const AdapterArgs &a, cudaStream_t s) {
   const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
   float *u = reinterpret_cast<float *>(a.ws + sc.u);
@@ -680,12 +679,13 @@ template <typename T> cudaError_t backward(const AdapterArgs &a, cudaStream_t s)
   const Shrink sh{plan, a.dy, a.B, a.ld_out, a.d_out, a.rank, 0, nullptr, a.scale, 1.0f, du, nullptr};
   cudaError_t e = shrink<T, true>(a, sh, s);
   if (e == cudaSuccess && a.dA != nullptr) {
-    const Wgrad wa{plan, a.x, du, 0, a.ld_in, a.d_in, a.rank, a.threshold, a.rng, nullptr, keep, a.dA,
-                   reinterpret_cast<float *>(a.ws + sc.dA)};
-    const Wgrad wb{plan, a.dy, a.u_in, 1, a.ld_out, a.d_out, a.rank, 0, nullptr, a.scale, 1.0f, a.dB,
-                   reinterpret_cast<float *>(a.ws + sc.dB)};
-    e = wgrad<T, false>(a, wa, s);
-    if (e == cudaSuccess) e = wgrad<T, true>(a, wb, s);
+    Wgrad w{};
+    w.plan = plan; w.rank = a.rank; w.rng = a.rng;
+    w.job[0] = WgradJob{a.x, du, 0, 0, a.ld_in, a.d_in, a.threshold, nullptr, keep, a.dA, reinterpret_cast<float *>(a.ws + sc.dA)};
+    w.job[1] = WgradJob{a.dy, a.u_in, 1, 1, a.ld_out, a.d_out, 0, a.scale, 1.0f, a.dB, reinterpret_cast<float *>(a.ws + sc.dB)};
+    const int d = a.d_in > a.d_out ? a.d_in : a.d_out;
+    e = launch_pdl(wgrad_kernel<T>, dim3((unsigned)host_chunks(a), (unsigned)((d + kGradCols - 1) / kGradCols), 2),
+                   dim3(kSimtThreads), 0, s, w);
     if (e == cudaSuccess) e = launch_adapter_join(a, s);
   }
   if (e == cudaSuccess && a.dx != nullptr) {

@@ -193,14 +193,15 @@ struct ShrinkTc {
   bf16 *parts_in;
 };
 
-template <int RPMAX, bool WT, bool DROP> struct ShrinkSize {
+template <int RPMAX, bool WT, bool DROP, bool DEEP> struct ShrinkSize {
   static constexpr int kW = WT ? 8192 * ((RPMAX + 63) / 64) : RPMAX * 128;
   static constexpr int kStage = 16384 + kW;
   // Many CTAs an SM with short rings: one's start and end (7 us of loads that
   // wait for one another, and the sums' way out) hide behind the others. With
-  // dropout three, for the registers.
-  static constexpr int kCtas = RPMAX > 64 ? 2 : DROP ? 3 : 4;
-  static constexpr int kStages = kCtas == 4 ? 2 : 3;
+  // dropout three, for the registers. Where there are not more than two CTAs an
+  // SM anyway (DEEP), longer rings.
+  static constexpr int kCtas = RPMAX > 64 || DEEP ? 2 : DROP ? 3 : 4;
+  static constexpr int kStages = RPMAX > 64 ? 3 : DEEP ? 4 : kCtas == 4 ? 2 : 3;
   static constexpr int kAcc = RPMAX <= 32 ? 4 : 2;
   static constexpr int kTmem = kAcc * RPMAX;
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
@@ -213,9 +214,9 @@ struct Shared {
   int tok[kTileRows];
 };
 
-template <int RPMAX, bool WT, bool DROP>
-__global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP>::kCtas) shrink_tc_kernel(const __grid_constant__ ShrinkTc p) {
-  using Z = ShrinkSize<RPMAX, WT, DROP>;
+template <int RPMAX, bool WT, bool DROP, bool DEEP>
+__global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP, DEEP>::kCtas) shrink_tc_kernel(const __grid_constant__ ShrinkTc p) {
+  using Z = ShrinkSize<RPMAX, WT, DROP, DEEP>;
   constexpr int NST = Z::kStages, WORK = DROP ? 256 : 128, THREADS = WORK + 64;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -980,16 +981,19 @@ void set_split(const AdapterArgs &a, ShrinkTc &p) {
   p.per = (int)((all + p.split - 1) / p.split);
 }
 
-template <int RPMAX, bool WT, bool DROP> cudaError_t shrink(const AdapterArgs &a, const ShrinkTc &p, cudaStream_t s) {
-  constexpr size_t smem = ShrinkSize<RPMAX, WT, DROP>::kSmem;
-  cudaError_t e = allow(shrink_tc_kernel<RPMAX, WT, DROP>, smem);
+template <int RPMAX, bool WT, bool DROP, bool DEEP>
+cudaError_t shrink(const AdapterArgs &a, const ShrinkTc &p, cudaStream_t s) {
+  constexpr size_t smem = ShrinkSize<RPMAX, WT, DROP, DEEP>::kSmem;
+  cudaError_t e = allow(shrink_tc_kernel<RPMAX, WT, DROP, DEEP>, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl_clusters(shrink_tc_kernel<RPMAX, WT, DROP>, dim3((unsigned)(host_tiles(a) * p.split)),
+  return launch_pdl_clusters(shrink_tc_kernel<RPMAX, WT, DROP, DEEP>, dim3((unsigned)(host_tiles(a) * p.split)),
                              dim3(DROP ? 320 : 192), p.split, smem, s, p);
 }
 template <bool WT, bool DROP> cudaError_t shrink(const AdapterArgs &a, const ShrinkTc &p, cudaStream_t s) {
-  return p.rp <= 32 ? shrink<32, WT, DROP>(a, p, s) : p.rp <= 64 ? shrink<64, WT, DROP>(a, p, s)
-                                                                  : shrink<128, WT, DROP>(a, p, s);
+  const bool deep = host_tiles(a) * p.split <= 2 * sm_count();
+  if (p.rp > 64) return shrink<128, WT, DROP, false>(a, p, s);
+  if (deep) return p.rp <= 32 ? shrink<32, WT, DROP, true>(a, p, s) : shrink<64, WT, DROP, true>(a, p, s);
+  return p.rp <= 32 ? shrink<32, WT, DROP, false>(a, p, s) : shrink<64, WT, DROP, false>(a, p, s);
 }
 // x [T, d] rows ld apart; W [n, rank, d], or [n, d, rank] (WT)
 template <bool WT>
