@@ -28,6 +28,7 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kMaxRing = 12;
 constexpr int kCols = 128;   // columns of a block of expand and wgrad
+constexpr int kExpandSmem = 216 * 1024;
 
 // Roles in kInfoAdapterTimeout + role
 enum { kRoleEmpty = 1, kRoleFull = 2, kRoleReady = 3, kRoleDone = 4, kRoleSlab = 5, kRoleAcc = 6 };
@@ -115,6 +116,11 @@ struct Mask {
   __device__ __forceinline__ uint4 words(uint64_t block) const {
     const uint4 w = g.block(block);
     return make_uint4(word(w.x), word(w.y), word(w.z), word(w.w));
+  }
+  // a bit an element, of the words of a block
+  static __device__ __forceinline__ uint32_t bits(const uint4 &m) {
+    const uint32_t v = (m.x & 0x00020001u) | (m.y & 0x00080004u) | (m.z & 0x00200010u) | (m.w & 0x00800040u);
+    return (v | v >> 16) & 0xFFu;
   }
   static __device__ __forceinline__ void apply(uint4 *at, const uint4 &m) {
     const uint4 v = *at;
@@ -400,6 +406,118 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP, 
 }
 
 // ---------------------------------------------------------------------------
+// Accumulators onto base rows, as the sets of expand and of the pass below do it.
+
+// a load from TMEM on its way, and its end: what is read of r stands after it
+struct TmemLoad {
+  uint32_t r[16];
+  __device__ __forceinline__ void start(uint32_t taddr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+  }
+  __device__ __forceinline__ void end() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+  }
+};
+
+// 16 columns, the (16 h)-th on, of this thread's row of a slab gain f v, under
+// the low 16 of `bits` with MASKED; without a base the slab's old contents count
+// as 0.
+template <typename TO, bool MASKED>
+__device__ __forceinline__ void onto_16(uint8_t *slab, int row, int h, const TmemLoad &v, float f, bool based, bool live,
+                                        uint32_t bits) {
+  constexpr int VN = 16 / sizeof(TO);
+#pragma unroll
+  for (int e = 0; e < 16; e += VN) {
+    TO *at = reinterpret_cast<TO *>(slab + swz(row, (h * 16 + e) / VN));
+    float o[VN] = {};
+    if (based) load16<TO>(at, o);
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < VN; ++i) {
+        const float sum = fmaf(f, __uint_as_float(v.r[e + i]), o[i]);
+        o[i] = !MASKED || (bits >> (e + i) & 1) ? sum : o[i];
+      }
+    }
+    store16<TO>(at, o);
+  }
+}
+// A whole slab; the accumulator's next columns are on their way meanwhile. The
+// bits of its columns are shifted out of `bits`.
+template <typename TO, bool MASKED>
+__device__ __forceinline__ void onto_slab(uint8_t *slab, int row, uint32_t acc, float f, bool based, bool live, uint4 &bits) {
+  constexpr int PIECES = 128 / sizeof(TO) / 16;
+  TmemLoad a, b;
+  if (live) a.start(acc);
+#pragma unroll 1
+  for (int h = 0; h < PIECES; h += 2) {
+    if (live) {
+      a.end();
+      b.start(acc + (h + 1) * 16);
+    }
+    onto_16<TO, MASKED>(slab, row, h, a, f, based, live, bits.x);
+    if (live) {
+      b.end();
+      if (h + 2 < PIECES) a.start(acc + (h + 2) * 16);
+    }
+    onto_16<TO, MASKED>(slab, row, h + 1, b, f, based, live, bits.x >> 16);
+    if constexpr (MASKED) bits = make_uint4(bits.y, bits.z, bits.w, 0);
+  }
+}
+
+// A warp's 32 rows of a slab leave: at once by TMA where they follow one another
+// (`whole`, from row `first` on), else row by row, -1 for none. The slab is given
+// back once it has been read, by the next call where TMA reads it (`pending`).
+template <typename TO>
+__device__ __forceinline__ void slab_out(uint8_t *slab, int quarter, int lane, int64_t t, bool whole, int first, const CUtensorMap *mo,
+                                         TO *out, int64_t ld, int col, int d, uint64_t *sempty, int b, int &pending) {
+  constexpr int VN = 16 / sizeof(TO);
+  if (whole && col < d) {
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                       reinterpret_cast<uint64_t>(mo)),
+                   "r"(smem_u32(slab) + quarter * 4096), "r"(col), "r"(first)
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      if (pending >= 0) {   // the slab before this one has been read
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        mbar_arrive(smem_u32(&sempty[pending]));
+      }
+    }
+    pending = b;
+    return;
+  }
+  if (pending >= 0 && lane == 0) {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    mbar_arrive(smem_u32(&sempty[pending]));
+  }
+  pending = -1;
+  __syncwarp();
+  const int rq = lane >> 3, ch = lane & 7, cc = col + ch * VN;   // four rows at once, eight chunks each
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + rq;
+    const int64_t tr = __shfl_sync(0xffffffffu, t, r);
+    if (tr >= 0 && cc < d)
+      *reinterpret_cast<uint4 *>(out + tr * ld + cc) = *reinterpret_cast<const uint4 *>(slab + swz(quarter * 32 + r, ch));
+  }
+  fence_proxy_async();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&sempty[b]));
+}
+
+// ---------------------------------------------------------------------------
 // Expand. One CTA an SM runs through an equal share of all tiles' blocks of 128
 // columns, tile after tile. Base rows come by TMA into slabs of 128 rows x 128
 // bytes, the product of a block into one of two accumulators of one of two sets
@@ -416,6 +534,7 @@ struct ExpandTc {
   void *out;
   int64_t ld;
   int d, rank, rp, nparts;
+  int bare_only;                        // only the rows without an adapter
   int p_bytes, v_bytes, n_v, n_slab;    // shared memory: parts, V and how many of them, slabs of a set
   uint32_t threshold;
   const uint64_t *rng;
@@ -436,7 +555,7 @@ struct ExpandShared {
 
 template <typename TO, bool VT, bool DROP>
 __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(const __grid_constant__ ExpandTc p) {
-  constexpr int VN = 16 / sizeof(TO), PER = 128 / sizeof(TO), SLABS = kCols / PER;
+  constexpr int PER = 128 / sizeof(TO), SLABS = kCols / PER;
   extern __shared__ uint8_t raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t *vs = smem + p.p_bytes, *slabs = vs + p.n_v * p.v_bytes;
@@ -481,7 +600,7 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
     b0 = (int)(at % blocks);
     b1 = (int)(end - at < blocks - b0 ? b0 + (end - at) : blocks);
     at += b1 - b0;
-    return tile.z > 0 && (tile.x >= 0 || base != out);
+    return tile.z > 0 && (tile.x >= 0 ? p.bare_only == 0 : base != out);
   };
   bool ok = true;
   int block = 0;   // blocks so far: block b is set b % 2's (b / 2)-th
@@ -622,11 +741,12 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
       for (int blk = b0; blk < b1; ++blk, ++block) {
         const int set = block & 1, n = set ? used[1]++ : used[0]++, buf = set * 2 + (n & 1);
         uint32_t bits[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 w = mask.words(first + blk * 16 + i);
-          const uint32_t v = (w.x & 0x00020001u) | (w.y & 0x00080004u) | (w.z & 0x00200010u) | (w.w & 0x00800040u);
-          bits[i >> 2] |= ((v | v >> 16) & 0xFFu) << (8 * (i & 3));
+        // a short loop: its instructions share the cache with the other roles'
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w = mask.words(first + blk * 16 + i), x = mask.words(first + blk * 16 + 4 + i);
+          bits[0] |= Mask::bits(w) << (8 * i);
+          bits[1] |= Mask::bits(x) << (8 * i);
         }
         if (n >= 2) ok = wait(&st.abort, &st.mempty[buf], (uint32_t)((n / 2 - 1) & 1), p.plan.status, kRoleEmpty);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -638,7 +758,6 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
   } else if (warp >= 4) {
     // ---- accumulators onto the base rows
     const int set = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-    const int rq = lane >> 3, ch = lane & 7;   // four rows at once, eight chunks each
     int used = 0, sn = 0, pending = -1;        // used, sn: this set's accumulator and slabs so far
     for (int64_t at = begin; at < end && ok;) {
       int4 tile;
@@ -673,62 +792,8 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
           uint8_t *slab = slabs + b * 16384;
           ok = __all_sync(0xffffffffu, wait(&st.abort, &st.sfull[b], (uint32_t)((sn / p.n_slab) & 1), p.plan.status, kRoleSlab));
           if (!ok) break;
-#pragma unroll 1
-          for (int h = 0; h < PER / 32; ++h) {
-            float v[32];
-            if (live) tmem_ld32(acc + s * PER + h * 32, v);
-            if constexpr (DROP) {
-              const uint32_t m = bits.x;   // of these 32 columns
-              bits = make_uint4(bits.y, bits.z, bits.w, 0);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(m >> e & 1)) v[e] = 0.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += VN) {
-              TO *at = reinterpret_cast<TO *>(slab + swz(row, (h * 32 + e) / VN));
-              float o[VN] = {};
-              if (base != nullptr) load16<TO>(at, o);
-              if (live)
-#pragma unroll
-                for (int i = 0; i < VN; ++i) o[i] = fmaf(f, v[e + i], o[i]);
-              store16<TO>(at, o);
-            }
-          }
-          if (whole && c0 < p.d) {
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-              asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                               reinterpret_cast<uint64_t>(&p.mo)),
-                           "r"(smem_u32(slab) + quarter * 4096), "r"(c0), "r"(first)
-                           : "memory");
-              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-              if (pending >= 0) {   // the slab before this one has been read
-                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                mbar_arrive(smem_u32(&st.sempty[pending]));
-              }
-            }
-            pending = b;
-          } else {
-            if (pending >= 0 && lane == 0) {
-              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-              mbar_arrive(smem_u32(&st.sempty[pending]));
-            }
-            pending = -1;
-            __syncwarp();
-            const int cc = c0 + ch * VN;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = i * 4 + rq;
-              const int64_t tr = __shfl_sync(0xffffffffu, t, r);
-              if (tr >= 0 && cc < p.d)
-                *reinterpret_cast<uint4 *>(out + tr * p.ld + cc) = *reinterpret_cast<const uint4 *>(slab + swz(quarter * 32 + r, ch));
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&st.sempty[b]));
-          }
+          onto_slab<TO, DROP>(slab, row, acc + s * PER, f, base != nullptr, live, bits);
+          slab_out<TO>(slab, quarter, lane, t, whole, first, &p.mo, out, p.ld, c0, p.d, st.sempty, b, pending);
         }
         if (!ok) break;
         if (live) {
@@ -942,6 +1007,345 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
 }
 
 // ---------------------------------------------------------------------------
+// A's gradient and dx in one pass over x's mask: with dropout the two kernels
+// above each make every mask, and the generator, not memory, bounds both (32768 x
+// 8192, rank 16: 203 and 281 us for 79 and 158 us of bytes). Here one CTA an SM
+// runs through units, 128 columns of a chunk, tile by tile of 128 tokens: x and
+// du's parts come in, mask warps take the dropped elements out of x and keep a
+// bit an element, dA += x^T du runs on from tile to tile, dx of the tile is du A
+// under the bits, onto its base rows. One tile of parts serves both products: as
+// rows of K for dA, as rows of M for dx.
+struct BothTc {
+  CUtensorMap mx, mx_row, mp, mp_row, mv, mb, mb_row, mo;
+  Plan plan;
+  const void *base;
+  void *out;
+  int64_t ld;           // of base and out
+  int d, rank, rp, nparts, n_slab;
+  uint32_t threshold;
+  const uint64_t *rng;
+  float factor;
+  float *dA, *partial;
+};
+constexpr int kBothThreads = 640;   // warps 0: x, parts and A, 1: products, 2: base, 3: none, 4-11: two sets, 12-19: masks
+
+// ATOMS: 64-column boxes of the parts
+template <int ATOMS> struct BothSize {
+  static constexpr int kStage = 32768 + 16384 * ATOMS;
+  static constexpr int kStages = 2;
+  static constexpr int kV = ATOMS * 16 * 256;           // A's rows of 128 columns: rank up to 16 ATOMS
+  static constexpr int kAcc = ATOMS * 64;               // columns of TMEM of dA
+  static constexpr int kSlabs = (kExpandSmem - kStages * kStage - 2 * kV) / 16384;
+};
+struct BothShared {
+  uint64_t full[2], ready[2], empty[2], vfull[2], vempty[2], afull[2], aempty[2], dfull[2], dempty[2];
+  uint64_t sfull[kMaxRing], sempty[kMaxRing], mfull[4], mempty[4];
+  uint32_t tmem;
+  volatile int abort;
+  uint4 masks[4][kTileRows];
+};
+
+template <int ATOMS, typename TO>
+__global__ void __launch_bounds__(kBothThreads, 1) both_tc_kernel(const __grid_constant__ BothTc p) {
+  using Z = BothSize<ATOMS>;
+  constexpr int PER = 128 / sizeof(TO), SLABS = kCols / PER;
+  extern __shared__ uint8_t raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *vs = smem + Z::kStages * Z::kStage, *slabs = vs + 2 * Z::kV;
+  __shared__ BothShared st;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    st.abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&st.full[i]), 1);
+      mbar_init(smem_u32(&st.ready[i]), 8);
+      mbar_init(smem_u32(&st.empty[i]), 1);
+      mbar_init(smem_u32(&st.vfull[i]), 1);
+      mbar_init(smem_u32(&st.vempty[i]), 1);
+      mbar_init(smem_u32(&st.afull[i]), 1);
+      mbar_init(smem_u32(&st.aempty[i]), 4);
+      mbar_init(smem_u32(&st.dfull[i]), 1);
+      mbar_init(smem_u32(&st.dempty[i]), 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&st.mfull[i]), 8);
+      mbar_init(smem_u32(&st.mempty[i]), 4);
+    }
+    for (int i = 0; i < 2 * p.n_slab; ++i) {
+      mbar_init(smem_u32(&st.sfull[i]), 1);
+      mbar_init(smem_u32(&st.sempty[i]), 4);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async();
+  }
+  if (warp == 1) tmem_alloc(&st.tmem, 512);
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = st.tmem;   // dx of set 0 and 1, then dA of even and odd units
+  const TO *base = static_cast<const TO *>(p.base);
+  TO *out = static_cast<TO *>(p.out);
+  const int blocks = (p.d + kCols - 1) / kCols;
+  const int64_t units = p.plan.chunks() * blocks;
+  // The same walk for every role: a unit's chunk and first column.
+  auto unit_of = [&](int64_t u, int4 &ch, int &c0) {
+    ch = p.plan.chunk(u / blocks);
+    c0 = (int)(u % blocks) * kCols;
+    return ch.z > 0;
+  };
+  bool ok = true;
+  int unit = 0, step = 0;   // units and tiles so far: tile `step` is set step % 2's (step / 2)-th
+
+  if (warp == 0) {
+    // ---- x, parts and A
+    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      int4 ch;
+      int c0;
+      if (!unit_of(u, ch, c0)) continue;
+      const int vb = unit & 1;
+      if (unit >= 2) ok = wait(&st.abort, &st.vempty[vb], (uint32_t)((unit / 2 - 1) & 1), p.plan.status, kRoleEmpty);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (lane == 0) {
+        mbar_expect_tx(smem_u32(&st.vfull[vb]), (uint32_t)p.rp * 256);
+        for (int k = 0; k < 2; ++k)
+          tma_load_3d(smem_u32(vs + vb * Z::kV) + k * p.rp * 128, &p.mv, &st.vfull[vb], c0 + 64 * k, 0, ch.x);
+      }
+      ++unit;
+      int t[4];
+      lane_tokens(p.plan, ch.y, 4 * lane, ch.z, t);
+      for (int r0 = 0; r0 < ch.z; r0 += kTileRows, ++step) {
+        const int s = step & 1;
+        const RowCopy rows = row_copy(t, lane, true, true);   // rows past the chunk's end count as zeros
+        if (step >= 2) ok = wait(&st.abort, &st.empty[s], (uint32_t)((step / 2 - 1) & 1), p.plan.status, kRoleEmpty);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const bool whole = r0 + kTileRows <= ch.z;
+        const uint32_t xs = smem_u32(smem + s * Z::kStage), ps = xs + 32768;
+        if (lane == 0) {
+          mbar_expect_tx(smem_u32(&st.full[s]), 2 * rows.bytes + 16384 * ATOMS);
+          if (whole)
+#pragma unroll
+            for (int b = 0; b < ATOMS; ++b) tma_load_2d(ps + b * 16384, &p.mp, smem_u32(&st.full[s]), b * 64, ch.y + r0);
+        }
+        __syncwarp();
+        copy_rows(rows, xs, &p.mx, &p.mx_row, &st.full[s], c0, t, lane);
+        copy_rows(rows, xs + 16384, &p.mx, &p.mx_row, &st.full[s], c0 + 64, t, lane);
+        if (!whole) {
+          int pos[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pos[i] = r0 + 4 * lane + i < ch.z ? ch.y + r0 + 4 * lane + i : -1;
+#pragma unroll
+          for (int b = 0; b < ATOMS; ++b) tma_gather4(ps + b * 16384 + lane * 512, &p.mp_row, &st.full[s], b * 64, pos);
+        }
+        if (r0 + kTileRows < ch.z) lane_tokens(p.plan, ch.y, r0 + kTileRows + 4 * lane, ch.z, t);
+      }
+    }
+    __syncwarp();
+    if (lane == 0)
+      for (int b = 0; b < 2; ++b) {
+        if (b < unit) drain(&st.vfull[b], (uint32_t)(((unit - 1 - b) / 2) & 1));
+        if (b < step) drain(&st.full[b], (uint32_t)(((step - 1 - b) / 2) & 1));
+      }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---- base rows
+    int fetched[2] = {};
+    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      int4 ch;
+      int c0;
+      if (!unit_of(u, ch, c0)) continue;
+      int t[4];
+      lane_tokens(p.plan, ch.y, 4 * lane, ch.z, t);
+      for (int r0 = 0; r0 < ch.z && ok; r0 += kTileRows, ++step) {
+        const int set = step & 1;
+        const RowCopy rows = row_copy(t, lane, false, true);
+        for (int s = 0; s < SLABS; ++s) {
+          const int n = (step >> 1) * SLABS + s, b = set * p.n_slab + n % p.n_slab, c = c0 + s * PER;
+          if (n >= p.n_slab)
+            ok = wait(&st.abort, &st.sempty[b], (uint32_t)((n / p.n_slab - 1) & 1), p.plan.status, kRoleEmpty);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (base == nullptr || c >= p.d) {
+            if (lane == 0) mbar_arrive(smem_u32(&st.sfull[b]));
+          } else {
+            if (lane == 0) mbar_expect_tx(smem_u32(&st.sfull[b]), rows.bytes);
+            __syncwarp();
+            copy_rows(rows, smem_u32(slabs + b * 16384), &p.mb, &p.mb_row, &st.sfull[b], c, t, lane);
+          }
+          if (set) fetched[1] = n + 1;
+          else fetched[0] = n + 1;
+        }
+        if (r0 + kTileRows < ch.z) lane_tokens(p.plan, ch.y, r0 + kTileRows + 4 * lane, ch.z, t);
+      }
+    }
+    __syncwarp();
+    if (lane == 0)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        for (int b = 0; b < p.n_slab && b < fetched[h]; ++b)
+          drain(&st.sfull[h * p.n_slab + b], (uint32_t)(((fetched[h] - 1 - b) / p.n_slab) & 1));
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- products
+    const uint32_t ida = instr_desc(128, 3 * p.rp, 1, 1), idx = instr_desc(128, kCols, 0, 1);
+    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      int4 ch;
+      int c0;
+      if (!unit_of(u, ch, c0)) continue;
+      const int ub = unit & 1;
+      const uint32_t acc = tmem + 2 * kCols + ub * Z::kAcc, vb = smem_u32(vs + ub * Z::kV);
+      ok = wait(&st.abort, &st.vfull[ub], (uint32_t)((unit / 2) & 1), p.plan.status, kRoleFull);
+      if (ok && unit >= 2) ok = wait(&st.abort, &st.aempty[ub], (uint32_t)((unit / 2 - 1) & 1), p.plan.status, kRoleAcc);
+      for (int r0 = 0; r0 < ch.z; r0 += kTileRows, ++step) {
+        const int s = step & 1;   // stage and set
+        if (ok) ok = wait(&st.abort, &st.ready[s], (uint32_t)((step / 2) & 1), p.plan.status, kRoleFull);
+        if (ok && step >= 2) ok = wait(&st.abort, &st.dempty[s], (uint32_t)((step / 2 - 1) & 1), p.plan.status, kRoleAcc);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t xs = smem_u32(smem + s * Z::kStage), ps = xs + 32768;
+          const int per = p.rp / 16;
+          int ks = 0;
+          for (int part = 0; part < p.nparts; ++part)
+            for (int kb = 0; kb < per; ++kb, ++ks)
+              tc_mma(tmem + s * kCols, smem_desc(ps + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
+                     smem_desc(vb + kb * 2048, (uint32_t)p.rp * 128, 1024), idx, ks > 0 ? 1u : 0u);
+          tc_commit(smem_u32(&st.dfull[s]));
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma(acc, smem_desc(xs + k * 2048, 16384, 1024), smem_desc(ps + k * 2048, 16384, 1024), ida,
+                   (r0 > 0 || k > 0) ? 1u : 0u);
+          tc_commit(smem_u32(&st.empty[s]));
+          if (r0 + kTileRows >= ch.z) {
+            tc_commit(smem_u32(&st.vempty[ub]));
+            tc_commit(smem_u32(&st.afull[ub]));
+          }
+        }
+        __syncwarp();
+      }
+      ++unit;
+    }
+    // the last products have ended before TMEM is freed
+    if (step > 0 && lane == 0) drain(&st.empty[(step - 1) & 1], (uint32_t)(((step - 1) / 2) & 1));
+    __syncwarp();
+  } else if (warp >= 12) {
+    // ---- masks: thread i takes half a row of a tile
+    const Mask mask(p.rng, p.threshold);
+    const int id = tid - 384, row = id >> 1, half = id & 1;
+    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      int4 ch;
+      int c0;
+      if (!unit_of(u, ch, c0)) continue;
+      int64_t t = row < ch.z ? p.plan.token(ch.y + row) : 0;
+      for (int r0 = 0; r0 < ch.z; r0 += kTileRows, ++step) {
+        const int s = step & 1, buf = s * 2 + (step >> 1 & 1);
+        const uint64_t first = (uint64_t)(t * (p.d >> 3) + (c0 >> 3) + half * 8);
+        const int next = r0 + kTileRows + row;
+        t = next < ch.z ? p.plan.token(ch.y + next) : 0;
+        uint8_t *xs = smem + s * Z::kStage + half * 16384;
+        uint32_t bits[2] = {0, 0};
+        // a short loop: unrolled whole, its instructions and the sets' threw each
+        // other out of the cache, a third of all stalls
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w = mask.words(first + i), x = mask.words(first + 4 + i);
+          bits[0] |= Mask::bits(w) << (8 * i);
+          bits[1] |= Mask::bits(x) << (8 * i);
+          if (i == 0) {
+            ok = __all_sync(0xffffffffu, wait(&st.abort, &st.full[s], (uint32_t)((step / 2) & 1), p.plan.status, kRoleReady));
+            if (!ok) break;
+          }
+          Mask::apply(reinterpret_cast<uint4 *>(xs + swz(row, i)), w);
+          Mask::apply(reinterpret_cast<uint4 *>(xs + swz(row, 4 + i)), x);
+        }
+        if (!ok) break;
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&st.ready[s]));
+        if (step >= 4) ok = wait(&st.abort, &st.mempty[buf], (uint32_t)((step / 4 - 1) & 1), p.plan.status, kRoleEmpty);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        reinterpret_cast<uint2 *>(st.masks[buf])[id] = make_uint2(bits[0], bits[1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&st.mfull[buf]));
+      }
+    }
+  } else if (warp >= 4) {
+    // ---- dx, and dA at a unit's end
+    const int set = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    int sn = 0, pending = -1;
+    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++unit) {
+      int4 ch;
+      int c0;
+      if (!unit_of(u, ch, c0)) {
+        --unit;
+        continue;
+      }
+      auto token = [&](int r) { return r + row < ch.z ? p.plan.token(ch.y + r + row) : int64_t(-1); };
+      int64_t next = token((step & 1) == set ? 0 : kTileRows);   // of the set's next tile
+      for (int r0 = 0; r0 < ch.z; r0 += kTileRows, ++step) {
+        if ((step & 1) != set) continue;
+        const int buf = set * 2 + (step >> 1 & 1);
+        const int64_t t = next;
+        next = token(r0 + 2 * kTileRows);
+        const int first = __shfl_sync(0xffffffffu, (int)t, 0);
+        const bool whole = __all_sync(0xffffffffu, t >= 0 && t == first + lane);   // these 32 rows leave at once
+        ok = __all_sync(0xffffffffu, wait(&st.abort, &st.mfull[buf], (uint32_t)((step / 4) & 1), p.plan.status, kRoleReady));
+        if (!ok) break;
+        uint4 bits = st.masks[buf][row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&st.mempty[buf]));
+        ok = __all_sync(0xffffffffu, wait(&st.abort, &st.dfull[set], (uint32_t)((step / 2) & 1), p.plan.status, kRoleDone));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int s = 0; s < SLABS; ++s, ++sn) {
+          const int b = set * p.n_slab + sn % p.n_slab, cs = c0 + s * PER;
+          uint8_t *slab = slabs + b * 16384;
+          ok = __all_sync(0xffffffffu, wait(&st.abort, &st.sfull[b], (uint32_t)((sn / p.n_slab) & 1), p.plan.status, kRoleSlab));
+          if (!ok) break;
+          onto_slab<TO, true>(slab, row, tmem + lanes + set * kCols + s * PER, p.factor, base != nullptr, true, bits);
+          slab_out<TO>(slab, quarter, lane, t, whole, first, &p.mo, out, p.ld, cs, p.d, st.sempty, b, pending);
+        }
+        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&st.dempty[set]));
+      }
+      if (!ok || (unit & 1) != set) continue;
+      // dA of this unit, by the set of its parity
+      ok = __all_sync(0xffffffffu, wait(&st.abort, &st.afull[set], (uint32_t)((unit / 2) & 1), p.plan.status, kRoleAcc));
+      if (!ok) break;
+      tc_fence_after();
+      float *dst = ch.w < 0 ? p.dA + (int64_t)ch.x * p.rank * p.d : p.partial + (int64_t)ch.w * p.rank * p.d;
+      const int col = c0 + row;
+      for (int r = 0; r < p.rp; r += 16) {
+        float v[16] = {};
+#pragma unroll
+        for (int part = 2; part >= 0; --part) {
+          float w[16];
+          tmem_ld16(tmem + lanes + 2 * kCols + set * Z::kAcc + part * p.rp + r, w);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += w[i];
+        }
+        if (col < p.d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (r + i < p.rank) dst[(int64_t)(r + i) * p.d + col] = p.factor * v[i];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&st.aempty[set]));
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_free(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
 // Tensor maps: 128-byte swizzle, zeros outside.
 cudaError_t map2(CUtensorMap *m, const void *base, int esize, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
   auto fn = encode_fn();
@@ -1009,7 +1413,6 @@ cudaError_t shrink(const AdapterArgs &a, ShrinkTc &p, const void *x, int64_t ld,
   return p.threshold != 0 ? shrink<WT, true>(a, p, s) : shrink<WT, false>(a, p, s);
 }
 
-constexpr int kExpandSmem = 216 * 1024;
 // out [T, d] rows ld apart; V [n, d, rank], or [n, rank, d] (VT)
 template <typename TO, bool VT>
 cudaError_t expand(const AdapterArgs &a, ExpandTc &p, const bf16 *parts, const void *V, cudaStream_t s) {
@@ -1049,7 +1452,8 @@ template <int ATOMS, bool DROP> cudaError_t wgrad(const AdapterArgs &a, const Wg
   return launch_pdl(wgrad_tc_kernel<ATOMS, DROP>, dim3((unsigned)(p.blocks[0] + p.blocks[1]), (unsigned)host_chunks(a)),
                     dim3(DROP ? 320 : 192), smem, s, p);
 }
-cudaError_t wgrad(const AdapterArgs &a, const bf16 *u, const bf16 *du, cudaStream_t s) {
+// dA and dB, or (dA_too false) dB alone
+cudaError_t wgrad(const AdapterArgs &a, const bf16 *u, const bf16 *du, bool dA_too, cudaStream_t s) {
   const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
   WgradTc p{};
   p.plan = plan_of(a);
@@ -1076,12 +1480,42 @@ cudaError_t wgrad(const AdapterArgs &a, const bf16 *u, const bf16 *du, cudaStrea
   p.job[1].transposed = 1;
   p.job[1].scale = a.scale;
   p.job[1].factor = 1.0f;
+  if (!dA_too) p.blocks[0] = 0;
   const int atoms = (3 * p.rp + 63) / 64;
-  if (a.threshold != 0)
+  if (a.threshold != 0 && dA_too)
     return atoms == 1 ? wgrad<1, true>(a, p, s) : atoms == 2 ? wgrad<2, true>(a, p, s)
            : atoms == 3 ? wgrad<3, true>(a, p, s) : wgrad<6, true>(a, p, s);
   return atoms == 1 ? wgrad<1, false>(a, p, s) : atoms == 2 ? wgrad<2, false>(a, p, s)
          : atoms == 3 ? wgrad<3, false>(a, p, s) : wgrad<6, false>(a, p, s);
+}
+
+template <int ATOMS, typename TO> cudaError_t both(const AdapterArgs &a, const bf16 *du, cudaStream_t s) {
+  using Z = BothSize<ATOMS>;
+  constexpr int esize = sizeof(TO);
+  const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
+  BothTc p{};
+  p.plan = plan_of(a);
+  p.base = a.dx_in; p.out = a.dx; p.ld = a.d_in; p.d = a.d_in; p.rank = a.rank; p.rp = padded_rank(a.rank);
+  p.nparts = esize == 4 ? 3 : 2;
+  p.n_slab = (Z::kSlabs < kMaxRing ? Z::kSlabs : kMaxRing) / 2;
+  static_assert(Z::kSlabs >= 4, "two slabs a set");
+  p.threshold = a.threshold; p.rng = a.rng; p.factor = drop_scale(a.threshold);
+  p.dA = a.dA;
+  p.partial = reinterpret_cast<float *>(a.ws + sc.dA);
+  const int64_t d = a.d_in;
+  cudaError_t e = map2(&p.mx, a.x, 2, d, a.T, a.ld_in, 32);
+  if (e == cudaSuccess) e = map2(&p.mx_row, a.x, 2, d, a.T, a.ld_in, 1);
+  if (e == cudaSuccess) e = map2(&p.mp, du, 2, 3 * p.rp, a.T, 3 * p.rp, kTileRows);
+  if (e == cudaSuccess) e = map2(&p.mp_row, du, 2, 3 * p.rp, a.T, 3 * p.rp, 1);
+  if (e == cudaSuccess) e = map3(&p.mv, a.A, d, a.rank, a.n, p.rp);
+  if (e == cudaSuccess && p.base != nullptr) e = map2(&p.mb, p.base, esize, d, a.T, p.ld, 32);
+  if (e == cudaSuccess && p.base != nullptr) e = map2(&p.mb_row, p.base, esize, d, a.T, p.ld, 1);
+  if (e == cudaSuccess) e = map2(&p.mo, p.out, esize, d, a.T, p.ld, 32);
+  if (e == cudaSuccess) e = allow(both_tc_kernel<ATOMS, TO>, kExpandSmem + 1024);
+  if (e != cudaSuccess) return e;
+  const int64_t units = host_chunks(a) * ((d + kCols - 1) / kCols), sms = sm_count();
+  return launch_pdl(both_tc_kernel<ATOMS, TO>, dim3((unsigned)(units < sms ? units : sms)), dim3(kBothThreads),
+                    (size_t)kExpandSmem + 1024, s, p);
 }
 
 }  // namespace
@@ -1106,14 +1540,21 @@ cudaError_t launch_adapter_bwd_tc(const AdapterArgs &a, cudaStream_t s) {
   sh.d = a.d_out; sh.scale = a.scale; sh.factor = 1.0f; sh.parts = du;
   if (a.dA != nullptr) { sh.u_in = a.u_in; sh.parts_in = u; }
   cudaError_t e = shrink<true>(a, sh, a.dy, a.ld_out, a.B, s);
+  // dA and dx in one pass where the generator would bound two, and both tiles fit
+  const int rp = padded_rank(a.rank);
+  const bool one_pass = a.threshold != 0 && a.dA != nullptr && a.dx != nullptr && rp <= 32;
+  if (e == cudaSuccess && one_pass) {
+    if (a.dx_dtype == MOE_F32) e = rp <= 16 ? both<1, float>(a, du, s) : both<2, float>(a, du, s);
+    else e = rp <= 16 ? both<1, bf16>(a, du, s) : both<2, bf16>(a, du, s);
+  }
   if (e == cudaSuccess && a.dA != nullptr) {
-    e = wgrad(a, u, du, s);
+    e = wgrad(a, u, du, !one_pass, s);
     if (e == cudaSuccess) e = launch_adapter_join(a, s);
   }
-  if (e == cudaSuccess && a.dx != nullptr) {
+  if (e == cudaSuccess && a.dx != nullptr && !(one_pass && (a.map == nullptr || a.dx_in == a.dx))) {
     ExpandTc ex{};
     ex.base = a.dx_in; ex.out = a.dx; ex.ld = a.d_in; ex.d = a.d_in; ex.threshold = a.threshold; ex.rng = a.rng;
-    ex.factor = drop_scale(a.threshold);
+    ex.factor = drop_scale(a.threshold); ex.bare_only = one_pass;
     e = a.dx_dtype == MOE_F32 ? expand<float, true>(a, ex, du, a.A, s) : expand<bf16, true>(a, ex, du, a.A, s);
   }
   return e;
