@@ -458,7 +458,7 @@ __device__ __forceinline__ void onto_slab(uint8_t *slab, int row, uint32_t acc, 
   constexpr int PIECES = 128 / sizeof(TO) / 16;
   TmemLoad a, b;
   if (live) a.start(acc);
-#pragma unroll 1
+#pragma unroll(MASKED ? 1 : PIECES)   // beside masks a short loop, for the instruction cache
   for (int h = 0; h < PIECES; h += 2) {
     if (live) {
       a.end();
