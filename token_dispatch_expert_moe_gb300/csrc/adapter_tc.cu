@@ -832,13 +832,16 @@ struct WgradTc {
   const uint64_t *rng;
 };
 
-// ATOMS: 64-column boxes of the parts, three parts of up to ATOMS * 64 / 3 columns
+// ATOMS: 64-column boxes of the three parts of 16, 32, 64 or 128 columns. At 16
+// one product covers the parts, in two accumulators in turn. Beyond, where that
+// would cost CTAs, the first part alone takes turns over two and the other two,
+// which weigh 2^-8 of it, share the third: chains half as long in the same TMEM
+// (32768 tokens, rank 128: 2.5e-6 of dA off with one chain of 128 additions).
 template <int ATOMS, bool DROP> struct WgradSize {
   static constexpr int kStage = 16384 + 8192 * ATOMS;
   static constexpr int kCtas = ATOMS == 1 ? (DROP ? 3 : 4) : ATOMS == 2 ? 3 : ATOMS == 3 ? 2 : 1;
   static constexpr int kStages = ATOMS == 6 || (ATOMS == 1 && DROP) ? 3 : 2;
-  static constexpr int kAccCols = ATOMS == 1 ? 64 : ATOMS == 2 ? 128 : ATOMS == 3 ? 256 : 512;
-  static constexpr int kAcc = ATOMS == 1 ? 2 : 1;
+  static constexpr int kTmem = ATOMS <= 2 ? 128 : ATOMS == 3 ? 256 : 512;
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
 };
 struct WgradShared {
@@ -877,7 +880,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
   const WgradJob &job = p.job[j];
   const int c0 = (bx < 2 * both ? bx >> 1 : bx - both) * kCols;
   const bool drops = DROP && job.threshold != 0;
-  if (warp == 1) tmem_alloc(&st.tmem, Z::kAcc * Z::kAccCols);
+  if (warp == 1) tmem_alloc(&st.tmem, Z::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -921,9 +924,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
       for (int s = 0; s < NST && s < i; ++s) drain(&st.full[s], (uint32_t)(((i - 1 - s) / NST) & 1));
     __syncwarp();
   } else if (warp == 1) {
-    // three parts beside one another; beyond 256 columns the third on its own
-    const int n1 = 3 * p.rp <= 256 ? 3 * p.rp : 2 * p.rp;
-    const uint32_t id1 = instr_desc(128, n1, 1, 1), id2 = instr_desc(128, p.rp, 1, 1);
+    const uint32_t idesc = instr_desc(128, ATOMS == 1 ? 48 : p.rp, 1, 1);
     for (int i = 0; i < steps; ++i) {
       const int s = i % NST;
       if (!__all_sync(0xffffffffu, wait(&st.abort, drops ? &st.ready[s] : &st.full[s], (uint32_t)((i / NST) & 1),
@@ -931,14 +932,22 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
         break;
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t zs = smem_u32(smem + s * Z::kStage), ps = zs + 16384;
-        const uint32_t acc = tmem + (uint32_t)(i % Z::kAcc) * Z::kAccCols, more = i >= Z::kAcc;
+        const uint32_t zs = smem_u32(smem + s * Z::kStage), ps = zs + 16384, turn = i & 1;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           const uint64_t ad = smem_desc(zs + ks * 2048, 8192, 1024);
-          tc_mma(acc, ad, smem_desc(ps + ks * 2048, 8192, 1024), id1, more || ks > 0);
-          if (n1 < 3 * p.rp)
-            tc_mma(acc + n1, ad, smem_desc(ps + (n1 / 64) * 8192 + ks * 2048, 8192, 1024), id2, more || ks > 0);
+          if constexpr (ATOMS == 1) {
+            tc_mma(tmem + turn * 64, ad, smem_desc(ps + ks * 2048, 8192, 1024), idesc, i >= 2 || ks > 0);
+          } else {
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+              // columns part rp on: a box of 64 columns is 8192 bytes, a column 2
+              const int col = part * p.rp;
+              const uint64_t bd = smem_desc(ps + (col >> 6) * 8192 + (col & 63) * 2 + ks * 2048, 8192, 1024);
+              tc_mma(tmem + (part == 0 ? turn : 2) * p.rp, ad, bd, idesc,
+                     part == 0 ? i >= 2 || ks > 0 : i > 0 || ks > 0 || part == 2);
+            }
+          }
         }
         tc_commit(smem_u32(&st.empty[s]));
       }
@@ -974,17 +983,20 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
   if (warp >= 2 && warp < 6 && st.abort == 0) {
     const float f = job.factor * (job.scale != nullptr ? job.scale[ch.x] : 1.0f);
     float *out = ch.w < 0 ? job.out + (int64_t)ch.x * p.rank * job.d : job.partial + (int64_t)ch.w * p.rank * job.d;
-    const int quarter = warp & 3, col = c0 + quarter * 32 + lane, accs = min(steps, Z::kAcc);
+    const int quarter = warp & 3, col = c0 + quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     for (int r = 0; r < p.rp; r += 16) {
+      // smallest first; the second turn's accumulator holds nothing after one step
       float v[16] = {};
-      for (int a = 0; a < accs; ++a)
 #pragma unroll
-        for (int part = 2; part >= 0; --part) {
-          float w[16];
-          tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + a * Z::kAccCols + part * p.rp + r, w);
+      for (int k = ATOMS == 1 ? 5 : 2; k >= 0; --k) {
+        const bool second = ATOMS == 1 ? k >= 3 : k == 1;
+        if (second && steps == 1) continue;
+        float w[16];
+        tmem_ld16(lanes + (ATOMS == 1 ? (k / 3) * 64 + (k % 3) * 16 : k * p.rp) + r, w);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += w[i];
-        }
+        for (int i = 0; i < 16; ++i) v[i] += w[i];
+      }
       if (col < job.d) {
         if (job.transposed) {   // a thread's values lie side by side
 #pragma unroll
@@ -1003,7 +1015,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_free(tmem, Z::kAcc * Z::kAccCols);
+  if (warp == 1) tmem_free(tmem, Z::kTmem);
 }
 
 // ---------------------------------------------------------------------------
@@ -1034,7 +1046,10 @@ template <int ATOMS> struct BothSize {
   static constexpr int kStage = 32768 + 16384 * ATOMS;
   static constexpr int kStages = 2;
   static constexpr int kV = ATOMS * 16 * 256;           // A's rows of 128 columns: rank up to 16 ATOMS
-  static constexpr int kAcc = ATOMS * 64;               // columns of TMEM of dA
+  // dA in TMEM: the tiles take turns over two accumulators, of two units as long
+  // as that fits beside dx's 256 columns
+  static constexpr int kAcc = ATOMS * 64;
+  static constexpr int kUnits = ATOMS == 1 ? 2 : 1;
   static constexpr int kSlabs = (kExpandSmem - kStages * kStage - 2 * kV) / 16384;
 };
 struct BothShared {
@@ -1083,7 +1098,7 @@ __global__ void __launch_bounds__(kBothThreads, 1) both_tc_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = st.tmem;   // dx of set 0 and 1, then dA of even and odd units
+  const uint32_t tmem = st.tmem;   // dx of set 0 and 1, then dA of the unit, or of even and odd units
   const TO *base = static_cast<const TO *>(p.base);
   TO *out = static_cast<TO *>(p.out);
   const int blocks = (p.d + kCols - 1) / kCols;
@@ -1191,10 +1206,10 @@ __global__ void __launch_bounds__(kBothThreads, 1) both_tc_kernel(const __grid_c
       int4 ch;
       int c0;
       if (!unit_of(u, ch, c0)) continue;
-      const int ub = unit & 1;
-      const uint32_t acc = tmem + 2 * kCols + ub * Z::kAcc, vb = smem_u32(vs + ub * Z::kV);
-      ok = wait(&st.abort, &st.vfull[ub], (uint32_t)((unit / 2) & 1), p.plan.status, kRoleFull);
-      if (ok && unit >= 2) ok = wait(&st.abort, &st.aempty[ub], (uint32_t)((unit / 2 - 1) & 1), p.plan.status, kRoleAcc);
+      const int ub = unit % Z::kUnits, use = unit / Z::kUnits;
+      const uint32_t vb = smem_u32(vs + (unit & 1) * Z::kV);
+      ok = wait(&st.abort, &st.vfull[unit & 1], (uint32_t)((unit / 2) & 1), p.plan.status, kRoleFull);
+      if (ok && use > 0) ok = wait(&st.abort, &st.aempty[ub], (uint32_t)((use - 1) & 1), p.plan.status, kRoleAcc);
       for (int r0 = 0; r0 < ch.z; r0 += kTileRows, ++step) {
         const int s = step & 1;   // stage and set
         if (ok) ok = wait(&st.abort, &st.ready[s], (uint32_t)((step / 2) & 1), p.plan.status, kRoleFull);
@@ -1210,13 +1225,14 @@ __global__ void __launch_bounds__(kBothThreads, 1) both_tc_kernel(const __grid_c
               tc_mma(tmem + s * kCols, smem_desc(ps + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024),
                      smem_desc(vb + kb * 2048, (uint32_t)p.rp * 128, 1024), idx, ks > 0 ? 1u : 0u);
           tc_commit(smem_u32(&st.dfull[s]));
+          const uint32_t acc = tmem + 2 * kCols + (ub * 2 + (r0 / kTileRows & 1)) * Z::kAcc;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             tc_mma(acc, smem_desc(xs + k * 2048, 16384, 1024), smem_desc(ps + k * 2048, 16384, 1024), ida,
-                   (r0 > 0 || k > 0) ? 1u : 0u);
+                   (r0 >= 2 * kTileRows || k > 0) ? 1u : 0u);
           tc_commit(smem_u32(&st.empty[s]));
           if (r0 + kTileRows >= ch.z) {
-            tc_commit(smem_u32(&st.vempty[ub]));
+            tc_commit(smem_u32(&st.vempty[unit & 1]));
             tc_commit(smem_u32(&st.afull[ub]));
           }
         }
@@ -1311,22 +1327,24 @@ __global__ void __launch_bounds__(kBothThreads, 1) both_tc_kernel(const __grid_c
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&st.dempty[set]));
       }
-      if (!ok || (unit & 1) != set) continue;
-      // dA of this unit, by the set of its parity
-      ok = __all_sync(0xffffffffu, wait(&st.abort, &st.afull[set], (uint32_t)((unit / 2) & 1), p.plan.status, kRoleAcc));
+      if (!ok || unit % Z::kUnits != set) continue;
+      // dA of this unit, by the set of its accumulators: one set sees all their phases
+      ok = __all_sync(0xffffffffu, wait(&st.abort, &st.afull[set], (uint32_t)((unit / Z::kUnits) & 1), p.plan.status, kRoleAcc));
       if (!ok) break;
       tc_fence_after();
       float *dst = ch.w < 0 ? p.dA + (int64_t)ch.x * p.rank * p.d : p.partial + (int64_t)ch.w * p.rank * p.d;
       const int col = c0 + row;
       for (int r = 0; r < p.rp; r += 16) {
         float v[16] = {};
+#pragma unroll 1
+        for (int a = 0; a < (ch.z > kTileRows ? 2 : 1); ++a)
 #pragma unroll
-        for (int part = 2; part >= 0; --part) {
-          float w[16];
-          tmem_ld16(tmem + lanes + 2 * kCols + set * Z::kAcc + part * p.rp + r, w);
+          for (int part = 2; part >= 0; --part) {
+            float w[16];
+            tmem_ld16(tmem + lanes + 2 * kCols + (set * 2 + a) * Z::kAcc + part * p.rp + r, w);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += w[i];
-        }
+            for (int i = 0; i < 16; ++i) v[i] += w[i];
+          }
         if (col < p.d)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -1374,12 +1392,15 @@ template <typename K> cudaError_t allow(K kernel, size_t smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
-// CTAs a tile: several waves of two an SM, as long as each has eight steps, so
-// that the last wave weighs little; where tiles are few, down to four steps.
+// CTAs a tile: three an SM, as long as each has eight steps, or with dropout,
+// where the generator bounds them, six, so that the last wave weighs little
+// (16384 x 6144, rank 64: 142 us for the whole call against 158 us with six;
+// 32768 x 8192, rank 16, dropout: 346 us against 368 us with three); where tiles
+// are few, down to four steps.
 void set_split(const AdapterArgs &a, ShrinkTc &p) {
-  const int64_t tiles = host_tiles(a), all = (p.d + 63) / 64, sms = sm_count();
+  const int64_t tiles = host_tiles(a), all = (p.d + 63) / 64, sms = sm_count(), want = (p.threshold != 0 ? 6 : 3) * sms;
   p.split = 1;
-  while (p.split < 8 && ((tiles * p.split < 6 * sms && all / (p.split * 2) >= 8) ||
+  while (p.split < 8 && ((tiles * p.split < want && all / (p.split * 2) >= 8) ||
                          (tiles * p.split < sms && all / (p.split * 2) >= 4)))
     p.split *= 2;
   p.per = (int)((all + p.split - 1) / p.split);
