@@ -368,3 +368,38 @@ def test_past_32_bits():
         L.moe_adapter(s, x, A, B, None, ids, map, rng_tensor(SEED, OFFSET), None, y, None, ws)
         within("y", y, want, bound)
     assert L.moe_get_status(ws)[0] == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("order", ["packed", "mixed", "one"])
+@pytest.mark.parametrize("rank", [8, 16])
+def test_long_batches_with_dropout(order, rank):
+    """From 8192 tokens on dA and a bf16 dx are made in one pass: chunks of several tiles, ragged ends, columns past the
+    last whole block, bare rows with and without a base and in place."""
+    T, d_in, d_out, n = 8705, 264, 72, 5
+    t = torch.arange(T)
+    ids = {"packed": (t * 7 // T).clamp_max(5) - 1, "mixed": None, "one": torch.zeros(T)}[order]
+    b = Batch(T, d_in, d_out, 1 if order == "one" else n, rank, BF16, 0.25, bare=0.3, ids=ids)
+    b.check_forward()
+    got = b.check_backward(BF16, map=order != "one")
+    b.check_backward(BF16, dx_in=False, map=order != "one")
+    g = torch.randn(T, d_in, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(BF16)
+    over, dA, dB = g.clone(), b.new(*b.A.shape), b.new(*b.B.shape)
+    b.L.moe_adapter_bwd(b.shape, b.L.MOE_BF16, b.dy, b.x, b.A, b.B, b.scale, None if order == "one" else b.map, b.rng, b.u, over,
+                        over, dA, dB, b.ws)
+    assert torch.equal(over, got["dx"]) and torch.equal(dA, got["dA"]) and torch.equal(dB, got["dB"])
+    assert b.status() == 0
+    # dA is the one of the two separate passes within the bounds, dx without dA bit for bit
+    alone = b.new(T, d_in, dt=BF16)
+    b.L.moe_adapter_bwd(b.shape, b.L.MOE_BF16, b.dy, b.x, b.A, b.B, b.scale, None if order == "one" else b.map, b.rng, b.u, g,
+                        alone, None, None, b.ws)
+    assert torch.equal(alone, got["dx"])
+    b.check_backward(F32, map=order != "one")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,n,rank", [(20000, 1, 64), (9000, 200, 128), (16500, 3, 40)])
+def test_long_batches(T, n, rank):
+    b = Batch(T, 136, 200, n, rank, BF16, 0.0, bare=0.1)
+    b.check_forward()
+    b.check_backward(BF16)
