@@ -542,10 +542,13 @@ moe_status_t moe_adapter_map(const moe_adapter_shape_t *shape, const int32_t *ad
  *   kept for the backward; rng: see above, for the dense [T, d_in] matrix.
  *   The tokens' adapters: map; or map NULL and adapter_of, row by row; or both
  *   NULL: adapter 0 for all of them. adapter_of is not read beside a map.
- * In bf16 the products run on the tensor cores with u held in two bf16 parts
- * (2^-17 of it), accumulated in fp32. No output overlaps another, an input or
- * ws, but columns of one wider matrix may be x here and y there.
- * Errors: a map of another T or n records MOE_ERR_DEVICE and leaves rows out.   */
+ * In bf16 the tiles' products run on the tensor cores, accumulated in fp32; u
+ * goes into the second one as bf16 parts, two (2^-16 of the product is left out)
+ * where the result is bf16, three (2^-24) where it is fp32, so that an infinite u
+ * gives NaN. No output overlaps another, an input or ws, but columns of one wider
+ * matrix may be x here and y there.
+ * Errors: a map of another T or n, or words in it that moe_adapter_map has not
+ * written, record MOE_ERR_DEVICE and leave rows out.                             */
 moe_status_t moe_adapter(const moe_adapter_shape_t *shape, const void *x, const void *A,
                          const void *B, const float *scale, const int32_t *adapter_of,
                          const void *map, const uint64_t *rng, const void *base, void *y, float *u,
