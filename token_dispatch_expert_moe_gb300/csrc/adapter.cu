@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(int64_t T, int n, int 
 
   for (int i = tid; i < runs * bins; i += kMapThreads) hist[i] = 0;
   pdl_wait();
+  pdl_trigger();
   // the bin of token t; -1 past the run
   auto bin = [&](int64_t t) {
     if (t >= hi) return -1;
@@ -248,6 +249,7 @@ constexpr int kRowCtas = 8, kRowThreads = 256;
 template <typename T, bool DROP>
 __global__ void __launch_bounds__(kRowThreads, DROP ? 2 : 4) row_kernel(const AdapterArgs a, float keep_scale) {
   pdl_wait();
+  pdl_trigger();
   __shared__ float part[128], us[128];
   const int64_t t = blockIdx.x / kRowCtas;
   const int q = (int)cluster_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -370,6 +372,7 @@ struct Shrink {   // v[pos] = factor W_a drop(x[token]), W_a [rank, d], or [d, r
 template <typename T, bool WT>
 __global__ void __launch_bounds__(kSimtThreads) shrink_kernel(const Shrink p) {
   pdl_wait();
+  pdl_trigger();
   __shared__ __align__(16) float xs[kSimtRows * kPad];
   __shared__ __align__(16) float ws[128 * kPad];
   __shared__ int64_t tok[kSimtRows];
@@ -467,6 +470,7 @@ constexpr int kExpandCols = 128;
 template <typename T, typename TO, bool VT>
 __global__ void __launch_bounds__(kSimtThreads) expand_kernel(const Expand p) {
   pdl_wait();
+  pdl_trigger();
   __shared__ __align__(16) float us[kSimtRows][36];
   __shared__ __align__(16) float wt[32][kExpandCols + 4];
   __shared__ int64_t tok[kSimtRows];
@@ -558,6 +562,7 @@ constexpr int kGradCols = 64;
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) wgrad_kernel(const Wgrad all) {
   pdl_wait();
+  pdl_trigger();
   const WgradJob &p = all.job[blockIdx.z];
   if ((int)blockIdx.y * kGradCols >= p.d) return;
   __shared__ __align__(16) float buf[256 / 2 * 64];   // 32 KB: 32 rows of z and of v, then the sets' sums
@@ -630,6 +635,7 @@ constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(Plan plan, int64_t na, int64_t nb, float *dA, float *dB,
                                                             const float *pa, const float *pb) {
   pdl_wait();
+  pdl_trigger();
   if (!plan.of_this_batch()) return;
   const int a = blockIdx.y;
   const int2 g = plan.group(a);

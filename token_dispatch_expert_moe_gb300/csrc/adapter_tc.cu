@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP, 
     fence_proxy_async();
   }
   pdl_wait();
+  pdl_trigger();
   const int64_t ti = blockIdx.x / p.split;
   const int q = (int)(blockIdx.x % p.split);   // the CTA's rank in its cluster
   const int4 tile = p.plan.tile_of(ti);
@@ -584,6 +585,7 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
   }
   if (warp == 1) tmem_alloc(&st.tmem, 4 * kCols);
   pdl_wait();
+  pdl_trigger();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -872,6 +874,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
     fence_proxy_async();
   }
   pdl_wait();
+  pdl_trigger();
   const int4 ch = p.plan.chunk_of(blockIdx.y);
   if (ch.z <= 0) return;
   // block by block in turn while both jobs have some
@@ -1087,6 +1090,7 @@ __global__ void __launch_bounds__(kBothThreads, 1) both_tc_kernel(const __grid_c
   }
   if (warp == 1) tmem_alloc(&st.tmem, 512);
   pdl_wait();
+  pdl_trigger();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
