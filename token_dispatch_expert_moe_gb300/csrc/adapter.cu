@@ -205,26 +205,13 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(int64_t T, int n, int 
 }
 
 // ---------------------------------------------------------------------------
-// Elements in fours: 16 bytes of fp32, 8 of bf16.
+// Elements in fours.
 __device__ __forceinline__ void load4(const float *p, float (&v)[4]) {
   const float4 q = *reinterpret_cast<const float4 *>(p);
   v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&v)[4]) {
-  const uint2 q = *reinterpret_cast<const uint2 *>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q.y));
-  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-}
 __device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
   *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4]) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-  uint2 q;
-  q.x = *reinterpret_cast<const uint32_t *>(&a);
-  q.y = *reinterpret_cast<const uint32_t *>(&b);
-  *reinterpret_cast<uint2 *>(p) = q;
 }
 // zeros in the dropped ones' place; i: index of the first in the dense matrix, a multiple of 4
 __device__ __forceinline__ void mask4(const Philox &g, int64_t i, float (&v)[4]) {
@@ -351,16 +338,23 @@ __global__ void __launch_bounds__(kRowThreads, DROP ? 2 : 4) row_kernel(const Ad
 }
 
 // ---------------------------------------------------------------------------
-// Tiles on the CUDA cores.
+// Tiles on the CUDA cores, for fp32 shapes: the type of the checking cases, whose
+// products want all 24 bits. Bound by the multiplications and the latency of
+// their steps (8192 x 4096, rank 16: 227 us forward, 60 us of bytes and 29 us of
+// multiplications). 64 registers for four CTAs an SM, though the generator's keys
+// then spill: without that bound 280 us, and 281 instead of 243 us with dropout.
 constexpr int kSimtThreads = 256;
 constexpr int kSimtRows = 32;   // positions a CTA: a quarter of a tile
 constexpr int kStep = 64, kPad = kStep + 4;
 
+// A cluster of `split` CTAs takes 32 rows; each runs through a part of the width,
+// and the sums meet in shared memory, added in the CTAs' order.
 struct Shrink {   // v[pos] = factor W_a drop(x[token]), W_a [rank, d], or [d, rank] (WT)
   Plan plan;
-  const void *x, *W;
+  const float *x, *W;
   int64_t ld;
   int d, rank;
+  int split, per;       // CTAs for the same rows, columns each (a multiple of kStep)
   uint32_t threshold;
   const uint64_t *rng;
   const float *scale;   // per adapter, or NULL
@@ -369,37 +363,39 @@ struct Shrink {   // v[pos] = factor W_a drop(x[token]), W_a [rank, d], or [d, r
   float *by_token;      // [T, rank], or NULL; 0 without an adapter
 };
 
-template <typename T, bool WT>
-__global__ void __launch_bounds__(kSimtThreads) shrink_kernel(const Shrink p) {
+template <bool WT>
+__global__ void __launch_bounds__(kSimtThreads, 4) shrink_kernel(const Shrink p) {
   pdl_wait();
   pdl_trigger();
   __shared__ __align__(16) float xs[kSimtRows * kPad];
   __shared__ __align__(16) float ws[128 * kPad];
   __shared__ int64_t tok[kSimtRows];
-  const int4 tile = p.plan.tile_of(blockIdx.x / 4);
-  const int r0 = (int)(blockIdx.x % 4) * kSimtRows, rows = min(kSimtRows, tile.z - r0), tid = threadIdx.x;
-  if (rows <= 0) return;
+  const int q = (int)(blockIdx.x % p.split);   // the CTA's rank in its cluster
+  const int64_t part = blockIdx.x / p.split;
+  const int4 tile = p.plan.tile_of(part / 4);
+  const int r0 = (int)(part % 4) * kSimtRows, rows = min(kSimtRows, tile.z - r0), tid = threadIdx.x;
+  if (rows <= 0) return;   // the whole cluster
   if (tid < kSimtRows) tok[tid] = tid < rows ? p.plan.token(tile.y + r0 + tid) : -1;
   __syncthreads();
   const int r = p.rank;
-  if (tile.x < 0) {
-    if (p.by_token != nullptr)
+  if (tile.x < 0) {   // the whole cluster
+    if (p.by_token != nullptr && q == 0)
       for (int i = tid; i < rows * r; i += kSimtThreads) p.by_token[tok[i / r] * r + i % r] = 0.0f;
     return;
   }
-  const T *W = static_cast<const T *>(p.W) + (int64_t)tile.x * r * p.d;
-  const T *x = static_cast<const T *>(p.x);
+  const float *W = p.W + (int64_t)tile.x * r * p.d;
   const Philox g(p.rng, p.threshold);
   // 4 x 4 results a thread; the threads beyond one set of them share the steps' k
   const int set = 8 * (r / 4), sets = kSimtThreads / set, mine = tid / set, at = tid % set;
   const int jr = (at % (r / 4)) * 4, rr = (at / (r / 4)) * 4;
+  const int end = min(p.d, (q + 1) * p.per);
   float acc[4][4] = {};
-  for (int k0 = 0; k0 < p.d; k0 += kStep) {
+  for (int k0 = q * p.per; k0 < end; k0 += kStep) {
     for (int i = tid; i < kSimtRows * (kStep / 4); i += kSimtThreads) {
       const int row = i / (kStep / 4), k = (i % (kStep / 4)) * 4;
       float v[4] = {};
       if (tok[row] >= 0 && k0 + k < p.d) {
-        load4(x + tok[row] * p.ld + k0 + k, v);
+        load4(p.x + tok[row] * p.ld + k0 + k, v);
         if (p.threshold != 0) mask4(g, tok[row] * p.d + k0 + k, v);
       }
       store4(xs + row * kPad + k, v);
@@ -439,25 +435,36 @@ __global__ void __launch_bounds__(kSimtThreads) shrink_kernel(const Shrink p) {
     __syncthreads();
   }
   // sets in order: [set][row][rank] in ws (at most 256 / set sets of 32 rank floats)
-  if (mine < sets)
+  if (mine < sets) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) store4(ws + (mine * kSimtRows + rr + i) * r + jr, acc[i]);
+  }
   __syncthreads();
+  const int all = kSimtRows * r;
+  for (int i = tid; i < all; i += kSimtThreads) {   // into the first set's place, which no other thread reads
+    float v = ws[i];
+    for (int c = 1; c < sets; ++c) v += ws[c * all + i];
+    ws[i] = v;
+  }
+  if (p.split > 1) cluster_meet();
+  else __syncthreads();
   const float f = p.factor * (p.scale != nullptr ? p.scale[tile.x] : 1.0f);
-  for (int i = tid; i < rows * r; i += kSimtThreads) {
+  const int share = all / p.split;   // split is at most 8, all a multiple of 128
+  for (int i = q * share + tid; i < (q + 1) * share && i < rows * r; i += kSimtThreads) {
     float v = 0.0f;
-    for (int c = 0; c < sets; ++c) v += ws[c * kSimtRows * r + i];
+    for (int c = 0; c < p.split; ++c) v += p.split > 1 ? remote_float(ws + i, (uint32_t)c) : ws[i];
     v *= f;
-    if (p.by_pos != nullptr) p.by_pos[(int64_t)(tile.y + r0) * r + i] = v;
+    p.by_pos[(int64_t)(tile.y + r0) * r + i] = v;
     if (p.by_token != nullptr) p.by_token[tok[i / r] * r + i % r] = v;
   }
+  if (p.split > 1) cluster_meet();   // no CTA leaves while another reads its sums
 }
 
 struct Expand {   // out[token] = base[token] + factor mask(V_a v[pos]), V_a [d, rank], or [rank, d] (VT)
   Plan plan;
   const float *v;   // [T, rank] by position
-  const void *V, *base;
-  void *out;
+  const float *V, *base;
+  float *out;
   int64_t ld;
   int d, rank;
   uint32_t threshold;
@@ -467,7 +474,7 @@ struct Expand {   // out[token] = base[token] + factor mask(V_a v[pos]), V_a [d,
 };
 constexpr int kExpandCols = 128;
 
-template <typename T, typename TO, bool VT>
+template <bool VT>
 __global__ void __launch_bounds__(kSimtThreads) expand_kernel(const Expand p) {
   pdl_wait();
   pdl_trigger();
@@ -477,8 +484,8 @@ __global__ void __launch_bounds__(kSimtThreads) expand_kernel(const Expand p) {
   const int4 tile = p.plan.tile_of(blockIdx.x / 4);
   const int r0 = (int)(blockIdx.x % 4) * kSimtRows, rows = min(kSimtRows, tile.z - r0), tid = threadIdx.x;
   if (rows <= 0) return;
-  const TO *base = static_cast<const TO *>(p.base);
-  TO *out = static_cast<TO *>(p.out);
+  const float *base = p.base;
+  float *out = p.out;
   if (tile.x < 0 && base == out) return;
   if (tid < kSimtRows) tok[tid] = tid < rows ? p.plan.token(tile.y + r0 + tid) : -1;
   __syncthreads();
@@ -488,7 +495,7 @@ __global__ void __launch_bounds__(kSimtThreads) expand_kernel(const Expand p) {
   float f = 0.0f;
   if (tile.x >= 0) {
     f = p.factor * (p.scale != nullptr ? p.scale[tile.x] : 1.0f);
-    const T *V = static_cast<const T *>(p.V) + (int64_t)tile.x * r * p.d;
+    const float *V = p.V + (int64_t)tile.x * r * p.d;
     for (int j0 = 0; j0 < r; j0 += 32) {
       const int nj = min(32, r - j0);
       for (int i = tid; i < kSimtRows * 8; i += kSimtThreads) {
@@ -541,8 +548,7 @@ __global__ void __launch_bounds__(kSimtThreads) expand_kernel(const Expand p) {
 }
 
 struct WgradJob {   // G_a = factor sum_t v_t z_t^T over a chunk: [rank, d], or `transposed` [d, rank]
-  const void *z;
-  const float *v;
+  const float *z, *v;
   int v_by_token, transposed;
   int64_t ld;
   int d;
@@ -557,52 +563,55 @@ struct Wgrad {   // both gradients of a backward in one launch
   int rank;
   const uint64_t *rng;
 };
-constexpr int kGradCols = 64;
+constexpr int kGradCols = 64, kGradRows = 64;   // columns of a CTA, tokens a step
+// a step's rows of z and v, or the sets' sums (at most 16 x 8 x 64)
+size_t grad_smem(int rank) {
+  const size_t step = (size_t)kGradRows * (kGradCols + 4 + (rank + 7) / 8 * 8) * 4;
+  return step > 32768 ? step : 32768;
+}
 
-template <typename T>
-__global__ void __launch_bounds__(kSimtThreads) wgrad_kernel(const Wgrad all) {
+__global__ void __launch_bounds__(kSimtThreads, 4) wgrad_kernel(const Wgrad all) {
   pdl_wait();
   pdl_trigger();
   const WgradJob &p = all.job[blockIdx.z];
   if ((int)blockIdx.y * kGradCols >= p.d) return;
-  __shared__ __align__(16) float buf[256 / 2 * 64];   // 32 KB: 32 rows of z and of v, then the sets' sums
-  float (*zs)[kGradCols + 4] = reinterpret_cast<float(*)[kGradCols + 4]>(buf);
-  float (*vs)[128] = reinterpret_cast<float(*)[128]>(buf + 32 * (kGradCols + 4));
-  __shared__ int64_t tok[32];
+  extern __shared__ __align__(16) float buf[];
+  const int r = all.rank, r8 = (r + 7) / 8, vp = r8 * 8;
+  float *zs = buf, *vs = buf + kGradRows * (kGradCols + 4);   // rows kGradCols + 4 and vp apart
+  __shared__ int64_t tok[kGradRows];
   const int4 ch = all.plan.chunk_of(blockIdx.x);
   if (ch.z <= 0) return;
-  const int r = all.rank, r8 = (r + 7) / 8, c0 = blockIdx.y * kGradCols, tid = threadIdx.x;
+  const int c0 = blockIdx.y * kGradCols, tid = threadIdx.x;
   const int set = r8 * 16, sets = kSimtThreads / set, mine = tid / set, at = tid % set;
   const int jj = (at / 16) * 8, cc = (at % 16) * 4;
-  const T *z = static_cast<const T *>(p.z);
   const Philox g(all.rng, p.threshold);
   float acc[8][4] = {};
-  for (int i0 = 0; i0 < ch.z; i0 += 32) {
-    const int rows = min(32, ch.z - i0);
-    if (tid < 32) tok[tid] = tid < rows ? all.plan.token(ch.y + i0 + tid) : -1;
+  for (int i0 = 0; i0 < ch.z; i0 += kGradRows) {
+    const int rows = min(kGradRows, ch.z - i0);
+    if (tid < kGradRows) tok[tid] = tid < rows ? all.plan.token(ch.y + i0 + tid) : -1;
     __syncthreads();
-    for (int i = tid; i < 32 * (kGradCols / 4); i += kSimtThreads) {
+    for (int i = tid; i < kGradRows * (kGradCols / 4); i += kSimtThreads) {
       const int row = i / (kGradCols / 4), c = (i % (kGradCols / 4)) * 4;
       float v[4] = {};
       if (row < rows && c0 + c < p.d) {
-        load4(z + tok[row] * p.ld + c0 + c, v);
+        load4(p.z + tok[row] * p.ld + c0 + c, v);
         if (p.threshold != 0) mask4(g, tok[row] * p.d + c0 + c, v);
       }
-      store4(&zs[row][c], v);
+      store4(zs + row * (kGradCols + 4) + c, v);
     }
-    for (int i = tid; i < 32 * 2 * r8; i += kSimtThreads) {
+    for (int i = tid; i < kGradRows * 2 * r8; i += kSimtThreads) {
       const int row = i / (2 * r8), j = (i % (2 * r8)) * 4;
       float v[4] = {};
       if (row < rows && j < r) load4(p.v + (p.v_by_token ? tok[row] : (int64_t)(ch.y + i0 + row)) * r + j, v);
-      store4(&vs[row][j], v);
+      store4(vs + row * vp + j, v);
     }
     __syncthreads();
     if (mine < sets)
-      for (int row = mine; row < 32; row += sets) {
+      for (int row = mine; row < kGradRows; row += sets) {
         float w[4], a[4], b[4];
-        load4(&zs[row][cc], w);
-        load4(&vs[row][jj], a);
-        load4(&vs[row][jj + 4], b);
+        load4(zs + row * (kGradCols + 4) + cc, w);
+        load4(vs + row * vp + jj, a);
+        load4(vs + row * vp + jj + 4, b);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -613,9 +622,10 @@ __global__ void __launch_bounds__(kSimtThreads) wgrad_kernel(const Wgrad all) {
       }
     __syncthreads();
   }
-  if (mine < sets)
+  if (mine < sets) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) store4(buf + ((mine * r8 * 8 + jj + i) * kGradCols + cc), acc[i]);
+    for (int i = 0; i < 8; ++i) store4(buf + (mine * vp + jj + i) * kGradCols + cc, acc[i]);
+  }
   __syncthreads();
   const float f = p.factor * (p.scale != nullptr ? p.scale[ch.x] : 1.0f);
   float *out = ch.w < 0 ? p.out + (int64_t)ch.x * r * p.d : p.partial + (int64_t)ch.w * r * p.d;
@@ -623,7 +633,7 @@ __global__ void __launch_bounds__(kSimtThreads) wgrad_kernel(const Wgrad all) {
     const int j = p.transposed ? i % r : i / kGradCols, c = p.transposed ? i / r : i % kGradCols;
     if (c0 + c >= p.d) continue;
     float v = 0.0f;
-    for (int k = 0; k < sets; ++k) v += buf[(k * r8 * 8 + j) * kGradCols + c];
+    for (int k = 0; k < sets; ++k) v += buf[(k * vp + j) * kGradCols + c];
     out[p.transposed ? (int64_t)(c0 + c) * r + j : (int64_t)j * p.d + c0 + c] = f * v;
   }
 }
@@ -656,47 +666,61 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Plan plan, int64_t n
   store4((second ? dB : dA) + a * n + k, v);
 }
 
-template <typename T, bool WT>
-cudaError_t shrink(const AdapterArgs &a, const Shrink &p, cudaStream_t s) {
-  return launch_pdl(shrink_kernel<T, WT>, dim3((unsigned)(host_tiles(a) * 4)), dim3(kSimtThreads), 0, s, p);
+// CTAs for the same rows: four an SM, as long as each has four steps.
+template <bool WT> cudaError_t shrink(const AdapterArgs &a, Shrink p, cudaStream_t s) {
+  const int64_t parts = host_tiles(a) * 4, steps = (p.d + kStep - 1) / kStep;
+  p.split = 1;
+  while (p.split < 8 && parts * p.split < 4 * sm_count() && steps / (p.split * 2) >= 4) p.split *= 2;
+  p.per = (int)((steps + p.split - 1) / p.split) * kStep;
+  return launch_pdl_clusters(shrink_kernel<WT>, dim3((unsigned)(parts * p.split)), dim3(kSimtThreads), p.split, 0, s, p);
 }
-template <typename T, typename TO, bool VT>
-cudaError_t expand(const AdapterArgs &a, const Expand &p, cudaStream_t s) {
-  return launch_pdl(expand_kernel<T, TO, VT>,
+template <bool VT> cudaError_t expand(const AdapterArgs &a, const Expand &p, cudaStream_t s) {
+  return launch_pdl(expand_kernel<VT>,
                     dim3((unsigned)(host_tiles(a) * 4), (unsigned)((p.d + kExpandCols - 1) / kExpandCols)),
                     dim3(kSimtThreads), 0, s, p);
 }
-template <typename T> cudaError_t forward(const AdapterArgs &a, cudaStream_t s) {
+
+cudaError_t forward_f32(const AdapterArgs &a, cudaStream_t s) {
   const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
   float *u = reinterpret_cast<float *>(a.ws + sc.u);
-  const Plan plan = plan_of(a);
-  const Shrink sh{plan, a.x, a.A, a.ld_in, a.d_in, a.rank, a.threshold, a.rng, nullptr, drop_scale(a.threshold), u, a.u};
-  cudaError_t e = shrink<T, false>(a, sh, s);
+  Shrink sh{};
+  sh.plan = plan_of(a);
+  sh.x = static_cast<const float *>(a.x); sh.W = static_cast<const float *>(a.A); sh.ld = a.ld_in; sh.d = a.d_in;
+  sh.rank = a.rank; sh.threshold = a.threshold; sh.rng = a.rng; sh.factor = drop_scale(a.threshold);
+  sh.by_pos = u; sh.by_token = a.u;
+  cudaError_t e = shrink<false>(a, sh, s);
   if (e != cudaSuccess) return e;
-  const Expand ex{plan, u, a.B, a.base, a.y, a.ld_out, a.d_out, a.rank, 0, nullptr, a.scale, 1.0f};
-  return expand<T, T, false>(a, ex, s);
+  const Expand ex{sh.plan, u, static_cast<const float *>(a.B), static_cast<const float *>(a.base), static_cast<float *>(a.y),
+                  a.ld_out, a.d_out, a.rank, 0, nullptr, a.scale, 1.0f};
+  return expand<false>(a, ex, s);
 }
 
-template <typename T> cudaError_t backward(const AdapterArgs &a, cudaStream_t s) {
+cudaError_t backward_f32(const AdapterArgs &a, cudaStream_t s) {
   const Scratch sc = scratch_of(a.T, a.d_in, a.d_out, a.rank);
+  const float *x = static_cast<const float *>(a.x), *dy = static_cast<const float *>(a.dy);
   float *du = reinterpret_cast<float *>(a.ws + sc.du);
-  const Plan plan = plan_of(a);
   const float keep = drop_scale(a.threshold);
-  const Shrink sh{plan, a.dy, a.B, a.ld_out, a.d_out, a.rank, 0, nullptr, a.scale, 1.0f, du, nullptr};
-  cudaError_t e = shrink<T, true>(a, sh, s);
+  Shrink sh{};
+  sh.plan = plan_of(a);
+  sh.x = dy; sh.W = static_cast<const float *>(a.B); sh.ld = a.ld_out; sh.d = a.d_out; sh.rank = a.rank;
+  sh.scale = a.scale; sh.factor = 1.0f; sh.by_pos = du;
+  cudaError_t e = shrink<true>(a, sh, s);
   if (e == cudaSuccess && a.dA != nullptr) {
     Wgrad w{};
-    w.plan = plan; w.rank = a.rank; w.rng = a.rng;
-    w.job[0] = WgradJob{a.x, du, 0, 0, a.ld_in, a.d_in, a.threshold, nullptr, keep, a.dA, reinterpret_cast<float *>(a.ws + sc.dA)};
-    w.job[1] = WgradJob{a.dy, a.u_in, 1, 1, a.ld_out, a.d_out, 0, a.scale, 1.0f, a.dB, reinterpret_cast<float *>(a.ws + sc.dB)};
+    w.plan = sh.plan; w.rank = a.rank; w.rng = a.rng;
+    w.job[0] = WgradJob{x, du, 0, 0, a.ld_in, a.d_in, a.threshold, nullptr, keep, a.dA, reinterpret_cast<float *>(a.ws + sc.dA)};
+    w.job[1] = WgradJob{dy, a.u_in, 1, 1, a.ld_out, a.d_out, 0, a.scale, 1.0f, a.dB, reinterpret_cast<float *>(a.ws + sc.dB)};
     const int d = a.d_in > a.d_out ? a.d_in : a.d_out;
-    e = launch_pdl(wgrad_kernel<T>, dim3((unsigned)host_chunks(a), (unsigned)((d + kGradCols - 1) / kGradCols), 2),
-                   dim3(kSimtThreads), 0, s, w);
+    e = cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad_smem(128));
+    if (e == cudaSuccess)
+      e = launch_pdl(wgrad_kernel, dim3((unsigned)host_chunks(a), (unsigned)((d + kGradCols - 1) / kGradCols), 2),
+                     dim3(kSimtThreads), grad_smem(a.rank), s, w);
     if (e == cudaSuccess) e = launch_adapter_join(a, s);
   }
   if (e == cudaSuccess && a.dx != nullptr) {
-    const Expand ex{plan, du, a.A, a.dx_in, a.dx, a.d_in, a.d_in, a.rank, a.threshold, a.rng, nullptr, keep};
-    e = a.dx_dtype == MOE_F32 ? expand<T, float, true>(a, ex, s) : expand<T, __nv_bfloat16, true>(a, ex, s);
+    const Expand ex{sh.plan, du, static_cast<const float *>(a.A), static_cast<const float *>(a.dx_in),
+                    static_cast<float *>(a.dx), a.d_in, a.d_in, a.rank, a.threshold, a.rng, nullptr, keep};
+    e = expand<true>(a, ex, s);
   }
   return e;
 }
@@ -733,11 +757,11 @@ cudaError_t launch_adapter(const AdapterArgs &a, cudaStream_t s) {
     if (a.dtype == MOE_F32) return a.threshold != 0 ? run(row_kernel<float, true>) : run(row_kernel<float, false>);
     return a.threshold != 0 ? run(row_kernel<__nv_bfloat16, true>) : run(row_kernel<__nv_bfloat16, false>);
   }
-  return a.dtype == MOE_F32 ? forward<float>(a, s) : launch_adapter_tc(a, s);
+  return a.dtype == MOE_F32 ? forward_f32(a, s) : launch_adapter_tc(a, s);
 }
 
 cudaError_t launch_adapter_bwd(const AdapterArgs &a, cudaStream_t s) {
-  return a.dtype == MOE_F32 ? backward<float>(a, s) : launch_adapter_bwd_tc(a, s);
+  return a.dtype == MOE_F32 ? backward_f32(a, s) : launch_adapter_bwd_tc(a, s);
 }
 
 }  // namespace moe
