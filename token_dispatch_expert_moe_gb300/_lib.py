@@ -431,15 +431,19 @@ def moe_adapter_map(shape, adapter_of, map, ws, stream=None):
 
 def moe_adapter(shape, x, A, B, scale, adapter_of, map, rng, base, y, u, ws, stream=None):
     """x, base and y: dense, or slices [T, d] of wider matrices with shape.ld_in and shape.ld_out from row to row."""
-    A, B, scale, adapter_of, map, rng, u, ws = _pointers(A, B, scale, adapter_of, map, rng, u, ws)
-    x = _rows(x, shape.T, shape.d_in, shape.ld_in)
-    base, y = (_rows(t, shape.T, shape.d_out, shape.ld_out) for t in (base, y))
-    _call("moe_adapter", ctypes.byref(shape), x, A, B, scale, adapter_of, map, rng, base, y, u, ws, _stream(stream))
+    if shape.ld_in or shape.ld_out:
+        A, B, scale, adapter_of, map, rng, u, ws = _pointers(A, B, scale, adapter_of, map, rng, u, ws)
+        x = _rows(x, shape.T, shape.d_in, shape.ld_in)
+        base, y = (_rows(t, shape.T, shape.d_out, shape.ld_out) for t in (base, y))
+        args = x, A, B, scale, adapter_of, map, rng, base, y, u, ws
+    else:
+        args = _pointers(x, A, B, scale, adapter_of, map, rng, base, y, u, ws)
+    _call("moe_adapter", ctypes.byref(shape), *args, _stream(stream))
 
 
 def moe_adapter_bwd(shape, dx_dtype, dy, x, A, B, scale, map, rng, u, dx_in, dx, dA, dB, ws, stream=None):
     """dy and x: as in moe_adapter; dx_in and dx are dense."""
-    A, B, scale, map, rng, u, dx_in, dx, dA, dB, ws = _pointers(A, B, scale, map, rng, u, dx_in, dx, dA, dB, ws)
-    dy, x = _rows(dy, shape.T, shape.d_out, shape.ld_out), _rows(x, shape.T, shape.d_in, shape.ld_in)
-    _call("moe_adapter_bwd", ctypes.byref(shape), dx_dtype, dy, x, A, B, scale, map, rng, u, dx_in, dx, dA, dB, ws,
-          _stream(stream))
+    if shape.ld_in or shape.ld_out:
+        dy, x = _rows(dy, shape.T, shape.d_out, shape.ld_out), _rows(x, shape.T, shape.d_in, shape.ld_in)
+    args = _pointers(dy, x, A, B, scale, map, rng, u, dx_in, dx, dA, dB, ws)
+    _call("moe_adapter_bwd", ctypes.byref(shape), dx_dtype, *args, _stream(stream))
