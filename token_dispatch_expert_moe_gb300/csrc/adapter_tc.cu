@@ -543,7 +543,7 @@ struct ExpandTc {
   float factor;
 };
 
-// Warps 0: base, 1: products, 2: parts and V, 3: none, 4-11: the sets, 12-19: masks
+// Warps 0 and 3: base rows of set 0 and 1, 1: products, 2: parts and V, 4-11: the sets, 12-19: masks
 template <bool DROP> constexpr int expand_threads() { return DROP ? 640 : 384; }
 
 struct ExpandShared {
@@ -607,9 +607,10 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
   bool ok = true;
   int block = 0;   // blocks so far: block b is set b % 2's (b / 2)-th
 
-  if (warp == 0) {
-    // ---- base rows
-    int fetched[2] = {};   // slabs of each set
+  if (warp == 0 || warp == 3) {
+    // ---- base rows, a warp a set: gathers issue at half the rate from one
+    const int set = warp == 0 ? 0 : 1;
+    int n = 0;   // slabs so far
     for (int64_t at = begin; at < end && ok;) {
       int4 tile;
       int b0, b1;
@@ -618,31 +619,26 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
       lane_tokens(p.plan, tile.y, 4 * lane, tile.z, t);
       const RowCopy rows = row_copy(t, lane, false, true);
       for (int blk = b0; blk < b1 && ok; ++blk, ++block) {
-        const int set = block & 1;
-        for (int s = 0; s < SLABS; ++s) {
-          const int n = (block >> 1) * SLABS + s, b = set * p.n_slab + n % p.n_slab, c = blk * kCols + s * PER;
+        if ((block & 1) != set) continue;
+        for (int s = 0; s < SLABS; ++s, ++n) {
+          const int b = set * p.n_slab + n % p.n_slab, c = blk * kCols + s * PER;
           if (n >= p.n_slab)
             ok = wait(&st.abort, &st.sempty[b], (uint32_t)((n / p.n_slab - 1) & 1), p.plan.status, kRoleEmpty);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           if (base == nullptr || c >= p.d) {
             if (lane == 0) mbar_arrive(smem_u32(&st.sfull[b]));
           } else {
-            const uint32_t dst = smem_u32(slabs + b * 16384);
             if (lane == 0) mbar_expect_tx(smem_u32(&st.sfull[b]), rows.bytes);
             __syncwarp();
-            copy_rows(rows, dst, &p.mb, &p.mb_row, &st.sfull[b], c, t, lane);
+            copy_rows(rows, smem_u32(slabs + b * 16384), &p.mb, &p.mb_row, &st.sfull[b], c, t, lane);
           }
-          if (set) fetched[1] = n + 1;
-          else fetched[0] = n + 1;
         }
       }
     }
     __syncwarp();
     if (lane == 0)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        for (int b = 0; b < p.n_slab && b < fetched[h]; ++b)
-          drain(&st.sfull[h * p.n_slab + b], (uint32_t)(((fetched[h] - 1 - b) / p.n_slab) & 1));
+      for (int b = 0; b < p.n_slab && b < n; ++b)
+        drain(&st.sfull[set * p.n_slab + b], (uint32_t)(((n - 1 - b) / p.n_slab) & 1));
     __syncwarp();
   } else if (warp == 2) {
     // ---- parts and V
@@ -1043,7 +1039,7 @@ struct BothTc {
   float factor;
   float *dA, *partial;
 };
-constexpr int kBothThreads = 640;   // warps 0: x, parts and A, 1: products, 2: base, 3: none, 4-11: two sets, 12-19: masks
+constexpr int kBothThreads = 640;   // warps 0: x, parts and A, 1: products, 2 and 3: base of set 0 and 1, 4-11: the sets, 12-19: masks
 constexpr int kBothRank = 16;       // a part's columns: three parts in a box of 64
 constexpr int kBothStage = 32768 + 16384, kBothStages = 2;
 constexpr int kBothV = kBothRank * 256;
@@ -1155,20 +1151,21 @@ __global__ void __launch_bounds__(kBothThreads, 1) both_tc_kernel(const __grid_c
         if (b < step) drain(&st.full[b], (uint32_t)(((step - 1 - b) / 2) & 1));
       }
     __syncwarp();
-  } else if (warp == 2) {
-    // ---- base rows
-    int fetched[2] = {};
+  } else if (warp == 2 || warp == 3) {
+    // ---- base rows, a warp a set
+    const int set = warp - 2;
+    int n = 0;
     for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
       int4 ch;
       int c0;
       if (!unit_of(u, ch, c0)) continue;
-      int t[4];
-      lane_tokens(p.plan, ch.y, 4 * lane, ch.z, t);
       for (int r0 = 0; r0 < ch.z && ok; r0 += kTileRows, ++step) {
-        const int set = step & 1;
+        if ((step & 1) != set) continue;
+        int t[4];
+        lane_tokens(p.plan, ch.y, r0 + 4 * lane, ch.z, t);
         const RowCopy rows = row_copy(t, lane, false, true);
-        for (int s = 0; s < SLABS; ++s) {
-          const int n = (step >> 1) * SLABS + s, b = set * kBothSlabs + n % kBothSlabs, c = c0 + s * PER;
+        for (int s = 0; s < SLABS; ++s, ++n) {
+          const int b = set * kBothSlabs + n % kBothSlabs, c = c0 + s * PER;
           if (n >= kBothSlabs)
             ok = wait(&st.abort, &st.sempty[b], (uint32_t)((n / kBothSlabs - 1) & 1), p.plan.status, kRoleEmpty);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -1179,18 +1176,13 @@ __global__ void __launch_bounds__(kBothThreads, 1) both_tc_kernel(const __grid_c
             __syncwarp();
             copy_rows(rows, smem_u32(slabs + b * 16384), &p.mb, &p.mb_row, &st.sfull[b], c, t, lane);
           }
-          if (set) fetched[1] = n + 1;
-          else fetched[0] = n + 1;
         }
-        if (r0 + kTileRows < ch.z) lane_tokens(p.plan, ch.y, r0 + kTileRows + 4 * lane, ch.z, t);
       }
     }
     __syncwarp();
     if (lane == 0)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        for (int b = 0; b < kBothSlabs && b < fetched[h]; ++b)
-          drain(&st.sfull[h * kBothSlabs + b], (uint32_t)(((fetched[h] - 1 - b) / kBothSlabs) & 1));
+      for (int b = 0; b < kBothSlabs && b < n; ++b)
+        drain(&st.sfull[set * kBothSlabs + b], (uint32_t)(((n - 1 - b) / kBothSlabs) & 1));
     __syncwarp();
   } else if (warp == 1) {
     // ---- products
