@@ -16,8 +16,9 @@
 //
 // Rows of one tile may lie anywhere in the batch. Where 32 of them follow one
 // another (packed requests, one adapter) a TMA box fetches them at once,
-// elsewhere tile::gather4 four rows at a time, at half the rate (16384 x 6144 of
-// 32 adapters of rank 64: 131 us in boxes, 220 us with tokens in any order).
+// elsewhere tile::gather4 four rows at a time (16384 x 6144 of
+// 32 adapters of rank 64: 133 us in boxes, 141 us with tokens in any order; with
+// one warp a CTA issuing the gathers it was 191 us).
 #include "adapter.cuh"
 #include "tmap.cuh"
 
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
   int block = 0;   // blocks so far: block b is set b % 2's (b / 2)-th
 
   if (warp == 0 || warp == 3) {
-    // ---- base rows, a warp a set: gathers issue at half the rate from one
+    // ---- base rows, a warp a set: from one alone, gathers come too slowly
     const int set = warp == 0 ? 0 : 1;
     int n = 0;   // slabs so far
     for (int64_t at = begin; at < end && ok;) {
@@ -887,37 +888,39 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
   const int steps = (ch.z + 63) / 64;
 
   if (warp == 0) {
+    // 64 rows in two boxes of 64 columns: the lower half of the lanes fetches the
+    // first, the upper half the same rows of the second
+    const int r4 = 4 * (lane & 15), col = c0 + (lane >> 4) * 64;
     int t[4], pos[4];
-    lane_tokens(p.plan, ch.y, 4 * lane, lane < 16 ? ch.z : 0, t);
+    lane_tokens(p.plan, ch.y, r4, ch.z, t);
     int i = 0;
     for (; i < steps; ++i) {
       const int s = i % NST, r0 = i * 64;
       const bool full = r0 + 64 <= ch.z;
-      const RowCopy rows = row_copy(t, lane, true, lane < 16);   // rows past the chunk's end count as zeros
+      const RowCopy rows = row_copy(t, lane, true, true);   // rows past the chunk's end count as zeros
       bool ok = true;
       if (i >= NST) ok = wait(&st.abort, &st.empty[s], (uint32_t)((i / NST - 1) & 1), p.plan.status, kRoleEmpty);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (drops && lane < 16)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) st.tok[s][4 * lane + k] = t[k];
+        for (int k = 0; k < 4; ++k) st.tok[s][r4 + k] = t[k];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) pos[k] = r0 + 4 * lane + k < ch.z ? ch.y + r0 + 4 * lane + k : -1;
+      for (int k = 0; k < 4; ++k) pos[k] = r0 + r4 + k < ch.z ? ch.y + r0 + r4 + k : -1;
       __syncwarp();
       const uint32_t zs = smem_u32(smem + s * Z::kStage), ps = zs + 16384;
       if (lane == 0) {
         if (drops) mbar_arrive(smem_u32(&st.known[s]));
-        mbar_expect_tx(smem_u32(&st.full[s]), 2 * rows.bytes + 8192 * ATOMS);
+        mbar_expect_tx(smem_u32(&st.full[s]), rows.bytes + 8192 * ATOMS);
         if (full)
 #pragma unroll
           for (int b = 0; b < ATOMS; ++b) tma_load_2d(ps + b * 8192, &job.mp, smem_u32(&st.full[s]), b * 64, ch.y + r0);
       }
       __syncwarp();
-      copy_rows(rows, zs, &job.mz, &job.mz_row, &st.full[s], c0, t, lane);
-      copy_rows(rows, zs + 8192, &job.mz, &job.mz_row, &st.full[s], c0 + 64, t, lane);
+      copy_rows(rows, zs, &job.mz, &job.mz_row, &st.full[s], col, t, lane);
       if (lane < 16 && !full)
 #pragma unroll
         for (int b = 0; b < ATOMS; ++b) tma_gather4(ps + b * 8192 + lane * 512, &job.mp_row, &st.full[s], b * 64, pos);
-      if (i + 1 < steps) lane_tokens(p.plan, ch.y, r0 + 64 + 4 * lane, lane < 16 ? ch.z : 0, t);
+      if (i + 1 < steps) lane_tokens(p.plan, ch.y, r0 + 64 + r4, ch.z, t);
     }
     if (lane == 0)
       for (int s = 0; s < NST && s < i; ++s) drain(&st.full[s], (uint32_t)(((i - 1 - s) / NST) & 1));
