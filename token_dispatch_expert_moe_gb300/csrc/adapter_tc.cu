@@ -211,7 +211,13 @@ template <int RPMAX, bool WT, bool DROP, bool DEEP> struct ShrinkSize {
   static constexpr int kStages = RPMAX > 64 ? 3 : DEEP ? 4 : kCtas == 4 ? 2 : 3;
   static constexpr int kAcc = RPMAX <= 32 ? 4 : 2;
   static constexpr int kTmem = kAcc * RPMAX;
-  static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+  // No more CTAs an SM than TMEM has room for, of this and other shapes at once:
+  // one that waited for TMEM would keep its cluster waiting, whose other CTAs hold
+  // theirs. 128 columns go with a fifth of an SM's shared memory or more, 256 with
+  // more than two fifths, so that five, or more than four halves of 256, never fit.
+  static constexpr size_t kRing = (size_t)kStages * kStage + 1024, kShare = 228 * 1024 / 5;
+  static constexpr size_t kSmem = kRing > kShare ? kRing : kShare;
+  static_assert(kTmem <= 128 ? kTmem * 4 <= 512 : kTmem <= 256 && kSmem > 2 * kShare, "TMEM of the CTAs of an SM");
 };
 
 struct Shared {
