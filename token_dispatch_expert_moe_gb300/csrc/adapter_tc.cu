@@ -590,7 +590,8 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
     fence_proxy_async();
   }
   if (warp == 1) tmem_alloc(&st.tmem, 4 * kCols);
-  if (!p.late) pdl_wait();
+  // The map and the base rows are older than the predecessor; only the parts are
+  // its work.
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
@@ -648,6 +649,7 @@ __global__ void __launch_bounds__(expand_threads<DROP>(), 1) expand_tc_kernel(co
     __syncwarp();
   } else if (warp == 2) {
     // ---- parts and V
+    if (!p.late) pdl_wait();
     int pi = 0, vi = 0;
     for (int64_t at = begin; at < end && ok;) {
       int4 tile;

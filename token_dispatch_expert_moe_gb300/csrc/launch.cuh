@@ -9,18 +9,23 @@ namespace moe {
 // stream still runs. It reads nothing that the predecessor writes, and writes
 // nothing to memory, before pdl_wait() has returned (the predecessor has
 // completed and its writes are visible). Every thread of every CTA waits, so
-// that this kernel's end means the end of all before it; one that needs nothing of
-// its predecessor's at all may leave that to its last CTA, at the end. The norm, the balance
-// loss, the permutation and the gradients' kernels do not trigger their successor
-// early: measured, that gained nothing (norm of 16384 x 6144: 131 us with or
-// without, 133 us without this launch) and cost up to 1 us where the successor's
-// CTAs took the place of work. The adapters' kernels do (pdl_trigger): theirs are
-// chains of short kernels, each of which has microseconds to set up.
+// that this kernel's end means the end of all before it.
+// Within one operator a kernel may let only those threads wait that use the
+// predecessor's results, and its last CTA at the end, which keeps that meaning: if
+// the predecessor triggers after a wait of its own, or likewise knows that all
+// before it has completed, and neither writes what the other touches.
+// The norm, the balance loss, the permutation and the gradients' kernels do not
+// trigger their successor early: measured, that gained nothing (norm of 16384 x
+// 6144: 131 us with or without, 133 us without this launch) and cost up to 1 us
+// where the successor's CTAs took the place of work. The adapters' kernels do
+// (pdl_trigger): theirs are chains of short kernels, each of which has
+// microseconds to set up.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Lets the successor be brought up as soon as every CTA of this grid has come
-// here. Only after pdl_wait(): a successor that has been brought up knows that all
-// before this kernel has completed.
+// here. After pdl_wait() a successor that has been brought up knows that all before
+// this kernel has completed; one that could rely on that is launched only behind
+// kernels that trigger so, or that were themselves brought up so.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... KArgs, typename... Args>
