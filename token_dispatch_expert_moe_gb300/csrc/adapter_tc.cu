@@ -1389,13 +1389,13 @@ template <typename K> cudaError_t allow(K kernel, size_t smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
-// CTAs a tile: three an SM, as long as each has eight steps, or with dropout,
+// CTAs a tile: two an SM, as long as each has eight steps, or with dropout,
 // where the generator bounds them, six, so that the last wave weighs little
-// (16384 x 6144, rank 64: 142 us for the whole call against 158 us with six;
-// 32768 x 8192, rank 16, dropout: 346 us against 368 us with three); where tiles
-// are few, down to four steps.
+// (16384 x 6144, rank 64, packed: 138 us for the whole call against 142 us with
+// three and 158 us with six, tokens in any order 156 against 151 us; 32768 x 8192, rank 16, dropout: 346 us against 368 us with
+// three); where tiles are few, down to four steps.
 void set_split(const AdapterArgs &a, ShrinkTc &p) {
-  const int64_t tiles = host_tiles(a), all = (p.d + 63) / 64, sms = sm_count(), want = (p.threshold != 0 ? 6 : 3) * sms;
+  const int64_t tiles = host_tiles(a), all = (p.d + 63) / 64, sms = sm_count(), want = (p.threshold != 0 ? 6 : 2) * sms;
   p.split = 1;
   while (p.split < 8 && ((tiles * p.split < want && all / (p.split * 2) >= 8) ||
                          (tiles * p.split < sms && all / (p.split * 2) >= 4)))
@@ -1412,7 +1412,8 @@ cudaError_t shrink(const AdapterArgs &a, const ShrinkTc &p, cudaStream_t s) {
                              dim3(DROP ? 320 : 192), p.split, smem, s, p);
 }
 template <bool WT, bool DROP> cudaError_t shrink(const AdapterArgs &a, const ShrinkTc &p, cudaStream_t s) {
-  const bool deep = host_tiles(a) * p.split <= 2 * sm_count();
+  // the map's bound on the tiles is some above their number
+  const bool deep = host_tiles(a) * p.split * 4 <= 9 * sm_count();
   if (p.rp > 64) return shrink<128, WT, DROP, false>(a, p, s);
   if (deep) return p.rp <= 32 ? shrink<32, WT, DROP, true>(a, p, s) : shrink<64, WT, DROP, true>(a, p, s);
   return p.rp <= 32 ? shrink<32, WT, DROP, false>(a, p, s) : shrink<64, WT, DROP, false>(a, p, s);
