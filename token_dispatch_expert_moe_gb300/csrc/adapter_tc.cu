@@ -1392,8 +1392,9 @@ template <typename K> cudaError_t allow(K kernel, size_t smem) {
 // CTAs a tile: two an SM, as long as each has eight steps, or with dropout,
 // where the generator bounds them, six, so that the last wave weighs little
 // (16384 x 6144, rank 64, packed: 138 us for the whole call against 142 us with
-// three and 158 us with six, tokens in any order 156 against 151 us; 32768 x 8192, rank 16, dropout: 346 us against 368 us with
-// three); where tiles are few, down to four steps.
+// three and 158 us with six, tokens in any order 156 us against 151 us with three;
+// 32768 x 8192, rank 16, dropout: 346 us against 368 us with three); where tiles
+// are few, down to four steps.
 void set_split(const AdapterArgs &a, ShrinkTc &p) {
   const int64_t tiles = host_tiles(a), all = (p.d + 63) / 64, sms = sm_count(), want = (p.threshold != 0 ? 6 : 2) * sms;
   p.split = 1;
