@@ -374,9 +374,21 @@ def test_past_32_bits():
 @pytest.mark.parametrize("order", ["packed", "mixed", "one"])
 @pytest.mark.parametrize("rank", [8, 16])
 def test_long_batches_with_dropout(order, rank):
-    """From 8192 tokens on dA and a bf16 dx are made in one pass: chunks of several tiles, ragged ends, columns past the
-    last whole block, bare rows with and without a base and in place."""
-    T, d_in, d_out, n = 8705, 264, 72, 5
+    """Chunks of several tiles, ragged ends, columns past the last whole block, bare rows with and without a base and in
+    place."""
+    dropout_backwards(8705, 264, 72, order, rank)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("order", ["packed", "mixed", "one"])
+@pytest.mark.parametrize("T,d_in,rank", [(8705, 648, 16), (700, 3464, 8), (700, 3464, 16), (130, 9736, 16), (1, 9736, 8)])
+def test_one_pass_of_the_backward(T, d_in, order, rank):
+    """With dropout, ranks up to 16, a bf16 dx and enough blocks of columns dA and dx are made in one pass."""
+    dropout_backwards(T, d_in, 40, order, rank)
+
+
+def dropout_backwards(T, d_in, d_out, order, rank):
+    n = 5
     t = torch.arange(T)
     ids = {"packed": (t * 7 // T).clamp_max(5) - 1, "mixed": None, "one": torch.zeros(T)}[order]
     b = Batch(T, d_in, d_out, 1 if order == "one" else n, rank, BF16, 0.25, bare=0.3, ids=ids)

@@ -1037,12 +1037,12 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
 // ---------------------------------------------------------------------------
 // A's gradient and a bf16 dx in one pass, with dropout and ranks up to 16: the
 // two kernels above each make every mask, and the generator, not memory, bounds
-// both (32768 x 8192: 203 and 281 us for 79 and 158 us of bytes). Here one CTA an
+// both (32768 x 8192: 533 us together for 237 us of bytes). Here one CTA an
 // SM runs through units, 128 columns of a chunk, tile by tile of 128 tokens: x
 // and du's parts come in, mask warps take the dropped elements out of x and keep
 // a bit an element, dA += x^T du runs on from tile to tile, dx of the tile is du A
 // under the bits, onto its base rows. One tile of parts serves both products: as
-// rows of K for dA, as rows of M for dx. Together 334 us. At rank 32, or with an
+// rows of K for dA, as rows of M for dx: 297 us. At rank 32, or with an
 // fp32 dx, the larger stages and slabs leave too few of them and nothing is won.
 struct BothTc {
   CUtensorMap mx, mx_row, mp, mp_row, mv, mb, mb_row, mo;
@@ -1558,10 +1558,12 @@ cudaError_t launch_adapter_bwd_tc(const AdapterArgs &a, cudaStream_t s) {
   if (a.dA != nullptr) { sh.u_in = a.u_in; sh.parts_in = u; }
   cudaError_t e = shrink<true>(a, sh, a.dy, a.ld_out, a.B, s);
   // dA and dx in one pass where the generator would bound two, both tiles fit and
-  // units are long enough (rank 16: 4096 tokens 73 us against 71 us, 8192 x 6144
-  // of 8 adapters 134 us against 159 us, 32768 x 6144 368 us against 472 us)
+  // its units are half as many as the SMs or more (rank 16, one adapter: 1000 x
+  // 1024 29 us against 24 us, 4096 x 2048 45 us against 59 us, 32768 x 6144 388 us
+  // against 571 us; 8192 x 6144 of 8 adapters 137 us against 195 us)
+  const int64_t units = host_chunks(a) * ((a.d_in + kCols - 1) / kCols);
   const bool one_pass = a.threshold != 0 && a.dA != nullptr && a.dx != nullptr && a.dx_dtype == MOE_BF16 &&
-                        padded_rank(a.rank) == kBothRank && a.T >= 8192;
+                        padded_rank(a.rank) == kBothRank && units * 2 >= sm_count();
   if (e == cudaSuccess && one_pass) e = both(a, du, s);
   // The weight gradients need nothing of that pass, nor dx anything of them: each
   // starts where the one before leaves SMs free.
