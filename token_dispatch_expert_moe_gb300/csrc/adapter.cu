@@ -20,8 +20,8 @@ size_t adapter_map_bytes(int64_t T, int n) { return (size_t)map_layout(T, n).wor
 // L2, at 4 MB/us measured; by tiles there are a map and two more kernels (17 us
 // for the smallest batch) and half a microsecond a tile, of up to 128 tokens of
 // one adapter each: measured at 6144 and rank 16, 256 tokens of 64 adapters 28
-// us by rows and 53 us by tiles, 1021 x 3584 to 5120 of 12 adapters of rank 24
-// 81 us by rows and 30 us by tiles.
+// us by rows and 51 us by tiles, 1021 x 3584 to 5120 of 12 adapters of rank 24
+// 76 us by rows and 26 us by tiles.
 bool adapter_rowwise(int64_t T, int d_in, int d_out, int n, int rank, int dtype) {
   const double bytes = (double)T * rank * ((double)d_in + d_out) * (dtype == MOE_BF16 ? 2 : 4);
   const double tiles = (double)(T / kTileRows) + (double)(n < T ? n : T);
@@ -228,7 +228,7 @@ __device__ __forceinline__ void mask4(const Philox &g, int64_t i, float (&v)[4])
 // Row by row: a cluster of 8 CTAs a token. Every CTA takes a part of d_in for u,
 // the parts meet in shared memory, and every CTA takes a part of d_out for y, of
 // which the first factors are fetched before u is known. Bound by latency for few
-// tokens (6144, rank 16: one token 4.8 us, 64 tokens 8.3 us in a graph, of which
+// tokens (6144, rank 16: one token 4.8 us, 64 tokens 8.4 us in a graph, of which
 // the launch is 2), by L2 from some hundreds on. 64 registers, four CTAs an SM:
 // more values in flight a thread and fewer CTAs took 11 us for the 64 tokens.
 constexpr int kRowCtas = 8, kRowThreads = 256;

@@ -12,9 +12,10 @@ constexpr int kTileRows = 128;   // tokens of a tile, all of one adapter
 // Tokens of a chunk: the weight gradients are summed over a chunk's tokens in
 // one CTA, and over an adapter's chunks in a second pass. A sixteenth of the
 // batch gives that pass few partial sums and the first enough CTAs (32768 x 8192
-// with dropout: an eighth 573 us, a sixteenth 546 us, a thirty-second 575 us);
-// under 256 tokens a CTA's start weighs more than what it does (1000 x 2048,
-// rank 128: 53 us with 128, 46 us with 256, 49 us with 512).
+// with dropout: an eighth 508 us, a sixteenth 490 us, a thirty-second 505 us);
+// under 256 tokens a CTA's start weighs more than what it does (backward of 1000
+// x 2048, rank 128: 47 us with 128, 41 us with 256 or 512; 2048 x 4096, rank 16:
+// 42, 36 and 39 us).
 __host__ __device__ constexpr int64_t chunk_rows(int64_t T) {
   const int64_t e = (T / 16 + kTileRows - 1) / kTileRows * kTileRows;
   return e < 256 ? 256 : e;

@@ -17,8 +17,8 @@
 // Rows of one tile may lie anywhere in the batch. Where 32 of them follow one
 // another (packed requests, one adapter) a TMA box fetches them at once,
 // elsewhere tile::gather4 four rows at a time (16384 x 6144 of
-// 32 adapters of rank 64: 133 us in boxes, 141 us with tokens in any order; with
-// one warp a CTA issuing the gathers it was 191 us).
+// 32 adapters of rank 64, without the map: 129 us in boxes, 146 us with tokens in
+// any order; with one warp a CTA issuing expand's gathers it was 191 us).
 #include "adapter.cuh"
 #include "tmap.cuh"
 
@@ -530,9 +530,10 @@ __device__ __forceinline__ void slab_out(uint8_t *slab, int quarter, int lane, i
 // of four warps, which take the blocks in turn: a thread adds its row of the
 // accumulator to its row of the slab, and the slab leaves by TMA, or row by row
 // where the tile's rows do not follow one another. Each set has a ring of slabs
-// of its own, so that it sees every phase of the barriers it waits on. With dropout eight more
-// warps make the masks ahead, a bit an element: made by the sets themselves
-// they kept the slabs waiting (32768 x 8192, rank 16: 355 us).
+// of its own, so that it sees every phase of the barriers it waits on (16384 x
+// 6144, rank 64: 84 us, 4.8 TB/s; 32768 x 8192, rank 16: 180 us, 6.0 TB/s). With
+// dropout eight more warps make the masks ahead, a bit an element: made by the sets
+// themselves they kept the slabs waiting (32768 x 8192, rank 16: 355 us).
 struct ExpandTc {
   CUtensorMap mp, mv, mb, mb_row, mo;   // parts, V [n, d, rank] or [n, rank, d], base (32 rows; one), out (32 rows)
   Plan plan;
@@ -1393,7 +1394,7 @@ template <typename K> cudaError_t allow(K kernel, size_t smem) {
 // where the generator bounds them, six, so that the last wave weighs little
 // (16384 x 6144, rank 64, packed: 138 us for the whole call against 142 us with
 // three and 158 us with six, tokens in any order 156 us against 151 us with three;
-// 32768 x 8192, rank 16, dropout: 346 us against 368 us with three); where tiles
+// 32768 x 8192, rank 16, dropout: 340 us against 358 us with twelve); where tiles
 // are few, down to four steps.
 void set_split(const AdapterArgs &a, ShrinkTc &p) {
   const int64_t tiles = host_tiles(a), all = (p.d + 63) / 64, sms = sm_count(), want = (p.threshold != 0 ? 6 : 2) * sms;
