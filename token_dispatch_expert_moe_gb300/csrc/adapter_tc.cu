@@ -17,8 +17,8 @@
 // Rows of one tile may lie anywhere in the batch. Where 32 of them follow one
 // another (packed requests, one adapter) a TMA box fetches them at once,
 // elsewhere tile::gather4 four rows at a time (16384 x 6144 of
-// 32 adapters of rank 64, without the map: 129 us in boxes, 146 us with tokens in
-// any order; with one warp a CTA issuing expand's gathers it was 191 us).
+// 32 adapters of rank 64, without the map: 129 us in boxes, 137 us with tokens in
+// any order, by two warps a CTA; by one warp 191 us).
 #include "adapter.cuh"
 #include "tmap.cuh"
 
@@ -222,7 +222,7 @@ struct Shared {
   uint64_t full[kMaxRing], ready[kMaxRing], empty[kMaxRing], done;
   uint32_t tmem;
   volatile int abort;
-  int tok[kTileRows];
+  int tok[kTileRows], issued[2];   // steps of the producers
 };
 
 template <int RPMAX, bool WT, bool DROP, bool DEEP>
@@ -263,14 +263,15 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP, 
   const uint32_t tmem = st.tmem;
   const int k0 = q * p.per, all = (p.d + 63) / 64, steps = max(0, min(p.per, all - k0));
 
-  if (warp == 0) {
+  if (warp == 0 || (!DROP && warp == 2)) {
     int t[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) t[i] = st.tok[4 * lane + i];
     const RowCopy rows = row_copy(t, lane, false, true);
     const uint32_t bytes = rows.bytes + (WT ? 8192 * ((p.rp + 63) / 64) : p.rp * 128);
-    int i = 0;
-    for (; i < steps; ++i) {
+    // two warps take the steps in turn: gathers come too slowly from one
+    int i = warp >> 1;
+    for (; i < steps; i += DROP ? 1 : 2) {
       const int s = i % NST;
       bool ok = true;
       if (i >= NST) ok = wait(&st.abort, &st.empty[s], (uint32_t)((i / NST - 1) & 1), p.plan.status, kRoleEmpty);
@@ -288,8 +289,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP, 
       __syncwarp();
       copy_rows(rows, xs, &p.mx, &p.mx_row, &st.full[s], k, t, lane);
     }
-    if (lane == 0)
-      for (int s = 0; s < NST && s < i; ++s) drain(&st.full[s], (uint32_t)(((i - 1 - s) / NST) & 1));
+    if (lane == 0) st.issued[warp >> 1] = i;
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t idesc = instr_desc(128, p.rp, 0, WT ? 1 : 0);
@@ -346,6 +346,11 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP, 
   tc_fence_after();
   __syncthreads();
   const bool good = st.abort == 0;
+  if (!good && tid == 0) {   // what has been issued must land: no producer is a ring ahead of the products
+    const int end = DROP ? st.issued[0] : max(st.issued[0], st.issued[1]) - 1;
+    for (int j = max(0, end - NST); j < min(end, steps); ++j)
+      if (DROP || j < st.issued[j & 1]) drain(&st.full[j % NST], (uint32_t)((j / NST) & 1));
+  }
   const int ls = p.rp + 4;   // floats from row to row of the sums
   float *sums = reinterpret_cast<float *>(smem);
   if (warp >= 2 && warp < 6 && good) {
@@ -1393,7 +1398,7 @@ template <typename K> cudaError_t allow(K kernel, size_t smem) {
 // CTAs a tile: two an SM, as long as each has eight steps, or with dropout,
 // where the generator bounds them, six, so that the last wave weighs little
 // (16384 x 6144, rank 64, packed: 138 us for the whole call against 142 us with
-// three and 158 us with six, tokens in any order 156 us against 151 us with three;
+// three and 158 us with six, tokens in any order 148 us;
 // 32768 x 8192, rank 16, dropout: 340 us against 358 us with twelve); where tiles
 // are few, down to four steps.
 void set_split(const AdapterArgs &a, ShrinkTc &p) {
