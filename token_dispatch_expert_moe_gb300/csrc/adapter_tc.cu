@@ -58,6 +58,14 @@ __device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
   }
 }
 
+// The same for a ring that one producer, or two in turn, have filled up to their
+// `issued` steps: none of them is a ring ahead of the products.
+template <int NST, bool TWO> __device__ __forceinline__ void drain_ring(uint64_t *full, const int *issued, int steps) {
+  const int end = TWO ? max(issued[0], issued[1]) - 1 : issued[0];
+  for (int j = max(0, end - NST); j < min(end, steps); ++j)
+    if (!TWO || j < issued[j & 1]) drain(&full[j % NST], (uint32_t)((j / NST) & 1));
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *tm, uint64_t *bar, int c0, int c1, int c2) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -346,11 +354,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, ShrinkSize<RPMAX, WT, DROP, 
   tc_fence_after();
   __syncthreads();
   const bool good = st.abort == 0;
-  if (!good && tid == 0) {   // what has been issued must land: no producer is a ring ahead of the products
-    const int end = DROP ? st.issued[0] : max(st.issued[0], st.issued[1]) - 1;
-    for (int j = max(0, end - NST); j < min(end, steps); ++j)
-      if (DROP || j < st.issued[j & 1]) drain(&st.full[j % NST], (uint32_t)((j / NST) & 1));
-  }
+  if (!good && tid == 0) drain_ring<NST, !DROP>(st.full, st.issued, steps);
   const int ls = p.rp + 4;   // floats from row to row of the sums
   float *sums = reinterpret_cast<float *>(smem);
   if (warp >= 2 && warp < 6 && good) {
@@ -862,7 +866,7 @@ struct WgradShared {
   uint64_t full[kMaxRing], ready[kMaxRing], empty[kMaxRing], known[kMaxRing], done;   // known: a stage's tokens
   uint32_t tmem;
   volatile int abort;
-  int tok[kMaxRing][64];
+  int tok[kMaxRing][64], issued[2];   // steps of the producers
 };
 
 template <int ATOMS, bool DROP>
@@ -906,14 +910,16 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
   const uint32_t tmem = st.tmem;
   const int steps = (ch.z + 63) / 64;
 
-  if (warp == 0) {
+  if (warp == 0 || (!DROP && warp == 2)) {
     // 64 rows in two boxes of 64 columns: the lower half of the lanes fetches the
     // first, the upper half the same rows of the second
     const int r4 = 4 * (lane & 15), col = c0 + (lane >> 4) * 64;
     int t[4], pos[4];
-    lane_tokens(p.plan, ch.y, r4, ch.z, t);
-    int i = 0;
-    for (; i < steps; ++i) {
+    // two warps take the steps in turn, as in shrink
+    constexpr int TURN = DROP ? 1 : 2;
+    int i = warp >> 1;
+    lane_tokens(p.plan, ch.y, i * 64 + r4, ch.z, t);
+    for (; i < steps; i += TURN) {
       const int s = i % NST, r0 = i * 64;
       const bool full = r0 + 64 <= ch.z;
       const RowCopy rows = row_copy(t, lane, true, true);   // rows past the chunk's end count as zeros
@@ -939,10 +945,9 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
       if (lane < 16 && !full)
 #pragma unroll
         for (int b = 0; b < ATOMS; ++b) tma_gather4(ps + b * 8192 + lane * 512, &job.mp_row, &st.full[s], b * 64, pos);
-      if (i + 1 < steps) lane_tokens(p.plan, ch.y, r0 + 64 + r4, ch.z, t);
+      if (i + TURN < steps) lane_tokens(p.plan, ch.y, r0 + 64 * TURN + r4, ch.z, t);
     }
-    if (lane == 0)
-      for (int s = 0; s < NST && s < i; ++s) drain(&st.full[s], (uint32_t)(((i - 1 - s) / NST) & 1));
+    if (lane == 0) st.issued[warp >> 1] = i;
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t idesc = instr_desc(128, ATOMS == 1 ? 48 : p.rp, 1, 1);
@@ -1001,6 +1006,7 @@ __global__ void __launch_bounds__(DROP ? 320 : 192, WgradSize<ATOMS, DROP>::kCta
   if (!wait(&st.abort, &st.done, 0, p.plan.status, kRoleDone)) st.abort = 1;
   tc_fence_after();
   __syncthreads();
+  if (st.abort != 0 && tid == 0) drain_ring<NST, !DROP>(st.full, st.issued, steps);
   if (warp >= 2 && warp < 6 && st.abort == 0) {
     const float f = job.factor * (job.scale != nullptr ? job.scale[ch.x] : 1.0f);
     float *out = ch.w < 0 ? job.out + (int64_t)ch.x * p.rank * job.d : job.partial + (int64_t)ch.w * p.rank * job.d;
