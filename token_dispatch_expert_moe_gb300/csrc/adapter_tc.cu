@@ -189,8 +189,9 @@ __device__ __forceinline__ void copy_rows(const RowCopy &r, uint32_t dst, const 
 // of the rows, adding in the CTAs' order. Warp 0 fetches, warp 1 issues the
 // products, the others take the accumulators, and before that, with dropout,
 // the dropped elements out of each stage.
-// The steps of K take turns over several accumulators, which are added at the
-// end: the tensor core truncates each addition, and a short chain loses less.
+// The steps of K take turns over several accumulators, as many as TMEM holds, which
+// are added at the end: the tensor core truncates each addition, and a short chain
+// loses less.
 struct ShrinkTc {
   CUtensorMap mx, mx_row, mw;   // x in boxes of 32 rows and of one; W [n, rank, d] or [n, d, rank]
   Plan plan;
@@ -206,6 +207,7 @@ struct ShrinkTc {
   bf16 *parts_in;
 };
 
+constexpr int accumulators(int rp, bool deep) { return rp <= 32 || (rp <= 64 && deep) ? 4 : 2; }
 template <int RPMAX, bool WT, bool DROP, bool DEEP> struct ShrinkSize {
   static constexpr int kW = WT ? 8192 * ((RPMAX + 63) / 64) : RPMAX * 128;
   static constexpr int kStage = 16384 + kW;
@@ -215,7 +217,7 @@ template <int RPMAX, bool WT, bool DROP, bool DEEP> struct ShrinkSize {
   // SM anyway (DEEP), longer rings.
   static constexpr int kCtas = RPMAX > 64 || DEEP ? 2 : DROP ? 3 : 4;
   static constexpr int kStages = RPMAX > 64 ? 3 : DEEP ? 4 : kCtas == 4 ? 2 : 3;
-  static constexpr int kAcc = RPMAX <= 32 ? 4 : 2;
+  static constexpr int kAcc = accumulators(RPMAX, DEEP);
   static constexpr int kTmem = kAcc * RPMAX;
   // No more CTAs an SM than TMEM has room for, of this and other shapes at once:
   // one that waited for TMEM would keep its cluster waiting, whose other CTAs hold
@@ -1401,17 +1403,23 @@ template <typename K> cudaError_t allow(K kernel, size_t smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
+// Whether there are not more than two CTAs an SM; the map's bound on the tiles is
+// some above their number.
+bool deep(const AdapterArgs &a, int split) { return host_tiles(a) * split * 4 <= 9 * sm_count(); }
+
 // CTAs a tile: two an SM, as long as each has eight steps, or with dropout,
 // where the generator bounds them, six, so that the last wave weighs little
-// (16384 x 6144, rank 64, packed: 138 us for the whole call against 142 us with
-// three and 158 us with six, tokens in any order 148 us;
-// 32768 x 8192, rank 16, dropout: 340 us against 358 us with twelve); where tiles
-// are few, down to four steps.
+// (16384 x 6144, rank 64, packed: 139 us for the whole call against 142 us with
+// three and 158 us with six; 32768 x 8192, rank 16, dropout: 340 us against 358 us
+// with twelve); where tiles are few, down to four steps. No accumulator takes more
+// than 16 steps, as far as eight CTAs go: each step costs 6e-8 of u (a sum in
+// elementary order has 1.7e-7).
 void set_split(const AdapterArgs &a, ShrinkTc &p) {
   const int64_t tiles = host_tiles(a), all = (p.d + 63) / 64, sms = sm_count(), want = (p.threshold != 0 ? 6 : 2) * sms;
   p.split = 1;
   while (p.split < 8 && ((tiles * p.split < want && all / (p.split * 2) >= 8) ||
-                         (tiles * p.split < sms && all / (p.split * 2) >= 4)))
+                         (tiles * p.split < sms && all / (p.split * 2) >= 4) ||
+                         all > 16 * p.split * accumulators(p.rp, deep(a, p.split))))
     p.split *= 2;
   p.per = (int)((all + p.split - 1) / p.split);
 }
@@ -1425,10 +1433,8 @@ cudaError_t shrink(const AdapterArgs &a, const ShrinkTc &p, cudaStream_t s) {
                              dim3(DROP ? 320 : 192), p.split, smem, s, p);
 }
 template <bool WT, bool DROP> cudaError_t shrink(const AdapterArgs &a, const ShrinkTc &p, cudaStream_t s) {
-  // the map's bound on the tiles is some above their number
-  const bool deep = host_tiles(a) * p.split * 4 <= 9 * sm_count();
   if (p.rp > 64) return shrink<128, WT, DROP, false>(a, p, s);
-  if (deep) return p.rp <= 32 ? shrink<32, WT, DROP, true>(a, p, s) : shrink<64, WT, DROP, true>(a, p, s);
+  if (deep(a, p.split)) return p.rp <= 32 ? shrink<32, WT, DROP, true>(a, p, s) : shrink<64, WT, DROP, true>(a, p, s);
   return p.rp <= 32 ? shrink<32, WT, DROP, false>(a, p, s) : shrink<64, WT, DROP, false>(a, p, s);
 }
 // x [T, d] rows ld apart; W [n, rank, d], or [n, d, rank] (WT)
