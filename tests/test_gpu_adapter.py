@@ -380,6 +380,30 @@ def test_long_batches_with_dropout(order, rank):
 
 
 @pytest.mark.gpu
+def test_ranks_side_by_side():
+    """Calls of three shapes on three streams at once, whose CTAs share SMs and their tensor memory, each call right behind
+    the one before on the same workspace: the same bits as alone."""
+    batches = [Batch(4200, 2048, 1536, 5, 128, BF16), Batch(4100, 4096, 1032, 3, 16, BF16, 0.25),
+               Batch(6000, 1544, 2048, 9, 40, BF16)]
+    want = [(b.forward(), b.backward(BF16)) for b in batches]
+    outs = [(b.new(b.T, b.shape.d_out, dt=BF16), b.new(b.T, b.shape.rank), {k: torch.zeros_like(v) for k, v in w[1].items()})
+            for b, w in zip(batches, want)]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for b, (y, u, back), s in zip(batches, outs, streams):
+            with torch.cuda.stream(s):
+                rng = b.rng if b.p else None
+                b.L.moe_adapter(b.shape, b.x, b.A, b.B, b.scale, None, b.map, rng, b.base, y, u, b.ws)
+                b.L.moe_adapter_bwd(b.shape, b.L.MOE_BF16, b.dy, b.x, b.A, b.B, b.scale, b.map, rng, b.u, None, back["dx"],
+                                    back["dA"], back["dB"], b.ws)
+    torch.cuda.synchronize()
+    for b, (y, u, back), ((wy, wu), w) in zip(batches, outs, want):
+        assert b.status() == 0 and torch.equal(y, wy) and torch.equal(u, wu)
+        assert all(torch.equal(back[k], w[k]) for k in w)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("order", ["packed", "mixed", "one"])
 @pytest.mark.parametrize("T,d_in,rank", [(8705, 648, 16), (700, 3464, 8), (700, 3464, 16), (130, 9736, 16), (1, 9736, 8)])
 def test_one_pass_of_the_backward(T, d_in, order, rank):
